@@ -12,6 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoestep.so")
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 
 ERR_SLOT_RANGE = 1 << 0
 ERR_EXPERT_NONLOCAL = 1 << 1
@@ -57,11 +58,59 @@ class CombineArgs(C.Structure):
                 ("rel_count", _p), ("err", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t)]
 
 
-_STRUCTS = [AssembleArgs, PackArgs, FfnArgs, StateC, CombineArgs]
+class RouteArgs(C.Structure):
+    _fields_ = [("T", _i32), ("E", _i32), ("K", _i32), ("logits", _p), ("dtype", _i32), ("pitch", _i64), ("bias", _p),
+                ("score", _i32), ("renorm", _i32), ("scale", C.c_float), ("expert", _p), ("w", _p)]
+
+
+class RouteBackwardArgs(C.Structure):
+    _fields_ = [("T", _i32), ("E", _i32), ("K", _i32), ("logits", _p), ("dtype", _i32), ("pitch", _i64),
+                ("expert", _p), ("dw", _p), ("score", _i32), ("renorm", _i32), ("scale", C.c_float), ("dlogits", _p),
+                ("dlogits_pitch", _i64), ("err", _p)]
+
+
+class SortRowsArgs(C.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("H", _i32), ("expert_base", _i32), ("E_loc", _i32), ("expert", _p),
+                ("x", _p), ("x_dtype", _i32), ("x_pitch", _i64), ("x_scale", _p), ("group", _i32), ("xs", _p),
+                ("xs_pitch", _i64), ("perm", _p), ("pos", _p), ("counts", _p), ("offsets", _p), ("row_slot", _p),
+                ("err", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t)]
+
+
+class MergeRowsArgs(C.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("H", _i32), ("rows", _p), ("row_dtype", _i32), ("row_pitch", _i64),
+                ("n_rows", _i64), ("pos", _p), ("w", _p), ("out", _p), ("out_dtype", _i32), ("out_pitch", _i64),
+                ("err", _p)]
+
+
+class MergeRowsBackwardArgs(C.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("H", _i32), ("dout", _p), ("dout_dtype", _i32), ("dout_pitch", _i64),
+                ("rows", _p), ("row_dtype", _i32), ("row_pitch", _i64), ("n_rows", _i64), ("pos", _p), ("w", _p),
+                ("drows", _p), ("drows_pitch", _i64), ("dw", _p), ("err", _p)]
+
+
+class ResidualNormArgs(C.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("x", _p), ("x_dtype", _i32), ("x_pitch", _i64), ("residual", _p),
+                ("res_dtype", _i32), ("res_pitch", _i64), ("gamma", _p), ("gamma_dtype", _i32), ("eps", C.c_float),
+                ("out", _p), ("out_dtype", _i32), ("out_pitch", _i64), ("out_scale", _p), ("group", _i32),
+                ("residual_out", _p), ("res_out_pitch", _i64), ("rstd", _p), ("row_list", _p), ("row_count", _p),
+                ("err", _p)]
+
+
+class ResidualNormBackwardArgs(C.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("dout", _p), ("dtype", _i32), ("dout_pitch", _i64), ("h", _p),
+                ("h_dtype", _i32), ("h_pitch", _i64), ("gamma", _p), ("gamma_dtype", _i32), ("rstd", _p),
+                ("dres", _p), ("dres_pitch", _i64), ("dx", _p), ("dx_pitch", _i64), ("dresidual", _p),
+                ("dresidual_pitch", _i64), ("dgamma", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t)]
+
+
+_STRUCTS = [AssembleArgs, PackArgs, FfnArgs, StateC, CombineArgs, RouteArgs, RouteBackwardArgs, SortRowsArgs,
+            MergeRowsArgs, MergeRowsBackwardArgs, ResidualNormArgs, ResidualNormBackwardArgs]
 EXPORTS = ["moe_assemble", "moe_pack_ffn_weights", "moe_ffn_workspace_size", "moe_expert_ffn_grouped",
            "moe_state_reset", "moe_combine_release", "moe_combine_plan", "moe_combine_apply",
            "moe_combine_workspace_size", "moe_strerror", "moe_version", "moe_struct_size",
-           "moe_combine_release_noalloc", "moe_combine_noalloc_max_arrivals"]
+           "moe_combine_release_noalloc", "moe_combine_noalloc_max_arrivals", "moe_route", "moe_route_backward",
+           "moe_sort_rows", "moe_sort_rows_workspace_size", "moe_merge_rows", "moe_merge_rows_backward",
+           "moe_residual_norm", "moe_residual_norm_backward", "moe_residual_norm_backward_workspace_size"]
 
 
 class MoeError(RuntimeError):
@@ -88,6 +137,13 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                        ("moe_combine_plan", [C.POINTER(CombineArgs), _p]),
                        ("moe_combine_apply", [C.POINTER(CombineArgs), _p]),
                        ("moe_combine_release_noalloc", [C.POINTER(CombineArgs), _p]),
+                       ("moe_route", [C.POINTER(RouteArgs), _p]),
+                       ("moe_route_backward", [C.POINTER(RouteBackwardArgs), _p]),
+                       ("moe_sort_rows", [C.POINTER(SortRowsArgs), _p]),
+                       ("moe_merge_rows", [C.POINTER(MergeRowsArgs), _p]),
+                       ("moe_merge_rows_backward", [C.POINTER(MergeRowsBackwardArgs), _p]),
+                       ("moe_residual_norm", [C.POINTER(ResidualNormArgs), _p]),
+                       ("moe_residual_norm_backward", [C.POINTER(ResidualNormBackwardArgs), _p]),
                        ("moe_version", []), ("moe_strerror", [C.c_int])]:
         f = getattr(lib, name)
         f.argtypes = args
@@ -99,6 +155,9 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.moe_combine_workspace_size.restype = C.c_size_t
     lib.moe_combine_noalloc_max_arrivals.argtypes = []
     lib.moe_combine_noalloc_max_arrivals.restype = C.c_size_t
+    for name in ("moe_sort_rows_workspace_size", "moe_residual_norm_backward_workspace_size"):
+        getattr(lib, name).argtypes = [_i32]
+        getattr(lib, name).restype = C.c_size_t
     lib.moe_struct_size.argtypes = [C.c_int]
     lib.moe_struct_size.restype = C.c_size_t
     for k, s in enumerate(_STRUCTS):
@@ -261,3 +320,301 @@ def combine_call(a: CombineArgs, part: str = "release", stream=None) -> None:
     fn = {"release": "moe_combine_release", "plan": "moe_combine_plan", "apply": "moe_combine_apply",
           "noalloc": "moe_combine_release_noalloc"}[part]
     _check(getattr(load(), fn)(C.byref(a), _stream(stream)), fn)
+
+
+# ------------------------------------------------------------------ the home rank's side
+# These calls check their tensors (device, type, shape, stride) before marshalling: a view that
+# the kernels cannot address is refused with a MoeError, and a tensor on another device than the
+# current one is worked on where it is.
+
+_ROWS = (torch.float32, torch.bfloat16)
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+_INT = (torch.int32,)
+_FLT = (torch.float32,)
+_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4M3,
+         torch.float8_e4m3fn: MOE_FP8_E4M3}
+
+
+def _mat(what: str, t, rows: int, cols: int, types) -> int:
+    """A [rows][cols] device tensor of one of `types` whose rows are contiguous; its pitch."""
+    if t.dtype not in types:
+        raise MoeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise MoeError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise MoeError(f"{what}: the elements of a row must be contiguous")
+    if rows <= 1:
+        return cols
+    if s0 < cols:
+        raise MoeError(f"{what}: rows overlap (stride {s0} for {cols} elements)")
+    return s0
+
+
+def _shape(what: str, t) -> tuple[int, int]:
+    if t.dim() != 2:
+        raise MoeError(f"{what}: {t.dim()} dimensions, 2 expected")
+    return t.shape
+
+
+def _int32(name: str, *values) -> None:
+    """Sizes that the argument struct holds in 32 bits (ctypes would cut them silently)."""
+    for v in values:
+        if not -(1 << 31) <= v < 1 << 31:
+            raise MoeError(f"{name}: a size of {v} is over the documented limits")
+
+
+def _room(workspace) -> int:
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise MoeError("workspace: must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
+def _vec(what: str, t, n: int, types) -> None:
+    """A contiguous device tensor of one of `types` with at least n elements."""
+    if t.dtype not in types:
+        raise MoeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.numel() < n:
+        raise MoeError(f"{what}: {t.numel()} elements, at least {n} expected")
+    if not t.is_contiguous():
+        raise MoeError(f"{what}: must be contiguous")
+
+
+def _home_call(name: str, args, tensors, stream) -> None:
+    """One call of the library on the device that its tensors are on.  With a stream other than
+    the current one, the tensors are recorded on it, so that the allocator keeps them until the
+    call's work is done."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise MoeError(f"{name}: tensors must be on a GPU, got {dev}")
+        elif t.device != dev:
+            raise MoeError(f"{name}: tensors on {dev} and {t.device}")
+    current = torch.cuda.current_stream(dev).cuda_stream
+    handle = current if stream is None else _stream(stream)
+    if stream is not None and getattr(stream, "device", dev) != dev:
+        raise MoeError(f"{name}: a stream of {stream.device} for tensors on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(getattr(_lib or load(), name)(C.byref(args), handle), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(_lib or load(), name)(C.byref(args), handle), name)
+    if handle != current:
+        s = stream
+        if not hasattr(stream, "cuda_stream"):
+            s = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _score(score, renorm) -> tuple[int, int]:
+    if score not in (MOE_SOFTMAX, MOE_SIGMOID):
+        raise MoeError(f"score must be MOE_SOFTMAX or MOE_SIGMOID, got {score!r}")
+    return score, 1 if renorm else 0
+
+
+def moe_route(logits, expert, w, bias=None, score: int = MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
+              stream=None) -> None:
+    """logits [T][E] (f32 or bf16); out: expert [T][K] int32, w [T][K] f32."""
+    (T, E), K = _shape("logits", logits), _shape("expert", expert)[1]
+    _int32("moe_route", T, E, K)
+    pitch = _mat("logits", logits, T, E, _ROWS)
+    _mat("expert", expert, T, K, _INT)
+    _mat("w", w, T, K, _FLT)
+    _vec("expert", expert, T * K, _INT)
+    _vec("w", w, T * K, _FLT)
+    if bias is not None:
+        _vec("bias", bias, E, _FLT)
+    score, renorm = _score(score, renorm)
+    a = RouteArgs(T, E, K, _ptr(logits), _CODE[logits.dtype], pitch, _ptr(bias), score, renorm, scale, _ptr(expert),
+                  _ptr(w))
+    _home_call("moe_route", a, (logits, expert, w, bias), stream)
+
+
+def moe_route_backward(logits, expert, dw, dlogits, err, score: int = MOE_SOFTMAX, renorm: bool = True,
+                       scale: float = 1.0, stream=None) -> None:
+    """expert [T][K] as moe_route gave it, dw [T][K] f32; out: dlogits [T][E] of the logits' type."""
+    (T, E), K = _shape("logits", logits), _shape("expert", expert)[1]
+    _int32("moe_route_backward", T, E, K)
+    pitch = _mat("logits", logits, T, E, _ROWS)
+    _mat("expert", expert, T, K, _INT)
+    _mat("dw", dw, T, K, _FLT)
+    _vec("expert", expert, T * K, _INT)
+    _vec("dw", dw, T * K, _FLT)
+    dpitch = _mat("dlogits", dlogits, T, E, (logits.dtype,))
+    _vec("err", err, 1, _INT)
+    score, renorm = _score(score, renorm)
+    a = RouteBackwardArgs(T, E, K, _ptr(logits), _CODE[logits.dtype], pitch, _ptr(expert), _ptr(dw), score, renorm,
+                          scale, _ptr(dlogits), dpitch, _ptr(err))
+    _home_call("moe_route_backward", a, (logits, expert, dw, dlogits, err), stream)
+
+
+def moe_sort_rows_workspace_size(n_max: int) -> int:
+    return load().moe_sort_rows_workspace_size(n_max)
+
+
+def _groups(H: int, group: int) -> int:
+    if group not in (0, 32, 64, 128):
+        raise MoeError(f"group must be 0, 32, 64 or 128, got {group}")
+    return (H + group - 1) // group if group else 1
+
+
+def moe_sort_rows(expert, E_loc: int, x, xs, perm, pos, counts, offsets, err, workspace, expert_base: int = 0,
+                  row_slot=None, x_scale=None, group: int = 0, stream=None) -> None:
+    """expert [T][K] int32; x [T][H] (f32, bf16, or fp8 with x_scale [T][groups] f32), xs [T * K][H]
+    of x's type (bf16 for fp8); xs None: the index alone (x may be None then).  perm and row_slot
+    are optional."""
+    T, K = _shape("expert", expert)
+    n = T * K
+    _vec("expert", expert, n, _INT)
+    H, code, xp, xsp = 8, MOE_BF16, 8, 8
+    if xs is not None:
+        if x is None:
+            raise MoeError("x: required with xs")
+        H = _shape("xs", xs)[1]
+        xp = _mat("x", x, T, H, _ROWS + _FP8)
+        code = _CODE[x.dtype]
+        xsp = _mat("xs", xs, n, H, (torch.bfloat16,) if code == MOE_FP8_E4M3 else (x.dtype,))
+        if code == MOE_FP8_E4M3:
+            if x_scale is None:
+                raise MoeError("x_scale: required for fp8 rows")
+            _vec("x_scale", x_scale, T * _groups(H, group), _FLT)
+    else:
+        x = x_scale = None
+    for what, t, m in (("perm", perm, n), ("row_slot", row_slot, n)):
+        if t is not None:
+            _vec(what, t, m, _INT)
+    _int32("moe_sort_rows", T, K, H, n, E_loc, expert_base)
+    _vec("pos", pos, n, _INT)
+    _vec("counts", counts, E_loc, _INT)
+    _vec("offsets", offsets, E_loc + 1, _INT)
+    _vec("err", err, 1, _INT)
+    a = SortRowsArgs(T, K, H, expert_base, E_loc, _ptr(expert), _ptr(x), code, xp, _ptr(x_scale), group, _ptr(xs),
+                     xsp, _ptr(perm), _ptr(pos), _ptr(counts), _ptr(offsets), _ptr(row_slot), _ptr(err),
+                     _ptr(workspace), _room(workspace))
+    _home_call("moe_sort_rows", a, (expert, x, xs, perm, pos, counts, offsets, err, workspace, row_slot, x_scale),
+               stream)
+
+
+def _positions(pos, w, T: int) -> int:
+    """pos: int32, T x K elements in token order ([T][K] or flat); K."""
+    K = pos.numel() // T if T else (pos.shape[-1] if pos.dim() > 1 else 1)
+    if pos.numel() != T * K:
+        raise MoeError(f"pos: {pos.numel()} elements are not a whole number for each of {T} tokens")
+    _vec("pos", pos, T * K, _INT)
+    if w is not None:
+        _vec("w", w, T * K, _FLT)
+        if w.numel() != T * K:
+            raise MoeError(f"w: {w.numel()} elements, {T * K} expected")
+    return K
+
+
+def moe_merge_rows(rows, pos, w, out, err, stream=None) -> None:
+    """rows [n_rows][H]; pos (int32) and w (f32, or None: 1) [T][K]; out [T][H].  f32 or bf16 each.
+    With the gradient of moe_sort_rows' xs as rows and w None, out is the gradient of its x."""
+    T, H = _shape("out", out)
+    K = _positions(pos, w, T)
+    _int32("moe_merge_rows", T, H, K)
+    n_rows = _shape("rows", rows)[0]
+    rp = _mat("rows", rows, n_rows, H, _ROWS)
+    op = _mat("out", out, T, H, _ROWS)
+    _vec("err", err, 1, _INT)
+    a = MergeRowsArgs(T, K, H, _ptr(rows), _CODE[rows.dtype], rp, n_rows, _ptr(pos), _ptr(w), _ptr(out),
+                      _CODE[out.dtype], op, _ptr(err))
+    _home_call("moe_merge_rows", a, (rows, pos, w, out, err), stream)
+
+
+def moe_merge_rows_backward(dout, rows, pos, w, drows, dw, err, stream=None) -> None:
+    """dout [T][H]; rows and drows [n_rows][H] of one type; pos, w and dw [T][K].  drows or dw (and
+    then rows) may be None."""
+    T, H = _shape("dout", dout)
+    K = _positions(pos, w, T)
+    _int32("moe_merge_rows_backward", T, H, K)
+    dp = _mat("dout", dout, T, H, _ROWS)
+    one = rows if rows is not None else drows
+    if one is None or (drows is None and dw is None) or (dw is not None and rows is None):
+        raise MoeError("moe_merge_rows_backward: drows, or dw with rows, must be given")
+    n_rows, rp, drp = _shape("rows", one)[0], H, H
+    if rows is not None:
+        rp = _mat("rows", rows, n_rows, H, _ROWS)
+    if drows is not None:
+        drp = _mat("drows", drows, n_rows, H, (one.dtype,) if one.dtype in _ROWS else _ROWS)
+    if dw is not None:
+        _vec("dw", dw, T * K, _FLT)
+    _vec("err", err, 1, _INT)
+    a = MergeRowsBackwardArgs(T, K, H, _ptr(dout), _CODE[dout.dtype], dp, _ptr(rows), _CODE[one.dtype], rp, n_rows,
+                              _ptr(pos), _ptr(w), _ptr(drows), drp, _ptr(dw), _ptr(err))
+    _home_call("moe_merge_rows_backward", a, (dout, rows, pos, w, drows, dw, err), stream)
+
+
+def moe_residual_norm(x, residual, gamma, eps: float, out, residual_out=None, rstd=None, out_scale=None,
+                      group: int = 0, row_list=None, row_count=None, err=None, stream=None) -> None:
+    """x, residual (optional) [T][H]; gamma [H]; out [T][H] f32, bf16 or fp8 (then out_scale [T][groups]
+    f32).  Optional outputs: residual_out [T][H], rstd [T].  row_list [T], row_count [1] (int32): only
+    these rows, with err."""
+    T, H = _shape("x", x)
+    _int32("moe_residual_norm", T, H)
+    xp = _mat("x", x, T, H, _ROWS)
+    op = _mat("out", out, T, H, _ROWS + _FP8)
+    _vec("gamma", gamma, H, _ROWS)
+    rt, rp, rop = x.dtype, H, H
+    if residual is not None:
+        rt = residual.dtype
+        rp = _mat("residual", residual, T, H, _ROWS)
+    if residual_out is not None:
+        if residual is None:
+            rt = residual_out.dtype
+        rop = _mat("residual_out", residual_out, T, H, (rt,) if rt in _ROWS else _ROWS)
+    if _CODE[out.dtype] == MOE_FP8_E4M3:
+        if out_scale is None:
+            raise MoeError("out_scale: required for fp8 output")
+        _vec("out_scale", out_scale, T * _groups(H, group), _FLT)
+    else:
+        out_scale = None
+    if rstd is not None:
+        _vec("rstd", rstd, T, _FLT)
+    if row_list is not None:
+        _vec("row_list", row_list, T, _INT)
+    for what, t in (("row_count", row_count), ("err", err)):
+        if t is not None:
+            _vec(what, t, 1, _INT)
+    a = ResidualNormArgs(T, H, _ptr(x), _CODE[x.dtype], xp, _ptr(residual), _CODE[rt], rp, _ptr(gamma),
+                         _CODE[gamma.dtype], eps, _ptr(out), _CODE[out.dtype], op, _ptr(out_scale), group,
+                         _ptr(residual_out), rop, _ptr(rstd), _ptr(row_list), _ptr(row_count), _ptr(err))
+    _home_call("moe_residual_norm", a, (x, residual, gamma, out, residual_out, rstd, out_scale, row_list, row_count,
+                                        err), stream)
+
+
+def moe_residual_norm_backward_workspace_size(H: int) -> int:
+    return load().moe_residual_norm_backward_workspace_size(H)
+
+
+def moe_residual_norm_backward(dout, h, gamma, rstd, dx, dgamma, workspace, dres=None, dresidual=None,
+                               stream=None) -> None:
+    """dout [T][H], h [T][H] (the forward's residual_out, or x), rstd [T]; out: dx [T][H] of dout's type,
+    dresidual [T][H] of h's, dgamma [H] f32 (with the workspace); each may be None.  dres [T][H] of h's
+    type is added to dx and dresidual."""
+    T, H = _shape("dout", dout)
+    _int32("moe_residual_norm_backward", T, H)
+    dp = _mat("dout", dout, T, H, _ROWS)
+    hp = _mat("h", h, T, H, _ROWS)
+    _vec("gamma", gamma, H, _ROWS)
+    _vec("rstd", rstd, T, _FLT)
+    p = {"dres": H, "dx": H, "dresidual": H}
+    for what, t, like in (("dres", dres, h), ("dx", dx, dout), ("dresidual", dresidual, h)):
+        if t is not None:
+            p[what] = _mat(what, t, T, H, (like.dtype,))
+    if dgamma is not None:
+        _vec("dgamma", dgamma, H, _FLT)
+    a = ResidualNormBackwardArgs(T, H, _ptr(dout), _CODE[dout.dtype], dp, _ptr(h), _CODE[h.dtype], hp, _ptr(gamma),
+                                 _CODE[gamma.dtype], _ptr(rstd), _ptr(dres), p["dres"], _ptr(dx), p["dx"],
+                                 _ptr(dresidual), p["dresidual"], _ptr(dgamma), _ptr(workspace),
+                                 _room(workspace))
+    _home_call("moe_residual_norm_backward", a, (dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual), stream)

@@ -25,6 +25,13 @@ extern "C" size_t moe_struct_size(int which) {
     case 2: return sizeof(moe_ffn_args);
     case 3: return sizeof(moe_combine_state);
     case 4: return sizeof(moe_combine_args);
+    case 5: return sizeof(moe_route_args);
+    case 6: return sizeof(moe_route_backward_args);
+    case 7: return sizeof(moe_sort_rows_args);
+    case 8: return sizeof(moe_merge_rows_args);
+    case 9: return sizeof(moe_merge_rows_backward_args);
+    case 10: return sizeof(moe_residual_norm_args);
+    case 11: return sizeof(moe_residual_norm_backward_args);
     default: return 0;
   }
 }

@@ -1,0 +1,160 @@
+// Device helpers of the home rank's operators (route.hip, rows.hip, norm.hip): eight elements of
+// a row as fp32 in registers, sums and maxima over lanes, and launches that report their own error.
+#pragma once
+
+#include "common.hpp"
+
+namespace moe {
+
+// A row is handled in chunks of eight elements: 16 bytes of bf16, two 16-byte runs of fp32, 8
+// bytes of fp8.  ld8 / st8 take the element offset of the chunk from the row's start.
+template <int DT>
+struct Chunk;
+
+template <>
+struct Chunk<MOE_BF16> {
+  u32x4 r;
+  __device__ __forceinline__ void load(const void* row, int64_t at) {
+    r = *reinterpret_cast<const u32x4*>((const uint16_t*)row + at);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(r[k] << 16);
+      f[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
+    }
+  }
+};
+
+template <>
+struct Chunk<MOE_F32> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const void* row, int64_t at) {
+    a = *reinterpret_cast<const f32x4*>((const float*)row + at);
+    b = *reinterpret_cast<const f32x4*>((const float*)row + at + 4);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[k] = a[k];
+      f[4 + k] = b[k];
+    }
+  }
+};
+
+template <>
+struct Chunk<MOE_FP8_E4M3> {
+  uint2 r;
+  __device__ __forceinline__ void load(const void* row, int64_t at) {
+    r = *reinterpret_cast<const uint2*>((const uint8_t*)row + at);
+  }
+  __device__ __forceinline__ void get(float* f) const {  // exact: every code is a bf16 value
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(r.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(r.x, true);
+    const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(r.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8(r.y, true);
+    f[0] = a[0]; f[1] = a[1]; f[2] = b[0]; f[3] = b[1];
+    f[4] = c[0]; f[5] = c[1]; f[6] = d[0]; f[7] = d[1];
+  }
+};
+
+// One rounding to the stored type, to nearest even.
+template <int DT>
+__device__ __forceinline__ void st8(void* row, int64_t at, const float* f) {
+  if constexpr (DT == MOE_F32) {
+    float* p = (float*)row + at;
+    *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+  } else if constexpr (DT == MOE_BF16) {
+    *reinterpret_cast<u32x4*>((uint16_t*)row + at) =
+        u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+  } else {
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], hi, true);
+    *reinterpret_cast<uint2*>((uint8_t*)row + at) = make_uint2((uint32_t)lo, (uint32_t)hi);
+  }
+}
+
+// Lane exchange inside rows of 16 lanes as DPP operands: lane ^ 1, lane ^ 2, then the mirrored
+// lane of 8 and of 16 (which equal the other half's value once 4, then 8 lanes agree).
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
+}
+
+// every lane of a row of 16 gets the row's sum / maximum / minimum (fixed order of additions)
+__device__ __forceinline__ float sum16(float v) {
+  v += dpp_f32<kDppXor1>(v);
+  v += dpp_f32<kDppXor2>(v);
+  v += dpp_f32<kDppHalfMirror>(v);
+  v += dpp_f32<kDppMirror>(v);
+  return v;
+}
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, dpp_f32<kDppXor1>(v));
+  v = fmaxf(v, dpp_f32<kDppXor2>(v));
+  v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+  v = fmaxf(v, dpp_f32<kDppMirror>(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t max16u(uint32_t v) {
+  v = max(v, dpp_u32<kDppXor1>(v));
+  v = max(v, dpp_u32<kDppXor2>(v));
+  v = max(v, dpp_u32<kDppHalfMirror>(v));
+  v = max(v, dpp_u32<kDppMirror>(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t min16u(uint32_t v) {
+  v = min(v, dpp_u32<kDppXor1>(v));
+  v = min(v, dpp_u32<kDppXor2>(v));
+  v = min(v, dpp_u32<kDppHalfMirror>(v));
+  v = min(v, dpp_u32<kDppMirror>(v));
+  return v;
+}
+
+__device__ __forceinline__ float lane_f32(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+// every lane of the wave gets its sum / maximum
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
+  return (lane_f32(v, 0) + lane_f32(v, 16)) + (lane_f32(v, 32) + lane_f32(v, 48));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max16(v);
+  return fmaxf(fmaxf(lane_f32(v, 0), lane_f32(v, 16)), fmaxf(lane_f32(v, 32), lane_f32(v, 48)));
+}
+
+// A launch whose own return value is the status (an error left by an earlier call of someone
+// else's is neither reported nor cleared).
+template <typename... P, typename... A>
+inline int launch(void (*kernel)(P...), unsigned grid, unsigned block, hipStream_t stream, A... args) {
+  static_assert(sizeof...(P) == sizeof...(A), "one argument for each parameter");
+  return [&](P... p) {
+    void* list[] = {(void*)&p...};
+    return hipLaunchKernel((const void*)kernel, dim3(grid), dim3(block), list, 0, stream) == hipSuccess ? MOE_OK
+                                                                                                       : MOE_ELAUNCH;
+  }(args...);
+}
+
+// Workgroups for as many units of work: kernels step by the grid, which has to stay below 2^32
+// threads.
+inline unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 20) ? units : 1 << 20); }
+
+// a pointer and the bytes between its rows are multiples of `to`
+inline bool aligned_rows(const void* p, int64_t pitch, int esz, int to) {
+  return (uintptr_t)p % (unsigned)to == 0 && (pitch * esz) % to == 0;
+}
+// rows are read and written in chunks of eight elements, by 16 bytes where a chunk has as many
+inline int chunk_align(int dt) { return dt == MOE_FP8_E4M3 ? 8 : 16; }
+
+constexpr int kHMaxRows = 1 << 16;  // longest row of the row operators
+
+}  // namespace moe

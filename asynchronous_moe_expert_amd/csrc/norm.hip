@@ -1,0 +1,368 @@
+// moe_residual_norm, moe_residual_norm_backward: h = x + residual, y = h * rsqrt(mean h^2 + eps) *
+// gamma in fp32, bf16 or 8 bits with scales; and its gradient.  A row stays in registers between
+// its reduction and its output, so each input is read once and each output written once.
+#include <float.h>
+#include <math.h>
+
+#include "home.hpp"
+
+namespace moe {
+
+constexpr int kNormT = 256, kNormWaves = kNormT / kWave;
+constexpr int kNormH = 16384;     // longest row: 256 threads x 8 chunks of 8
+constexpr int kPartials = 512;    // rows of the workspace that the sum over tokens goes through
+
+struct NormJob {
+  int T, H, groups, group_lanes, gamma_f32;  // group_lanes: lanes per scale, 0 for one per row
+  float eps;
+  const void *x, *residual, *gamma;
+  int64_t x_pitch, res_pitch, out_pitch, res_out_pitch;
+  void *out, *residual_out;
+  float *out_scale, *rstd;
+  const int32_t *row_list, *row_count;
+  uint32_t* err;
+};
+
+template <int DT>
+__device__ __forceinline__ int64_t row_bytes(int64_t t, int64_t pitch) {
+  return t * pitch * (DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1);
+}
+
+__device__ __forceinline__ void gamma8(const void* gamma, int f32, int64_t at, float* g) {
+  if (f32) {
+    Chunk<MOE_F32> q;
+    q.load(gamma, at);
+    q.get(g);
+  } else {
+    Chunk<MOE_BF16> q;
+    q.load(gamma, at);
+    q.get(g);
+  }
+}
+
+// the workgroup's sum / maximum in every thread; s[] is free again after the next barrier
+__device__ __forceinline__ float group_sum(float v, float* s) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+__device__ __forceinline__ float group_max(float v, float* s) {
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+
+// the maximum over aligned runs of 4, 8 or 16 lanes
+__device__ __forceinline__ float run_max(float v, int lanes) {
+  v = fmaxf(v, dpp_f32<kDppXor1>(v));
+  v = fmaxf(v, dpp_f32<kDppXor2>(v));
+  if (lanes >= 8) v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+  if (lanes >= 16) v = fmaxf(v, dpp_f32<kDppMirror>(v));
+  return v;
+}
+
+__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax / 448.f, FLT_MIN) : 1.f; }
+
+// A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + 256, ...
+template <int XT, int RT, int OT, int C>
+__global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
+  __shared__ float s_a[2][kNormWaves], s_b[2][kNormWaves];
+  const int rows = j.row_list ? min(j.T, *j.row_count) : j.T;
+  int par = 0;
+  for (int k = blockIdx.x; k < rows; k += gridDim.x) {
+    int t = k;
+    if (j.row_list) {
+      t = j.row_list[k];
+      if (t < 0 || t >= j.T) {
+        if (threadIdx.x == 0) atomicOr(j.err, MOE_ERR_ROW_RANGE);
+        continue;
+      }
+    }
+    const char* x = (const char*)j.x + row_bytes<XT>(t, j.x_pitch);
+    float h[C][8], ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
+      if (at < j.H) {
+        Chunk<XT> q;
+        q.load(x, at);
+        q.get(h[c]);
+        if (j.residual) {
+          Chunk<RT> r;
+          r.load((const char*)j.residual + row_bytes<RT>(t, j.res_pitch), at);
+          float f[8];
+          r.get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[c][e] += f[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
+      }
+    }
+    const float r = 1.f / sqrtf(group_sum(ss, s_a[par]) / (float)j.H + j.eps);
+    if (j.rstd && threadIdx.x == 0) j.rstd[t] = r;
+    char* out = (char*)j.out + row_bytes<OT>(t, j.out_pitch);
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      if (at < j.H) {
+        if (j.residual_out) st8<RT>((char*)j.residual_out + row_bytes<RT>(t, j.res_out_pitch), at, h[c]);
+        float g[8];
+        gamma8(j.gamma, j.gamma_f32, at, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[c][e] *= r * g[e];
+        if constexpr (OT != MOE_FP8_E4M3) st8<OT>(out, at, h[c]);
+      }
+      if constexpr (OT == MOE_FP8_E4M3) {
+        float a = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(h[c][e]));
+        amax = fmaxf(amax, a);
+        if (j.group_lanes) {
+          const float s = scale_of(run_max(a, j.group_lanes));
+          if (at < j.H) {
+            const float inv = 1.f / s;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[c][e] *= inv;
+            st8<OT>(out, at, h[c]);
+            const int lane = threadIdx.x & (j.group_lanes - 1);
+            if (lane == 0) j.out_scale[(int64_t)t * j.groups + at / (j.group_lanes * 8)] = s;
+          }
+        }
+      }
+    }
+    if constexpr (OT == MOE_FP8_E4M3) {
+      if (!j.group_lanes) {
+        const float s = scale_of(group_max(amax, s_b[par])), inv = 1.f / s;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int at = (c * kNormT + (int)threadIdx.x) * 8;
+          if (at < j.H) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[c][e] *= inv;
+            st8<OT>(out, at, h[c]);
+          }
+        }
+        if (threadIdx.x == 0) j.out_scale[t] = s;
+      }
+    }
+    par ^= 1;
+  }
+}
+
+struct NormBackJob {
+  int T, H, gamma_f32;
+  const void *dout, *h, *gamma, *dres;
+  int64_t dout_pitch, h_pitch, dres_pitch, dx_pitch, dresidual_pitch;
+  const float* rstd;
+  void *dx, *dresidual;
+  float* part;  // [gridDim.x][H] sums over this workgroup's tokens, or NULL
+};
+
+// With xhat = h r and g = dout gamma:  dh = r (g - xhat <g, xhat> / H) + dres,  dgamma = sum_t dout xhat.
+// A workgroup takes the rows blockIdx, blockIdx + gridDim, ... and keeps its share of dgamma in
+// registers.
+template <int DT, int HT, int C>
+__global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
+  __shared__ float s_a[2][kNormWaves];
+  float dg[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[c][e] = 0.f;
+  int par = 0;
+  for (int t = blockIdx.x; t < j.T; t += gridDim.x, par ^= 1) {
+    const char* dout = (const char*)j.dout + row_bytes<DT>(t, j.dout_pitch);
+    const char* hr = (const char*)j.h + row_bytes<HT>(t, j.h_pitch);
+    const float r = j.rstd[t];
+    float xh[C][8], g[C][8], dot = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xh[c][e] = g[c][e] = 0.f;
+      if (at < j.H) {
+        Chunk<DT> q;
+        q.load(dout, at);
+        q.get(g[c]);
+        Chunk<HT> p;
+        p.load(hr, at);
+        p.get(xh[c]);
+        float gm[8];
+        gamma8(j.gamma, j.gamma_f32, at, gm);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          xh[c][e] *= r;
+          dg[c][e] = fmaf(g[c][e], xh[c][e], dg[c][e]);
+          g[c][e] *= gm[e];
+          dot = fmaf(g[c][e], xh[c][e], dot);
+        }
+      }
+    }
+    const float mean = group_sum(dot, s_a[par]) / (float)j.H;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      if (at < j.H) {
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = r * (g[c][e] - xh[c][e] * mean);
+        if (j.dres) {
+          Chunk<HT> p;
+          p.load((const char*)j.dres + row_bytes<HT>(t, j.dres_pitch), at);
+          float f[8];
+          p.get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] += f[e];
+        }
+        if (j.dx) st8<DT>((char*)j.dx + row_bytes<DT>(t, j.dx_pitch), at, d);
+        if (j.dresidual) st8<HT>((char*)j.dresidual + row_bytes<HT>(t, j.dresidual_pitch), at, d);
+      }
+    }
+  }
+  if (j.part) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      if (at < j.H) st8<MOE_F32>(j.part + (int64_t)blockIdx.x * j.H, at, dg[c]);
+    }
+  }
+}
+
+// dgamma[col] = sum of the partial rows: 16 columns per workgroup, the rows in 16 runs
+__global__ __launch_bounds__(kNormT) void norm_dgamma_kernel(const float* __restrict__ part, int rows, int H,
+                                                             float* __restrict__ dgamma) {
+  __shared__ float s[16][17];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, col = blockIdx.x * 16 + cx;
+  float sum = 0.f;
+  if (col < H)
+    for (int r = ry; r < rows; r += 16) sum += part[(int64_t)r * H + col];
+  s[ry][cx] = sum;
+  __syncthreads();
+  if (ry == 0 && col < H) {
+    float all = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) all += s[k][cx];
+    dgamma[col] = all;
+  }
+}
+
+static bool norm_pitch_ok(int64_t pitch, int32_t H) { return pitch >= H && pitch <= ((int64_t)1 << 32); }
+static bool norm_types_ok(int a, int b) {
+  return (a == MOE_BF16 && (b == MOE_BF16 || b == MOE_F32)) || (a == MOE_F32 && b == MOE_F32);
+}
+
+template <int XT, int RT, int OT>
+static int norm_by_width(const NormJob& j, hipStream_t stream) {
+  const unsigned grid = grid_of(j.T);
+  if (j.H <= 2048) return launch(norm_kernel<XT, RT, OT, 1>, grid, kNormT, stream, j);
+  if (j.H <= 4096) return launch(norm_kernel<XT, RT, OT, 2>, grid, kNormT, stream, j);
+  if (j.H <= 8192) return launch(norm_kernel<XT, RT, OT, 4>, grid, kNormT, stream, j);
+  return launch(norm_kernel<XT, RT, OT, 8>, grid, kNormT, stream, j);
+}
+
+template <int XT, int RT>
+static int norm_by_out(const NormJob& j, int out, hipStream_t stream) {
+  if (out == MOE_F32) return norm_by_width<XT, RT, MOE_F32>(j, stream);
+  if (out == MOE_BF16) return norm_by_width<XT, RT, MOE_BF16>(j, stream);
+  return norm_by_width<XT, RT, MOE_FP8_E4M3>(j, stream);
+}
+
+template <int DT, int HT>
+static int norm_backward_by_width(const NormBackJob& j, unsigned grid, hipStream_t stream) {
+  if (j.H <= 2048) return launch(norm_backward_kernel<DT, HT, 1>, grid, kNormT, stream, j);
+  if (j.H <= 4096) return launch(norm_backward_kernel<DT, HT, 2>, grid, kNormT, stream, j);
+  if (j.H <= 8192) return launch(norm_backward_kernel<DT, HT, 4>, grid, kNormT, stream, j);
+  return launch(norm_backward_kernel<DT, HT, 8>, grid, kNormT, stream, j);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_residual_norm(const moe_residual_norm_args* a, hipStream_t stream) {
+  if (!a) return MOE_EINVAL_NULL;
+  if (a->T < 0 || a->T > (1 << 24) || a->H < 1 || a->H > kNormH || !(a->eps >= 0.f)) return MOE_EINVAL_SIZE;
+  const bool fp8 = a->out_dtype == MOE_FP8_E4M3;
+  if (!norm_types_ok(a->x_dtype, a->res_dtype) || (a->gamma_dtype != MOE_F32 && a->gamma_dtype != MOE_BF16) ||
+      (a->out_dtype != MOE_F32 && a->out_dtype != MOE_BF16 && !fp8))
+    return MOE_EINVAL_DTYPE;
+  if (a->H % 8) return MOE_EINVAL_SHAPE;
+  if (!norm_pitch_ok(a->x_pitch, a->H) || !norm_pitch_ok(a->out_pitch, a->H) ||
+      (a->residual && !norm_pitch_ok(a->res_pitch, a->H)) ||
+      (a->residual_out && !norm_pitch_ok(a->res_out_pitch, a->H)))
+    return MOE_EINVAL_SIZE;
+  if (fp8 && a->group != 0 && a->group != 32 && a->group != 64 && a->group != 128) return MOE_EINVAL_SIZE;
+  if (!a->row_list != !a->row_count || (a->row_list && !a->err)) return MOE_EINVAL_NULL;
+  if (a->T == 0) return MOE_OK;
+  if (!a->x || !a->gamma || !a->out || (fp8 && !a->out_scale)) return MOE_EINVAL_NULL;
+  const int xs = dtype_size(a->x_dtype), rs = dtype_size(a->res_dtype), os = dtype_size(a->out_dtype);
+  if (!aligned_rows(a->x, a->x_pitch, xs, 16) || !aligned16(a->gamma) ||
+      !aligned_rows(a->out, a->out_pitch, os, chunk_align(a->out_dtype)) ||
+      (a->residual && !aligned_rows(a->residual, a->res_pitch, rs, 16)) ||
+      (a->residual_out && !aligned_rows(a->residual_out, a->res_out_pitch, rs, 16)))
+    return MOE_EINVAL_ALIGN;
+  NormJob j;
+  j.T = a->T; j.H = a->H; j.eps = a->eps; j.gamma_f32 = a->gamma_dtype == MOE_F32;
+  j.group_lanes = fp8 ? a->group / 8 : 0;
+  j.groups = fp8 && a->group ? (a->H + a->group - 1) / a->group : 1;
+  j.x = a->x; j.residual = a->residual; j.gamma = a->gamma; j.out = a->out; j.residual_out = a->residual_out;
+  j.x_pitch = a->x_pitch; j.res_pitch = a->res_pitch; j.out_pitch = a->out_pitch; j.res_out_pitch = a->res_out_pitch;
+  j.out_scale = a->out_scale; j.rstd = a->rstd; j.row_list = a->row_list; j.row_count = a->row_count; j.err = a->err;
+  if (a->x_dtype == MOE_F32) return norm_by_out<MOE_F32, MOE_F32>(j, a->out_dtype, stream);
+  if (a->res_dtype == MOE_F32) return norm_by_out<MOE_BF16, MOE_F32>(j, a->out_dtype, stream);
+  return norm_by_out<MOE_BF16, MOE_BF16>(j, a->out_dtype, stream);
+}
+
+extern "C" size_t moe_residual_norm_backward_workspace_size(int32_t H) {
+  return H > 0 ? (size_t)kPartials * (size_t)H * sizeof(float) : 0;
+}
+
+extern "C" int moe_residual_norm_backward(const moe_residual_norm_backward_args* a, hipStream_t stream) {
+  if (!a) return MOE_EINVAL_NULL;
+  if (a->T < 0 || a->T > (1 << 24) || a->H < 1 || a->H > kNormH) return MOE_EINVAL_SIZE;
+  if (!norm_types_ok(a->dtype, a->h_dtype) || (a->gamma_dtype != MOE_F32 && a->gamma_dtype != MOE_BF16))
+    return MOE_EINVAL_DTYPE;
+  if (a->H % 8) return MOE_EINVAL_SHAPE;
+  if (!norm_pitch_ok(a->dout_pitch, a->H) || !norm_pitch_ok(a->h_pitch, a->H) ||
+      (a->dres && !norm_pitch_ok(a->dres_pitch, a->H)) || (a->dx && !norm_pitch_ok(a->dx_pitch, a->H)) ||
+      (a->dresidual && !norm_pitch_ok(a->dresidual_pitch, a->H)))
+    return MOE_EINVAL_SIZE;
+  if (a->T > 0) {
+    if (!a->dx && !a->dresidual && !a->dgamma) return MOE_EINVAL_NULL;
+    if (!a->dout || !a->h || !a->gamma || !a->rstd) return MOE_EINVAL_NULL;
+    const int ds = dtype_size(a->dtype), hs = dtype_size(a->h_dtype);
+    if (!aligned_rows(a->dout, a->dout_pitch, ds, 16) || !aligned_rows(a->h, a->h_pitch, hs, 16) ||
+        !aligned16(a->gamma) || (a->dres && !aligned_rows(a->dres, a->dres_pitch, hs, 16)) ||
+        (a->dx && !aligned_rows(a->dx, a->dx_pitch, ds, 16)) ||
+        (a->dresidual && !aligned_rows(a->dresidual, a->dresidual_pitch, hs, 16)))
+      return MOE_EINVAL_ALIGN;
+    if (a->dgamma) {
+      if (!a->workspace || a->workspace_bytes < moe_residual_norm_backward_workspace_size(a->H)) return MOE_EWORKSPACE;
+      if (!aligned16(a->workspace)) return MOE_EINVAL_ALIGN;
+    }
+  }
+  const unsigned grid = (unsigned)(a->T < kPartials ? a->T : kPartials);
+  if (a->T > 0) {
+    NormBackJob j;
+    j.T = a->T; j.H = a->H; j.gamma_f32 = a->gamma_dtype == MOE_F32;
+    j.dout = a->dout; j.h = a->h; j.gamma = a->gamma; j.dres = a->dres;
+    j.dout_pitch = a->dout_pitch; j.h_pitch = a->h_pitch; j.dres_pitch = a->dres_pitch; j.dx_pitch = a->dx_pitch;
+    j.dresidual_pitch = a->dresidual_pitch;
+    j.rstd = a->rstd; j.dx = a->dx; j.dresidual = a->dresidual;
+    j.part = a->dgamma ? (float*)a->workspace : nullptr;
+    int rc;
+    if (a->dtype == MOE_F32) rc = norm_backward_by_width<MOE_F32, MOE_F32>(j, grid, stream);
+    else if (a->h_dtype == MOE_F32) rc = norm_backward_by_width<MOE_BF16, MOE_F32>(j, grid, stream);
+    else rc = norm_backward_by_width<MOE_BF16, MOE_BF16>(j, grid, stream);
+    if (rc != MOE_OK) return rc;
+  }
+  if (!a->dgamma) return MOE_OK;
+  return launch(norm_dgamma_kernel, (unsigned)((a->H + 15) / 16), kNormT, stream, (const float*)a->workspace, (int)grid,
+                a->H, a->dgamma);
+}

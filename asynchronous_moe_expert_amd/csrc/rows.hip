@@ -1,0 +1,456 @@
+// moe_sort_rows, moe_merge_rows, moe_merge_rows_backward: rows of tokens sorted by expert and
+// back.  All three move rows and are bound by memory; the index is integer work on n = T K ids.
+#include "home.hpp"
+
+namespace moe {
+
+constexpr int kMaxEloc = 256, kMaxK = 32;
+constexpr int kNone = kMaxEloc;  // key of a pair without a row
+
+struct SortJob {
+  int T, K, n, base, E_loc;
+  const int32_t* expert;
+  int32_t *perm, *pos, *counts, *offsets, *row_slot;
+  uint32_t* err;
+};
+
+__device__ __forceinline__ int sort_key(const SortJob& j, int i, unsigned& bad) {
+  const int g = j.expert[i];
+  const int64_t e = (int64_t)g - j.base;
+  if (g != -1 && e >= 0 && e < j.E_loc) return (int)e;
+  if (g != -1) bad = MOE_ERR_EXPERT_NONLOCAL;
+  return kNone;
+}
+
+// ------------------------------------------------------------------------------- index
+// Two launches over at most kSegs segments of the pairs (a multiple of kIdx pairs each):
+//   count   each workgroup counts its segment's keys into ws[segment][E_loc]
+//   place   each workgroup sums the counts of the segments before its own and of all (at most
+//           kSegs x E_loc values, L2-resident), scans them over the experts, and gives its own
+//           pairs their rows, 1024 at a time: a pair's rank among equal keys of its wave from a
+//           9-bit ballot match, the waves' counts scanned per expert
+constexpr int kIdx = 1024, kIdxWaves = kIdx / kWave;
+constexpr int kSegs = 256;
+constexpr int kCopies = 4;  // counters per expert: a favoured expert's lanes do not queue on one
+
+__global__ __launch_bounds__(kIdx) void sort_count_kernel(SortJob j, int seg_len, int32_t* __restrict__ ws) {
+  __shared__ int s_cnt[kMaxEloc * (kCopies + 1)];
+  const int tid = threadIdx.x;
+  for (int x = tid; x < kMaxEloc * (kCopies + 1); x += kIdx) s_cnt[x] = 0;
+  __syncthreads();
+  const int lo = blockIdx.x * seg_len, hi = min(j.n, lo + seg_len);
+  unsigned bad = 0;
+  for (int i = lo + tid; i < hi; i += kIdx) {
+    const int key = sort_key(j, i, bad);
+    if (key < kNone) atomicAdd(&s_cnt[key * (kCopies + 1) + (tid & (kCopies - 1))], 1);
+  }
+  if (bad) atomicOr(j.err, bad);
+  __syncthreads();
+  for (int e = tid; e < j.E_loc; e += kIdx) {
+    int sum = 0;
+    for (int c = 0; c < kCopies; ++c) sum += s_cnt[e * (kCopies + 1) + c];
+    ws[blockIdx.x * j.E_loc + e] = sum;
+  }
+}
+
+__global__ __launch_bounds__(kIdx) void sort_place_kernel(SortJob j, int segs, int seg_len,
+                                                          const int32_t* __restrict__ ws) {
+  __shared__ int s_run[kMaxEloc];   // next row of each expert in this segment
+  __shared__ int s_all[kMaxEloc];
+  __shared__ int s_wcnt[kIdxWaves][kMaxEloc + 1];
+  __shared__ int s_total;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, seg = blockIdx.x;
+  for (int e = tid; e < kMaxEloc; e += kIdx) s_run[e] = s_all[e] = 0;
+  __syncthreads();
+  // column sums: thread (g, e) takes the segments g, g + 4, ...
+  {
+    const int e = tid & (kMaxEloc - 1);
+    int before = 0, all = 0;
+    if (e < j.E_loc) {
+      for (int s = tid / kMaxEloc; s < segs; s += kIdx / kMaxEloc) {
+        const int c = ws[s * j.E_loc + e];
+        all += c;
+        before += s < seg ? c : 0;
+      }
+      atomicAdd(&s_run[e], before);
+      atomicAdd(&s_all[e], all);
+    }
+  }
+  __syncthreads();
+  if (wv == 0) {  // exclusive scan over the experts, four per lane
+    int v[4], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = s_all[lane * 4 + k];
+      sum += v[k];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int t = __shfl_up(incl, d);
+      if (lane >= d) incl += t;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = lane * 4 + k;
+      if (seg == 0 && e < j.E_loc) {
+        j.counts[e] = v[k];
+        j.offsets[e] = run;
+      }
+      s_run[e] += run;
+      run += v[k];
+    }
+    if (lane == 63) {
+      s_total = incl;
+      if (seg == 0) j.offsets[j.E_loc] = incl;
+    }
+  }
+  const int lo = seg * seg_len, hi = min(j.n, lo + seg_len);
+  for (int c0 = lo; c0 < hi; c0 += kIdx) {
+    const int i = c0 + tid;
+    unsigned bad = 0;
+    const int key = i < hi ? sort_key(j, i, bad) : kNone;
+    for (int x = tid; x < kIdxWaves * (kMaxEloc + 1); x += kIdx) (&s_wcnt[0][0])[x] = 0;
+    uint64_t peers = ~0ull;
+#pragma unroll
+    for (int b = 0; b < 9; ++b) {
+      const bool bit = (key >> b) & 1;
+      const uint64_t bal = __ballot(bit);
+      peers &= bit ? bal : ~bal;
+    }
+    const int rank = __popcll(peers & ((1ull << lane) - 1ull));
+    __syncthreads();
+    if (key < kNone && rank == 0) s_wcnt[wv][key] = __popcll(peers);
+    __syncthreads();
+    if (tid < j.E_loc) {
+      int run = s_run[tid];
+#pragma unroll
+      for (int w = 0; w < kIdxWaves; ++w) {
+        const int cnt = s_wcnt[w][tid];
+        s_wcnt[w][tid] = run;
+        run += cnt;
+      }
+      s_run[tid] = run;
+    }
+    __syncthreads();
+    if (key < kNone) {
+      const int r = s_wcnt[wv][key] + rank;
+      j.pos[i] = r;
+      if (j.perm) j.perm[r] = i;
+      if (j.row_slot) j.row_slot[r] = i / j.K;
+    } else if (i < hi) {
+      j.pos[i] = -1;
+    }
+    if (i < hi && i >= s_total) {  // rows past the last
+      if (j.perm) j.perm[i] = -1;
+      if (j.row_slot) j.row_slot[i] = -1;
+    }
+    __syncthreads();
+  }
+}
+
+// no pairs: every count is zero
+__global__ void sort_empty_kernel(SortJob j) {
+  for (int e = threadIdx.x; e <= j.E_loc; e += blockDim.x) {
+    if (e < j.E_loc) j.counts[e] = 0;
+    j.offsets[e] = 0;
+  }
+}
+
+// -------------------------------------------------------------------------- copying rows
+struct CopyJob {
+  int K, H, chunks;  // chunks of eight elements in a row
+  int group_shift;   // fp8: log2 of the columns per scale, -1 for one per row
+  int groups;
+  const void* x;
+  int64_t x_pitch;
+  const float* x_scale;
+  void* xs;
+  int64_t xs_pitch;
+};
+
+template <int DT>
+struct SortedType {
+  static constexpr int out = DT == MOE_FP8_E4M3 ? MOE_BF16 : DT;
+};
+
+// One chunk of token t's row to its rows p[0 .. K): read once, written K times.
+template <int DT>
+__device__ __forceinline__ void copy_chunk(const CopyJob& c, int t, int ch, const int* p) {
+  constexpr int OUT = SortedType<DT>::out;
+  constexpr int esz = DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1;
+  const char* row = (const char*)c.x + (int64_t)t * c.x_pitch * esz;
+  Chunk<DT> q;
+  q.load(row, (int64_t)ch * 8);
+  float f[8];
+  q.get(f);
+  if constexpr (DT == MOE_FP8_E4M3) {
+    const int g = c.group_shift < 0 ? 0 : (ch * 8) >> c.group_shift;
+    const float s = c.x_scale[(int64_t)t * c.groups + g];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= s;
+  }
+  constexpr int osz = OUT == MOE_F32 ? 4 : 2;
+  for (int k = 0; k < c.K; ++k) {
+    const int r = p[k];
+    if (r < 0) continue;
+    char* dst = (char*)c.xs + (int64_t)r * c.xs_pitch * osz;
+    if constexpr (DT == MOE_BF16)
+      *reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8) = q.r;
+    else
+      st8<OUT>(dst, (int64_t)ch * 8, f);
+  }
+}
+
+// A workgroup per token (blockIdx, blockIdx + gridDim, ...).
+template <int DT>
+__global__ __launch_bounds__(256) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
+  __shared__ int s_pos[kMaxK];
+  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    if (threadIdx.x < c.K) s_pos[threadIdx.x] = pos[(int64_t)t * c.K + threadIdx.x];
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < c.chunks; ch += 256) copy_chunk<DT>(c, t, ch, s_pos);
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------------------- merging rows
+struct MergeJob {
+  int T, K, H, chunks;
+  const void* rows;
+  int64_t row_pitch, n_rows;
+  const int32_t* pos;
+  const float* w;
+  void* out;
+  int64_t out_pitch;
+  uint32_t* err;
+};
+
+template <int DT>
+__device__ __forceinline__ const char* row_at(const void* rows, int64_t r, int64_t pitch) {
+  return (const char*)rows + r * pitch * (DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1);
+}
+
+// A workgroup per token; each lane sums its chunks over the positions in order.
+template <int RT, int OT>
+__global__ __launch_bounds__(256) void merge_kernel(MergeJob m) {
+  __shared__ int s_pos[kMaxK];
+  __shared__ float s_w[kMaxK];
+  for (int t = blockIdx.x; t < m.T; t += gridDim.x) {
+    if (threadIdx.x < m.K) {
+      const int64_t at = (int64_t)t * m.K + threadIdx.x;
+      int p = m.pos[at];
+      if (p < -1 || p >= m.n_rows) {
+        p = -1;
+        atomicOr(m.err, MOE_ERR_ROW_RANGE);
+      }
+      s_pos[threadIdx.x] = p;
+      s_w[threadIdx.x] = m.w ? m.w[at] : 1.f;
+    }
+    __syncthreads();
+    char* out = (char*)m.out + (int64_t)t * m.out_pitch * (OT == MOE_F32 ? 4 : 2);
+    for (int ch = threadIdx.x; ch < m.chunks; ch += 256) {
+      float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int k = 0; k < m.K; ++k) {
+        if (s_pos[k] < 0) continue;
+        Chunk<RT> q;
+        q.load(row_at<RT>(m.rows, s_pos[k], m.row_pitch), (int64_t)ch * 8);
+        float f[8];
+        q.get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(s_w[k], f[e], acc[e]);
+      }
+      st8<OT>(out, (int64_t)ch * 8, acc);
+    }
+    __syncthreads();
+  }
+}
+
+struct MergeBackJob {
+  int T, K, H, chunks;
+  const void* dout;
+  int64_t dout_pitch;
+  const void* rows;
+  int64_t row_pitch, n_rows;
+  const int32_t* pos;
+  const float* w;
+  void* drows;
+  int64_t drows_pitch;
+  float* dw;
+  uint32_t* err;
+};
+
+// A workgroup per token, one position after the other.
+template <int DT, int RT>
+__global__ __launch_bounds__(256) void merge_backward_kernel(MergeBackJob m) {
+  __shared__ float s_sum[4];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  for (int t = blockIdx.x; t < m.T; t += gridDim.x) {
+    const char* dout = row_at<DT>(m.dout, t, m.dout_pitch);
+    for (int k = 0; k < m.K; ++k) {
+      const int64_t at = (int64_t)t * m.K + k;
+      const int p = m.pos[at];
+      if (p < 0 || p >= m.n_rows) {
+        if (threadIdx.x == 0) {
+          if (p != -1) atomicOr(m.err, MOE_ERR_ROW_RANGE);
+          if (m.dw) m.dw[at] = 0.f;
+        }
+        continue;
+      }
+      const float w = m.w ? m.w[at] : 1.f;
+      float dot = 0.f;
+      for (int ch = threadIdx.x; ch < m.chunks; ch += 256) {
+        Chunk<DT> q;
+        q.load(dout, (int64_t)ch * 8);
+        float g[8];
+        q.get(g);
+        if (m.dw) {
+          Chunk<RT> y;
+          y.load(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
+          float f[8];
+          y.get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(g[e], f[e], dot);
+        }
+        if (m.drows) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] *= w;
+          st8<RT>((char*)m.drows + (int64_t)p * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, g);
+        }
+      }
+      if (m.dw) {
+        dot = wave_sum(dot);
+        if (lane == 0) s_sum[wv] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) m.dw[at] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+        __syncthreads();
+      }
+    }
+  }
+}
+
+constexpr int64_t kMaxPitch = (int64_t)1 << 32;
+
+static bool row_size_ok(int32_t T, int32_t K, int32_t H) {
+  return T >= 0 && T <= (1 << 24) && K >= 1 && K <= kMaxK && (int64_t)T * K <= (1 << 24) && H >= 1 && H <= kHMaxRows;
+}
+static bool pitch_ok(int64_t pitch, int32_t H) { return pitch >= H && pitch <= kMaxPitch; }
+static bool f32_or_bf16(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_sort_rows_workspace_size(int32_t n_max) {
+  return n_max > 0 ? (size_t)kSegs * kMaxEloc * sizeof(int32_t) : 0;
+}
+
+static int check_sort(const moe_sort_rows_args* a) {
+  if (!row_size_ok(a->T, a->K, a->H) || a->E_loc < 1 || a->E_loc > kMaxEloc) return MOE_EINVAL_SIZE;
+  if (a->xs) {
+    if (a->x_dtype != MOE_FP8_E4M3 && !f32_or_bf16(a->x_dtype)) return MOE_EINVAL_DTYPE;
+    if (a->H % 8) return MOE_EINVAL_SHAPE;
+    if (!pitch_ok(a->x_pitch, a->H) || !pitch_ok(a->xs_pitch, a->H)) return MOE_EINVAL_SIZE;
+    if (a->x_dtype == MOE_FP8_E4M3 && a->group != 0 && a->group != 32 && a->group != 64 && a->group != 128)
+      return MOE_EINVAL_SIZE;
+  }
+  if (!a->counts || !a->offsets || !a->err) return MOE_EINVAL_NULL;
+  if (a->T == 0) return MOE_OK;
+  if (!a->expert || !a->pos) return MOE_EINVAL_NULL;
+  if (a->xs) {
+    if (!a->x || (a->x_dtype == MOE_FP8_E4M3 && !a->x_scale)) return MOE_EINVAL_NULL;
+    const int out = a->x_dtype == MOE_F32 ? MOE_F32 : MOE_BF16;
+    if (!aligned_rows(a->x, a->x_pitch, dtype_size(a->x_dtype), chunk_align(a->x_dtype)) ||
+        !aligned_rows(a->xs, a->xs_pitch, dtype_size(out), 16))
+      return MOE_EINVAL_ALIGN;
+  }
+  if (!a->workspace || a->workspace_bytes < moe_sort_rows_workspace_size(a->T * a->K)) return MOE_EWORKSPACE;
+  if (!aligned16(a->workspace)) return MOE_EINVAL_ALIGN;
+  return MOE_OK;
+}
+
+template <int DT>
+static int copy_rows(const moe_sort_rows_args* a, hipStream_t stream) {
+  CopyJob c;
+  c.K = a->K; c.H = a->H; c.chunks = a->H / 8;
+  c.group_shift = a->group ? __builtin_ctz((unsigned)a->group) : -1;
+  c.groups = a->group ? (a->H + a->group - 1) / a->group : 1;
+  c.x = a->x; c.x_pitch = a->x_pitch; c.x_scale = a->x_scale;
+  c.xs = a->xs; c.xs_pitch = a->xs_pitch;
+  return launch(sort_copy_kernel<DT>, grid_of(a->T), 256, stream, c, a->T, (const int32_t*)a->pos);
+}
+
+extern "C" int moe_sort_rows(const moe_sort_rows_args* a, hipStream_t stream) {
+  if (!a) return MOE_EINVAL_NULL;
+  int rc = check_sort(a);
+  if (rc != MOE_OK) return rc;
+  const int n = a->T * a->K;
+  SortJob j;
+  j.T = a->T; j.K = a->K; j.n = n; j.base = a->expert_base; j.E_loc = a->E_loc;
+  j.expert = a->expert; j.perm = a->perm; j.pos = a->pos; j.counts = a->counts; j.offsets = a->offsets;
+  j.row_slot = a->row_slot; j.err = a->err;
+  if (n == 0) return launch(sort_empty_kernel, 1, 256, stream, j);
+  const int per = (n + kSegs - 1) / kSegs, seg_len = (per + kIdx - 1) / kIdx * kIdx;
+  const int segs = (n + seg_len - 1) / seg_len;
+  rc = launch(sort_count_kernel, (unsigned)segs, kIdx, stream, j, seg_len, (int32_t*)a->workspace);
+  if (rc != MOE_OK) return rc;
+  rc = launch(sort_place_kernel, (unsigned)segs, kIdx, stream, j, segs, seg_len, (const int32_t*)a->workspace);
+  if (rc != MOE_OK || !a->xs) return rc;
+  if (a->x_dtype == MOE_F32) return copy_rows<MOE_F32>(a, stream);
+  if (a->x_dtype == MOE_BF16) return copy_rows<MOE_BF16>(a, stream);
+  return copy_rows<MOE_FP8_E4M3>(a, stream);
+}
+
+extern "C" int moe_merge_rows(const moe_merge_rows_args* a, hipStream_t stream) {
+  if (!a) return MOE_EINVAL_NULL;
+  if (!row_size_ok(a->T, a->K, a->H) || a->n_rows < 0) return MOE_EINVAL_SIZE;
+  if (!f32_or_bf16(a->row_dtype) || !f32_or_bf16(a->out_dtype)) return MOE_EINVAL_DTYPE;
+  if (a->H % 8) return MOE_EINVAL_SHAPE;
+  if (!pitch_ok(a->row_pitch, a->H) || !pitch_ok(a->out_pitch, a->H)) return MOE_EINVAL_SIZE;
+  if (!a->err) return MOE_EINVAL_NULL;
+  if (a->T == 0) return MOE_OK;
+  if (!a->pos || !a->out || (a->n_rows > 0 && !a->rows)) return MOE_EINVAL_NULL;
+  if (!aligned_rows(a->rows, a->row_pitch, dtype_size(a->row_dtype), 16) ||
+      !aligned_rows(a->out, a->out_pitch, dtype_size(a->out_dtype), 16))
+    return MOE_EINVAL_ALIGN;
+  MergeJob m;
+  m.T = a->T; m.K = a->K; m.H = a->H; m.chunks = a->H / 8;
+  m.rows = a->rows; m.row_pitch = a->row_pitch; m.n_rows = a->n_rows;
+  m.pos = a->pos; m.w = a->w; m.out = a->out; m.out_pitch = a->out_pitch; m.err = a->err;
+  const unsigned grid = grid_of(a->T);
+  if (a->row_dtype == MOE_F32)
+    return a->out_dtype == MOE_F32 ? launch(merge_kernel<MOE_F32, MOE_F32>, grid, 256, stream, m)
+                                   : launch(merge_kernel<MOE_F32, MOE_BF16>, grid, 256, stream, m);
+  return a->out_dtype == MOE_F32 ? launch(merge_kernel<MOE_BF16, MOE_F32>, grid, 256, stream, m)
+                                 : launch(merge_kernel<MOE_BF16, MOE_BF16>, grid, 256, stream, m);
+}
+
+extern "C" int moe_merge_rows_backward(const moe_merge_rows_backward_args* a, hipStream_t stream) {
+  if (!a) return MOE_EINVAL_NULL;
+  if (!row_size_ok(a->T, a->K, a->H) || a->n_rows < 0) return MOE_EINVAL_SIZE;
+  if (!f32_or_bf16(a->row_dtype) || !f32_or_bf16(a->dout_dtype)) return MOE_EINVAL_DTYPE;
+  if (a->H % 8) return MOE_EINVAL_SHAPE;
+  if (!pitch_ok(a->dout_pitch, a->H) || (a->dw && !pitch_ok(a->row_pitch, a->H)) ||
+      (a->drows && !pitch_ok(a->drows_pitch, a->H)))
+    return MOE_EINVAL_SIZE;
+  if (!a->err) return MOE_EINVAL_NULL;
+  if (a->T == 0) return MOE_OK;
+  if (!a->drows && !a->dw) return MOE_EINVAL_NULL;
+  if (!a->dout || !a->pos || (a->dw && a->n_rows > 0 && !a->rows)) return MOE_EINVAL_NULL;
+  if (!aligned_rows(a->dout, a->dout_pitch, dtype_size(a->dout_dtype), 16) ||
+      (a->dw && !aligned_rows(a->rows, a->row_pitch, dtype_size(a->row_dtype), 16)) ||
+      (a->drows && !aligned_rows(a->drows, a->drows_pitch, dtype_size(a->row_dtype), 16)))
+    return MOE_EINVAL_ALIGN;
+  MergeBackJob m;
+  m.T = a->T; m.K = a->K; m.H = a->H; m.chunks = a->H / 8;
+  m.dout = a->dout; m.dout_pitch = a->dout_pitch; m.rows = a->rows; m.row_pitch = a->row_pitch;
+  m.n_rows = a->n_rows; m.pos = a->pos; m.w = a->w; m.drows = a->drows; m.drows_pitch = a->drows_pitch;
+  m.dw = a->dw; m.err = a->err;
+  const unsigned grid = grid_of(a->T);
+  if (a->dout_dtype == MOE_F32)
+    return a->row_dtype == MOE_F32 ? launch(merge_backward_kernel<MOE_F32, MOE_F32>, grid, 256, stream, m)
+                                   : launch(merge_backward_kernel<MOE_F32, MOE_BF16>, grid, 256, stream, m);
+  return a->row_dtype == MOE_F32 ? launch(merge_backward_kernel<MOE_BF16, MOE_F32>, grid, 256, stream, m)
+                                 : launch(merge_backward_kernel<MOE_BF16, MOE_BF16>, grid, 256, stream, m);
+}

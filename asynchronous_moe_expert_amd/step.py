@@ -186,3 +186,56 @@ class SharedExpert:
             torch.cuda.synchronize(self._dev)
             self._kslots[kslot] = ks
         owner.combine(s.y, s.pos, tok, ks[:n], self._one[:n], gen, m=n, n_rows=n, stream=stream)
+
+
+class ExpertLayer:
+    """A layer whose experts are all on this rank, so that a token's K results come back together
+    and nothing waits: moe_route chooses, moe_sort_rows gives the index (no row is copied), the
+    grouped FFN gathers its rows from x through row_slot, moe_merge_rows applies the weights.
+
+    After run() the buffers hold what a caller may want further on: expert and w ([T][K]), pos,
+    counts and offsets as moe_sort_rows gives them, y (the experts' rows, before the weights)."""
+
+    def __init__(self, E: int, H: int, I: int, K: int, act_dtype: int, w_dtype: int, T_max: int, device="cuda",
+                 score: int = N.MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0):
+        self.E, self.H, self.I, self.K, self.T_max = E, H, I, K, T_max
+        self.act_dtype, self.w_dtype = act_dtype, w_dtype
+        self.how = dict(score=score, renorm=renorm, scale=scale)
+        dev = torch.device(device)
+        n = max(T_max * K, 1)
+        self._expert = torch.empty(n, dtype=torch.int32, device=dev)
+        self._w = torch.empty(n, dtype=torch.float32, device=dev)
+        self.pos = torch.empty(n, dtype=torch.int32, device=dev)
+        self.row_slot = torch.empty(n, dtype=torch.int32, device=dev)
+        self.counts = torch.empty(E, dtype=torch.int32, device=dev)
+        self.offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        self.y = torch.empty((n, H), dtype=_TORCH[act_dtype], device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.workspace = torch.empty(N.moe_ffn_workspace_size(n, E, H, I, act_dtype), dtype=torch.uint8, device=dev)
+        self.sort_ws = torch.empty(max(N.moe_sort_rows_workspace_size(n), 16), dtype=torch.uint8, device=dev)
+        self.w_gu = self.w_d = self.s_gate = self.s_up = self.s_down = None
+        self.expert = self.w = None
+
+    load_weights = ExpertStep.load_weights
+
+    @property
+    def E_loc(self) -> int:
+        return self.E
+
+    def run(self, x, logits, out, bias=None, stream=None) -> None:
+        """x [T][H] in act_dtype, logits [T][E]; out [T][H]: sum_j w_j E_j(x)."""
+        T = x.shape[0]
+        n = T * self.K
+        if T > self.T_max:
+            raise N.MoeError(f"ExpertLayer: {T} tokens, built for {self.T_max}")
+        if x.shape[1] != self.H or x.dtype != _TORCH[self.act_dtype] or logits.shape[0] != T:
+            raise N.MoeError(f"ExpertLayer: x {tuple(x.shape)} {x.dtype} with logits {tuple(logits.shape)}")
+        self.expert, self.w = self._expert[:n].view(T, self.K), self._w[:n].view(T, self.K)
+        N.moe_route(logits, self.expert, self.w, bias=bias, stream=stream, **self.how)
+        N.moe_sort_rows(self.expert, self.E, None, None, None, self.pos, self.counts, self.offsets, self.err,
+                        self.sort_ws, row_slot=self.row_slot, stream=stream)
+        if n:
+            N.moe_expert_ffn_grouped(n, self.E, self.H, self.I, self.act_dtype, self.w_dtype, None, self.offsets,
+                                     self.w_gu, self.w_d, self.y, self.workspace, self.s_gate, self.s_up, self.s_down,
+                                     stream=stream, gather=(None, None, x, self.row_slot))
+        N.moe_merge_rows(self.y[:n], self.pos[:n], self.w, out, self.err, stream=stream)

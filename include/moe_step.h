@@ -352,12 +352,243 @@ int moe_combine_apply(const moe_combine_args* args, hipStream_t stream);
 int moe_combine_release_noalloc(const moe_combine_args* args, hipStream_t stream);
 size_t moe_combine_noalloc_max_arrivals(void);
 
+/* =============================================================== the home rank's side ==
+ * What the rank that owns a token does between two layers' expert steps when all of a token's
+ * results come back together (or there is one rank): norm with the residual, choice of experts,
+ * rows sorted by expert for moe_expert_ffn_grouped (through xb and offsets, or gather-on-load
+ * through row_slot), results merged back; and the gradients of each.  The conventions above
+ * hold.  Moreover:
+ *   - Outputs must not overlap inputs or each other unless a call says so.  A workspace belongs
+ *     to one call at a time: calls that may overlap (streams, captured graphs that are replayed
+ *     side by side) take one each.  Its contents need no preparation and mean nothing afterwards.
+ *   - Every sum is fp32 in a fixed order: the same inputs give the same bits.
+ *   - Rows are [T][pitch], pitch >= the row's length in elements; fp32 and bf16 rows are 16-byte
+ *     aligned (pointer and pitch), fp8 rows 8-byte.  H is a multiple of 8 and at most 65536.
+ *   - Sizes are limited to T * K <= 2^24 and T <= 2^24; offsets of elements are 64 bits wide.
+ *   - A call with T = 0 writes what does not depend on a token (counts, offsets, dgamma).
+ */
+
+/* ---------------------------------------------------------------------- moe_route --
+ * Chooses K of E experts per token and gives their weights.
+ *   score_e = logits[t][e] + bias[e]  (one fp32 addition; bias NULL: the logit)
+ *   expert[t][0..K-1] = the experts of the K largest scores, descending, equal scores in
+ *                       ascending order of e
+ *   MOE_SOFTMAX : w_j = scale * exp(l_j - m) / Z with Z summed over the K chosen experts if renorm,
+ *                 else over all E
+ *   MOE_SIGMOID : w_j = scale * s(l_j), s(z) = 1 / (1 + exp(-z)); divided by the sum of the chosen
+ *                 experts' s if renorm
+ * The bias enters the choice only.  An expert whose score is NaN or -inf is never chosen (a logit
+ * or bias of -inf takes an expert out); a token with fewer than K others gets expert -1 and weight
+ * 0 in the positions left.  A NaN logit counts as probability 0 in Z; logits of +inf share it.
+ * Limits: 1 <= E <= 512, 1 <= K <= min(E, 32); logits F32 or BF16 at their own alignment, any
+ * pitch >= E. */
+typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+
+typedef struct moe_route_args {
+  int32_t T, E, K;
+  const void* logits;      /* [T][pitch] */
+  int32_t dtype;           /* MOE_F32 or MOE_BF16 */
+  int64_t pitch;
+  const float* bias;       /* [E], optional */
+  int32_t score;           /* moe_score */
+  int32_t renorm;          /* 0 or 1 */
+  float scale;
+  int32_t* expert;         /* out [T][K] */
+  float* w;                /* out [T][K] */
+} moe_route_args;
+
+int moe_route(const moe_route_args* args, hipStream_t stream);
+
+/* The gradient of moe_route's weights with respect to the logits, for the experts that it chose
+ * (the choice itself has none): dlogits[t][e] = sum_j dw[t][j] * d w_j / d l_e, zero for experts
+ * that no weight depends on.  expert as moe_route gave it: -1 positions count for nothing, other
+ * values outside [0, E) neither and raise MOE_ERR_EXPERT_NONLOCAL; an expert named twice by one
+ * token counts twice.  dlogits has the logits' type; limits as for moe_route. */
+typedef struct moe_route_backward_args {
+  int32_t T, E, K;
+  const void* logits;      /* [T][pitch] */
+  int32_t dtype;
+  int64_t pitch;
+  const int32_t* expert;   /* [T][K] */
+  const float* dw;         /* [T][K] */
+  int32_t score, renorm;
+  float scale;
+  void* dlogits;           /* out [T][dlogits_pitch] */
+  int64_t dlogits_pitch;
+  uint32_t* err;           /* device error word (OR-ed) */
+} moe_route_backward_args;
+
+int moe_route_backward(const moe_route_backward_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------------------ moe_sort_rows --
+ * Sorts the n = T * K pairs i = t * K + j (token t to expert[t][j]) by local expert, ascending,
+ * in the order of i inside an expert, and copies each pair's row.  Outputs as moe_assemble's for
+ * the queue of all pairs:
+ *   counts[e], offsets[e], offsets[E_loc]                       (int32 [E_loc], [E_loc + 1])
+ *   perm[r]     = pair at row r, -1 for r >= offsets[E_loc]     (int32 [n], may be NULL)
+ *   pos[i]      = row of pair i, -1 if it has none              (int32 [n])
+ *   row_slot[r] = token of row r, -1 for r >= offsets[E_loc]    (int32 [n], may be NULL)
+ *   xs[r][:]    = x[row_slot[r]][:]                             ([n][xs_pitch], may be NULL: index only)
+ * xs has x's type; for MOE_FP8_E4M3 x it is MOE_BF16 and holds code * scale, x_scale being
+ * [T][ceil(H / group)] with one scale per `group` columns (32, 64 or 128), or [T] for group = 0.
+ * Rows of xs from offsets[E_loc] on are left as they were.
+ * A pair with expert -1 (no expert) gets no row; one with another value outside
+ * [expert_base, expert_base + E_loc) neither, and raises MOE_ERR_EXPERT_NONLOCAL.
+ * The gradient of x is moe_merge_rows of the rows' gradient with this pos and w = NULL.
+ * Limits: 1 <= E_loc <= 256, 1 <= K <= 32; the workspace holds moe_sort_rows_workspace_size(n)
+ * bytes (none for short queues, at most 256 KiB), 16-byte aligned. */
+typedef struct moe_sort_rows_args {
+  int32_t T, K, H;
+  int32_t expert_base, E_loc;
+  const int32_t* expert;   /* [T][K] */
+  const void* x;           /* [T][x_pitch]; not read when xs is NULL */
+  int32_t x_dtype;         /* MOE_F32, MOE_BF16 or MOE_FP8_E4M3 */
+  int64_t x_pitch;
+  const float* x_scale;    /* fp8 only */
+  int32_t group;           /* fp8 only: 0, 32, 64 or 128 */
+  void* xs;                /* out [n][xs_pitch], optional */
+  int64_t xs_pitch;
+  int32_t* perm;           /* out [n], optional */
+  int32_t* pos;            /* out [n] */
+  int32_t* counts;         /* out [E_loc] */
+  int32_t* offsets;        /* out [E_loc + 1] */
+  int32_t* row_slot;       /* out [n], optional */
+  uint32_t* err;           /* device error word (OR-ed) */
+  void* workspace;
+  size_t workspace_bytes;
+} moe_sort_rows_args;
+
+size_t moe_sort_rows_workspace_size(int32_t n_max);
+int moe_sort_rows(const moe_sort_rows_args* args, hipStream_t stream);
+
+/* ----------------------------------------------------------------- moe_merge_rows --
+ * out[t][:] = sum_j w[t][j] * rows[pos[t][j]][:], fp32 in the order of j, rounded once to
+ * out_dtype; w NULL: all weights 1 (then it is the gradient of moe_sort_rows' x).  A position of
+ * -1 adds nothing whatever its weight; one outside [-1, n_rows) neither, and raises
+ * MOE_ERR_ROW_RANGE.  A token with none gets zeros.  1 <= K <= 32, types F32 or BF16. */
+typedef struct moe_merge_rows_args {
+  int32_t T, K, H;
+  const void* rows;        /* [n_rows][row_pitch] */
+  int32_t row_dtype;
+  int64_t row_pitch, n_rows;
+  const int32_t* pos;      /* [T][K] */
+  const float* w;          /* [T][K], optional */
+  void* out;               /* out [T][out_pitch] */
+  int32_t out_dtype;
+  int64_t out_pitch;
+  uint32_t* err;           /* device error word (OR-ed) */
+} moe_merge_rows_args;
+
+int moe_merge_rows(const moe_merge_rows_args* args, hipStream_t stream);
+
+/* The gradients of moe_merge_rows:
+ *   drows[pos[t][j]][:] = w[t][j] * dout[t][:]     (row_dtype; may be NULL)
+ *   dw[t][j]            = <dout[t], rows[pos[t][j]]>, 0 where pos gives no row   (fp32 [T][K]; may
+ *                         be NULL, then rows may be too)
+ * Each row belongs to one (t, j), as in moe_sort_rows' pos: drows of a row that several name holds
+ * the product of one of them.  Rows that none names are left as they were.  pos outside
+ * [-1, n_rows) as in moe_merge_rows.  At least one of drows and dw is given. */
+typedef struct moe_merge_rows_backward_args {
+  int32_t T, K, H;
+  const void* dout;        /* [T][dout_pitch] */
+  int32_t dout_dtype;
+  int64_t dout_pitch;
+  const void* rows;        /* [n_rows][row_pitch], for dw */
+  int32_t row_dtype;       /* of rows and drows */
+  int64_t row_pitch, n_rows;
+  const int32_t* pos;      /* [T][K] */
+  const float* w;          /* [T][K], optional (1) */
+  void* drows;             /* out [n_rows][drows_pitch], optional */
+  int64_t drows_pitch;
+  float* dw;               /* out [T][K], optional */
+  uint32_t* err;           /* device error word (OR-ed) */
+} moe_merge_rows_backward_args;
+
+int moe_merge_rows_backward(const moe_merge_rows_backward_args* args, hipStream_t stream);
+
+/* -------------------------------------------------------------- moe_residual_norm --
+ *   h = x[t] + residual[t] (residual NULL: x[t]),  r = 1 / sqrt(mean(h^2) + eps),  y = h * r * gamma
+ *   residual_out[t] = h in the residual's type (optional),  rstd[t] = r (optional),  out[t] = y
+ * all from the unrounded fp32 h.  residual_out may be residual itself and out may be x itself
+ * (same type and pitch).
+ * out_dtype MOE_FP8_E4M3: out_scale is [T][ceil(H / group)], one scale per `group` columns (32, 64
+ * or 128; the last group may be shorter), or [T] for group = 0; over a group
+ *   scale = max|y| / 448, at least the smallest normal fp32 (1 where all are 0),
+ *   code  = y / scale to nearest even, by the reciprocal of scale.
+ * A NaN keeps a NaN code; a group that holds an infinity stands for NaN.
+ * row_list, row_count (both or neither): only the rows row_list[0 .. *row_count - 1] are computed, the others
+ * left as they were (moe_combine_release's rel_list and rel_count, for the rows that a step
+ * released).  row_list has T entries, *row_count is read on the device and cut to [0, T]; an entry
+ * outside [0, T) raises MOE_ERR_ROW_RANGE in *err (required then) and is skipped; entries are distinct.
+ * Types: (x, residual) = (BF16, BF16), (BF16, F32) or (F32, F32); gamma F32 or BF16; out F32, BF16
+ * or FP8.  H <= 16384, eps >= 0. */
+typedef struct moe_residual_norm_args {
+  int32_t T, H;
+  const void* x;           /* [T][x_pitch] */
+  int32_t x_dtype;
+  int64_t x_pitch;
+  const void* residual;    /* [T][res_pitch], optional */
+  int32_t res_dtype;       /* of residual and residual_out */
+  int64_t res_pitch;
+  const void* gamma;       /* [H] */
+  int32_t gamma_dtype;
+  float eps;
+  void* out;               /* out [T][out_pitch] */
+  int32_t out_dtype;
+  int64_t out_pitch;
+  float* out_scale;        /* out, fp8 only */
+  int32_t group;           /* fp8 only: 0, 32, 64 or 128 */
+  void* residual_out;      /* out [T][res_out_pitch], optional */
+  int64_t res_out_pitch;
+  float* rstd;             /* out [T], optional */
+  const int32_t* row_list; /* optional [T] */
+  const int32_t* row_count;
+  uint32_t* err;           /* device error word (OR-ed), with row_list */
+} moe_residual_norm_args;
+
+int moe_residual_norm(const moe_residual_norm_args* args, hipStream_t stream);
+
+/* The gradients of moe_residual_norm for given h (its residual_out, or x) and rstd:
+ *   g = dout[t] * gamma,  dh = r * (g - h * r^2 * <g, h> / H) + dres[t]   (dres optional: what reaches
+ *                                                                          residual_out from elsewhere)
+ *   dx[t] = dh in dout's type, dresidual[t] = dh in h's type (each optional)
+ *   dgamma = sum_t dout[t] * h * r   (fp32 [H], optional)
+ * dx may be dout itself, dresidual may be dres or h itself (same type and pitch); at least one
+ * output is given.  The sum over tokens takes the workspace, moe_residual_norm_backward_workspace_size(H)
+ * bytes (2 KiB per column, 16-byte aligned; none without dgamma).
+ * Types: (dout, h) = (BF16, BF16), (BF16, F32) or (F32, F32); gamma F32 or BF16.  H <= 16384. */
+typedef struct moe_residual_norm_backward_args {
+  int32_t T, H;
+  const void* dout;        /* [T][dout_pitch] */
+  int32_t dtype;           /* of dout and dx */
+  int64_t dout_pitch;
+  const void* h;           /* [T][h_pitch] */
+  int32_t h_dtype;         /* of h, dres and dresidual */
+  int64_t h_pitch;
+  const void* gamma;       /* [H] */
+  int32_t gamma_dtype;
+  const float* rstd;       /* [T] */
+  const void* dres;        /* [T][dres_pitch], optional */
+  int64_t dres_pitch;
+  void* dx;                /* out [T][dx_pitch], optional */
+  int64_t dx_pitch;
+  void* dresidual;         /* out [T][dresidual_pitch], optional */
+  int64_t dresidual_pitch;
+  float* dgamma;           /* out [H], optional */
+  void* workspace;
+  size_t workspace_bytes;
+} moe_residual_norm_backward_args;
+
+size_t moe_residual_norm_backward_workspace_size(int32_t H);
+int moe_residual_norm_backward(const moe_residual_norm_backward_args* args, hipStream_t stream);
+
 /* ---------------------------------------------------------------------- helpers -- */
 const char* moe_strerror(int status);
 int moe_version(void);
 /* sizeof of the argument structs as compiled into the library (which: 0 assemble,
- * 1 pack, 2 ffn, 3 combine state, 4 combine args), so that bindings can check their
- * own struct layout; 0 for an unknown id. */
+ * 1 pack, 2 ffn, 3 combine state, 4 combine args, 5 route, 6 route backward, 7 sort rows,
+ * 8 merge rows, 9 merge rows backward, 10 residual norm, 11 residual norm backward), so that
+ * bindings can check their own struct layout; 0 for an unknown id. */
 size_t moe_struct_size(int which);
 
 #ifdef __cplusplus
