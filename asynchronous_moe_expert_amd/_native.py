@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -137,13 +138,13 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                        ("moe_combine_plan", [C.POINTER(CombineArgs), _p]),
                        ("moe_combine_apply", [C.POINTER(CombineArgs), _p]),
                        ("moe_combine_release_noalloc", [C.POINTER(CombineArgs), _p]),
-                       ("moe_route", [C.POINTER(RouteArgs), _p]),
-                       ("moe_route_backward", [C.POINTER(RouteBackwardArgs), _p]),
-                       ("moe_sort_rows", [C.POINTER(SortRowsArgs), _p]),
-                       ("moe_merge_rows", [C.POINTER(MergeRowsArgs), _p]),
-                       ("moe_merge_rows_backward", [C.POINTER(MergeRowsBackwardArgs), _p]),
-                       ("moe_residual_norm", [C.POINTER(ResidualNormArgs), _p]),
-                       ("moe_residual_norm_backward", [C.POINTER(ResidualNormBackwardArgs), _p]),
+                       ("moe_route", [_p, _p]),
+                       ("moe_route_backward", [_p, _p]),
+                       ("moe_sort_rows", [_p, _p]),
+                       ("moe_merge_rows", [_p, _p]),
+                       ("moe_merge_rows_backward", [_p, _p]),
+                       ("moe_residual_norm", [_p, _p]),
+                       ("moe_residual_norm_backward", [_p, _p]),
                        ("moe_version", []), ("moe_strerror", [C.c_int])]:
         f = getattr(lib, name)
         f.argtypes = args
@@ -324,44 +325,81 @@ def combine_call(a: CombineArgs, part: str = "release", stream=None) -> None:
 
 # ------------------------------------------------------------------ the home rank's side
 # These calls check their tensors (device, type, shape, stride) before marshalling: a view that
-# the kernels cannot address is refused with a MoeError, and a tensor on another device than the
-# current one is worked on where it is.
+# the kernels cannot address is refused with a MoeError, and tensors on another device than the
+# current one are worked on where they are.  A decode step's calls take the GPU 3-5 us each, so
+# the host path is kept short: the argument struct is packed as bytes in the struct's own layout
+# (0.4 us; a ctypes.Structure takes four times as long to fill), the checks test for what is right
+# first, and the current stream's handle is read directly (0.1 us; a torch.cuda.Stream object
+# 1.9 us).  moe_residual_norm of 64 rows: 9.7 us a call before, 3.0 us of them the launch itself.
 
-_ROWS = (torch.float32, torch.bfloat16)
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_ROWS = (_F32, _BF16)
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
-_INT = (torch.int32,)
-_FLT = (torch.float32,)
-_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4M3,
-         torch.float8_e4m3fn: MOE_FP8_E4M3}
+_ROWS8 = _ROWS + _FP8
+_CODE = {_F32: MOE_F32, _BF16: MOE_BF16, torch.uint8: MOE_FP8_E4M3, torch.float8_e4m3fn: MOE_FP8_E4M3}
+
+
+def _packer(cls) -> struct.Struct:
+    """Packs the fields of an argument struct in its native layout."""
+    chars = {_i32: "i", _i64: "q", _p: "P", C.c_size_t: "N", C.c_float: "f"}
+    s = struct.Struct("@" + "".join(chars[t] for _, t in cls._fields_) + "0P")
+    if s.size != C.sizeof(cls):
+        raise MoeError(f"packed layout of {cls.__name__}: {s.size} bytes, {C.sizeof(cls)} expected")
+    return s
+
+
+_HOME = {"moe_route": _packer(RouteArgs), "moe_route_backward": _packer(RouteBackwardArgs),
+         "moe_sort_rows": _packer(SortRowsArgs), "moe_merge_rows": _packer(MergeRowsArgs),
+         "moe_merge_rows_backward": _packer(MergeRowsBackwardArgs), "moe_residual_norm": _packer(ResidualNormArgs),
+         "moe_residual_norm_backward": _packer(ResidualNormBackwardArgs)}
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _mat(what: str, t, rows: int, cols: int, types) -> int:
     """A [rows][cols] device tensor of one of `types` whose rows are contiguous; its pitch."""
     if t.dtype not in types:
         raise MoeError(f"{what}: unsupported dtype {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise MoeError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
     s0, s1 = t.stride()
+    if s1 == 1 and s0 >= cols and rows > 1:
+        return s0
     if s1 != 1 and cols > 1:
         raise MoeError(f"{what}: the elements of a row must be contiguous")
-    if rows <= 1:
-        return cols
-    if s0 < cols:
+    if rows > 1 and s0 < cols:
         raise MoeError(f"{what}: rows overlap (stride {s0} for {cols} elements)")
-    return s0
+    return s0 if rows > 1 else cols
+
+
+def _vec(what: str, t, n: int, *types) -> int:
+    """A contiguous device tensor of one of `types` with at least n elements; its address, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype not in types:
+        raise MoeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.numel() < n:
+        raise MoeError(f"{what}: {t.numel()} elements, at least {n} expected")
+    if not t.is_contiguous():
+        raise MoeError(f"{what}: must be contiguous")
+    return t.data_ptr()
+
+
+def _each(what: str, t, T: int, K: int, dtype) -> int:
+    """A contiguous device tensor of shape (T, K); its address."""
+    if t.dtype is not dtype or t.shape != (T, K) or not t.is_contiguous():
+        _mat(what, t, T, K, (dtype,))
+        _vec(what, t, T * K, dtype)
+    return t.data_ptr()
 
 
 def _shape(what: str, t) -> tuple[int, int]:
-    if t.dim() != 2:
-        raise MoeError(f"{what}: {t.dim()} dimensions, 2 expected")
-    return t.shape
-
-
-def _int32(name: str, *values) -> None:
-    """Sizes that the argument struct holds in 32 bits (ctypes would cut them silently)."""
-    for v in values:
-        if not -(1 << 31) <= v < 1 << 31:
-            raise MoeError(f"{name}: a size of {v} is over the documented limits")
+    s = t.shape
+    if len(s) != 2:
+        raise MoeError(f"{what}: {len(s)} dimensions, 2 expected")
+    return s
 
 
 def _room(workspace) -> int:
@@ -372,46 +410,40 @@ def _room(workspace) -> int:
     return workspace.numel() * workspace.element_size()
 
 
-def _vec(what: str, t, n: int, types) -> None:
-    """A contiguous device tensor of one of `types` with at least n elements."""
-    if t.dtype not in types:
-        raise MoeError(f"{what}: unsupported dtype {t.dtype}")
-    if t.numel() < n:
-        raise MoeError(f"{what}: {t.numel()} elements, at least {n} expected")
-    if not t.is_contiguous():
-        raise MoeError(f"{what}: must be contiguous")
-
-
-def _home_call(name: str, args, tensors, stream) -> None:
+def _home_call(name: str, values, tensors, stream) -> None:
     """One call of the library on the device that its tensors are on.  With a stream other than
     the current one, the tensors are recorded on it, so that the allocator keeps them until the
     call's work is done."""
-    dev = None
+    try:
+        args = _HOME[name].pack(*values)
+    except (struct.error, OverflowError, TypeError) as e:
+        raise MoeError(f"{name}: an argument is over the documented limits ({e})") from None
+    at = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
-                raise MoeError(f"{name}: tensors must be on a GPU, got {dev}")
-        elif t.device != dev:
-            raise MoeError(f"{name}: tensors on {dev} and {t.device}")
-    current = torch.cuda.current_stream(dev).cuda_stream
-    handle = current if stream is None else _stream(stream)
-    if stream is not None and getattr(stream, "device", dev) != dev:
-        raise MoeError(f"{name}: a stream of {stream.device} for tensors on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        _check(getattr(_lib or load(), name)(C.byref(args), handle), name)
+        if t is not None and t.get_device() != at:
+            raise MoeError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    if at < 0:
+        raise MoeError(f"{name}: tensors must be on a GPU, got {tensors[0].device}")
+    fn = getattr(_lib or load(), name)
+    handle = current = _raw_stream(at)
+    if stream is not None:
+        where = getattr(stream, "device", None)
+        if where is not None and where.index != at:
+            raise MoeError(f"{name}: a stream of {where} for tensors on {tensors[0].device}")
+        handle = _stream(stream)
+    if _device() == at:
+        rc = fn(args, handle)
     else:
-        with torch.cuda.device(dev):
-            _check(getattr(_lib or load(), name)(C.byref(args), handle), name)
+        with torch.cuda.device(at):
+            rc = fn(args, handle)
+    if rc != 0:
+        _check(rc, name)
     if handle != current:
-        s = stream
         if not hasattr(stream, "cuda_stream"):
-            s = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+            stream = torch.cuda.ExternalStream(handle, device=at) if handle else torch.cuda.default_stream(at)
         for t in tensors:
             if t is not None:
-                t.record_stream(s)
+                t.record_stream(stream)
 
 
 def _score(score, renorm) -> tuple[int, int]:
@@ -423,37 +455,27 @@ def _score(score, renorm) -> tuple[int, int]:
 def moe_route(logits, expert, w, bias=None, score: int = MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
               stream=None) -> None:
     """logits [T][E] (f32 or bf16); out: expert [T][K] int32, w [T][K] f32."""
-    (T, E), K = _shape("logits", logits), _shape("expert", expert)[1]
-    _int32("moe_route", T, E, K)
+    T, E = _shape("logits", logits)
+    K = _shape("expert", expert)[1]
     pitch = _mat("logits", logits, T, E, _ROWS)
-    _mat("expert", expert, T, K, _INT)
-    _mat("w", w, T, K, _FLT)
-    _vec("expert", expert, T * K, _INT)
-    _vec("w", w, T * K, _FLT)
-    if bias is not None:
-        _vec("bias", bias, E, _FLT)
     score, renorm = _score(score, renorm)
-    a = RouteArgs(T, E, K, _ptr(logits), _CODE[logits.dtype], pitch, _ptr(bias), score, renorm, scale, _ptr(expert),
-                  _ptr(w))
-    _home_call("moe_route", a, (logits, expert, w, bias), stream)
+    _home_call("moe_route", (T, E, K, logits.data_ptr(), _CODE[logits.dtype], pitch, _vec("bias", bias, E, _F32), score,
+                             renorm, scale, _each("expert", expert, T, K, _I32), _each("w", w, T, K, _F32)),
+               (logits, expert, w, bias), stream)
 
 
 def moe_route_backward(logits, expert, dw, dlogits, err, score: int = MOE_SOFTMAX, renorm: bool = True,
                        scale: float = 1.0, stream=None) -> None:
     """expert [T][K] as moe_route gave it, dw [T][K] f32; out: dlogits [T][E] of the logits' type."""
-    (T, E), K = _shape("logits", logits), _shape("expert", expert)[1]
-    _int32("moe_route_backward", T, E, K)
+    T, E = _shape("logits", logits)
+    K = _shape("expert", expert)[1]
     pitch = _mat("logits", logits, T, E, _ROWS)
-    _mat("expert", expert, T, K, _INT)
-    _mat("dw", dw, T, K, _FLT)
-    _vec("expert", expert, T * K, _INT)
-    _vec("dw", dw, T * K, _FLT)
     dpitch = _mat("dlogits", dlogits, T, E, (logits.dtype,))
-    _vec("err", err, 1, _INT)
     score, renorm = _score(score, renorm)
-    a = RouteBackwardArgs(T, E, K, _ptr(logits), _CODE[logits.dtype], pitch, _ptr(expert), _ptr(dw), score, renorm,
-                          scale, _ptr(dlogits), dpitch, _ptr(err))
-    _home_call("moe_route_backward", a, (logits, expert, dw, dlogits, err), stream)
+    _home_call("moe_route_backward",
+               (T, E, K, logits.data_ptr(), _CODE[logits.dtype], pitch, _each("expert", expert, T, K, _I32),
+                _each("dw", dw, T, K, _F32), score, renorm, scale, dlogits.data_ptr(), dpitch,
+                _vec("err", err, 1, _I32)), (logits, expert, dw, dlogits, err), stream)
 
 
 def moe_sort_rows_workspace_size(n_max: int) -> int:
@@ -473,85 +495,72 @@ def moe_sort_rows(expert, E_loc: int, x, xs, perm, pos, counts, offsets, err, wo
     are optional."""
     T, K = _shape("expert", expert)
     n = T * K
-    _vec("expert", expert, n, _INT)
-    H, code, xp, xsp = 8, MOE_BF16, 8, 8
+    H, code, xp, xsp, xd, xsd, sd = 8, MOE_BF16, 8, 8, 0, 0, 0
     if xs is not None:
         if x is None:
             raise MoeError("x: required with xs")
         H = _shape("xs", xs)[1]
-        xp = _mat("x", x, T, H, _ROWS + _FP8)
+        xp = _mat("x", x, T, H, _ROWS8)
         code = _CODE[x.dtype]
-        xsp = _mat("xs", xs, n, H, (torch.bfloat16,) if code == MOE_FP8_E4M3 else (x.dtype,))
+        xsp = _mat("xs", xs, n, H, (_BF16,) if code == MOE_FP8_E4M3 else (x.dtype,))
+        xd, xsd = x.data_ptr(), xs.data_ptr()
         if code == MOE_FP8_E4M3:
             if x_scale is None:
                 raise MoeError("x_scale: required for fp8 rows")
-            _vec("x_scale", x_scale, T * _groups(H, group), _FLT)
+            sd = _vec("x_scale", x_scale, T * _groups(H, group), _F32)
+        else:
+            x_scale = None
     else:
         x = x_scale = None
-    for what, t, m in (("perm", perm, n), ("row_slot", row_slot, n)):
-        if t is not None:
-            _vec(what, t, m, _INT)
-    _int32("moe_sort_rows", T, K, H, n, E_loc, expert_base)
-    _vec("pos", pos, n, _INT)
-    _vec("counts", counts, E_loc, _INT)
-    _vec("offsets", offsets, E_loc + 1, _INT)
-    _vec("err", err, 1, _INT)
-    a = SortRowsArgs(T, K, H, expert_base, E_loc, _ptr(expert), _ptr(x), code, xp, _ptr(x_scale), group, _ptr(xs),
-                     xsp, _ptr(perm), _ptr(pos), _ptr(counts), _ptr(offsets), _ptr(row_slot), _ptr(err),
-                     _ptr(workspace), _room(workspace))
-    _home_call("moe_sort_rows", a, (expert, x, xs, perm, pos, counts, offsets, err, workspace, row_slot, x_scale),
-               stream)
+    _home_call("moe_sort_rows",
+               (T, K, H, expert_base, E_loc, _each("expert", expert, T, K, _I32), xd, code, xp, sd, group, xsd, xsp,
+                _vec("perm", perm, n, _I32), _vec("pos", pos, n, _I32), _vec("counts", counts, E_loc, _I32),
+                _vec("offsets", offsets, E_loc + 1, _I32), _vec("row_slot", row_slot, n, _I32),
+                _vec("err", err, 1, _I32), 0 if workspace is None else workspace.data_ptr(), _room(workspace)),
+               (expert, x, xs, perm, pos, counts, offsets, err, workspace, row_slot, x_scale), stream)
 
 
-def _positions(pos, w, T: int) -> int:
-    """pos: int32, T x K elements in token order ([T][K] or flat); K."""
-    K = pos.numel() // T if T else (pos.shape[-1] if pos.dim() > 1 else 1)
-    if pos.numel() != T * K:
-        raise MoeError(f"pos: {pos.numel()} elements are not a whole number for each of {T} tokens")
-    _vec("pos", pos, T * K, _INT)
-    if w is not None:
-        _vec("w", w, T * K, _FLT)
-        if w.numel() != T * K:
-            raise MoeError(f"w: {w.numel()} elements, {T * K} expected")
-    return K
+def _positions(pos, w, T: int) -> tuple[int, int, int]:
+    """pos: int32, T x K elements in token order ([T][K] or flat), w f32 like it or None; K and their
+    addresses."""
+    n = pos.numel()
+    K = n // T if T else (pos.shape[-1] if pos.dim() > 1 else 1)
+    if n != T * K:
+        raise MoeError(f"pos: {n} elements are not a whole number for each of {T} tokens")
+    if w is not None and w.numel() != n:
+        raise MoeError(f"w: {w.numel()} elements, {n} expected")
+    return K, _vec("pos", pos, n, _I32), _vec("w", w, n, _F32)
 
 
 def moe_merge_rows(rows, pos, w, out, err, stream=None) -> None:
     """rows [n_rows][H]; pos (int32) and w (f32, or None: 1) [T][K]; out [T][H].  f32 or bf16 each.
     With the gradient of moe_sort_rows' xs as rows and w None, out is the gradient of its x."""
     T, H = _shape("out", out)
-    K = _positions(pos, w, T)
-    _int32("moe_merge_rows", T, H, K)
+    K, posd, wd = _positions(pos, w, T)
     n_rows = _shape("rows", rows)[0]
     rp = _mat("rows", rows, n_rows, H, _ROWS)
     op = _mat("out", out, T, H, _ROWS)
-    _vec("err", err, 1, _INT)
-    a = MergeRowsArgs(T, K, H, _ptr(rows), _CODE[rows.dtype], rp, n_rows, _ptr(pos), _ptr(w), _ptr(out),
-                      _CODE[out.dtype], op, _ptr(err))
-    _home_call("moe_merge_rows", a, (rows, pos, w, out, err), stream)
+    _home_call("moe_merge_rows", (T, K, H, rows.data_ptr(), _CODE[rows.dtype], rp, n_rows, posd, wd, out.data_ptr(),
+                                  _CODE[out.dtype], op, _vec("err", err, 1, _I32)), (rows, pos, w, out, err), stream)
 
 
 def moe_merge_rows_backward(dout, rows, pos, w, drows, dw, err, stream=None) -> None:
     """dout [T][H]; rows and drows [n_rows][H] of one type; pos, w and dw [T][K].  drows or dw (and
     then rows) may be None."""
     T, H = _shape("dout", dout)
-    K = _positions(pos, w, T)
-    _int32("moe_merge_rows_backward", T, H, K)
+    K, posd, wd = _positions(pos, w, T)
     dp = _mat("dout", dout, T, H, _ROWS)
     one = rows if rows is not None else drows
     if one is None or (drows is None and dw is None) or (dw is not None and rows is None):
         raise MoeError("moe_merge_rows_backward: drows, or dw with rows, must be given")
-    n_rows, rp, drp = _shape("rows", one)[0], H, H
+    n_rows, rp, drp, rd, drd = _shape("rows", one)[0], H, H, 0, 0
     if rows is not None:
-        rp = _mat("rows", rows, n_rows, H, _ROWS)
+        rp, rd = _mat("rows", rows, n_rows, H, _ROWS), rows.data_ptr()
     if drows is not None:
-        drp = _mat("drows", drows, n_rows, H, (one.dtype,) if one.dtype in _ROWS else _ROWS)
-    if dw is not None:
-        _vec("dw", dw, T * K, _FLT)
-    _vec("err", err, 1, _INT)
-    a = MergeRowsBackwardArgs(T, K, H, _ptr(dout), _CODE[dout.dtype], dp, _ptr(rows), _CODE[one.dtype], rp, n_rows,
-                              _ptr(pos), _ptr(w), _ptr(drows), drp, _ptr(dw), _ptr(err))
-    _home_call("moe_merge_rows_backward", a, (dout, rows, pos, w, drows, dw, err), stream)
+        drp, drd = _mat("drows", drows, n_rows, H, (rows.dtype,) if rows is not None else _ROWS), drows.data_ptr()
+    _home_call("moe_merge_rows_backward",
+               (T, K, H, dout.data_ptr(), _CODE[dout.dtype], dp, rd, _CODE[one.dtype], rp, n_rows, posd, wd, drd, drp,
+                _vec("dw", dw, T * K, _F32), _vec("err", err, 1, _I32)), (dout, rows, pos, w, drows, dw, err), stream)
 
 
 def moe_residual_norm(x, residual, gamma, eps: float, out, residual_out=None, rstd=None, out_scale=None,
@@ -560,36 +569,28 @@ def moe_residual_norm(x, residual, gamma, eps: float, out, residual_out=None, rs
     f32).  Optional outputs: residual_out [T][H], rstd [T].  row_list [T], row_count [1] (int32): only
     these rows, with err."""
     T, H = _shape("x", x)
-    _int32("moe_residual_norm", T, H)
     xp = _mat("x", x, T, H, _ROWS)
-    op = _mat("out", out, T, H, _ROWS + _FP8)
-    _vec("gamma", gamma, H, _ROWS)
-    rt, rp, rop = x.dtype, H, H
+    op = _mat("out", out, T, H, _ROWS8)
+    rt, rp, rop, rd, rod, sd = x.dtype, H, H, 0, 0, 0
     if residual is not None:
         rt = residual.dtype
-        rp = _mat("residual", residual, T, H, _ROWS)
+        rp, rd = _mat("residual", residual, T, H, _ROWS), residual.data_ptr()
     if residual_out is not None:
         if residual is None:
             rt = residual_out.dtype
-        rop = _mat("residual_out", residual_out, T, H, (rt,) if rt in _ROWS else _ROWS)
-    if _CODE[out.dtype] == MOE_FP8_E4M3:
+        rop, rod = _mat("residual_out", residual_out, T, H, (rt,) if residual is not None else _ROWS), residual_out.data_ptr()
+    oc = _CODE[out.dtype]
+    if oc == MOE_FP8_E4M3:
         if out_scale is None:
             raise MoeError("out_scale: required for fp8 output")
-        _vec("out_scale", out_scale, T * _groups(H, group), _FLT)
+        sd = _vec("out_scale", out_scale, T * _groups(H, group), _F32)
     else:
         out_scale = None
-    if rstd is not None:
-        _vec("rstd", rstd, T, _FLT)
-    if row_list is not None:
-        _vec("row_list", row_list, T, _INT)
-    for what, t in (("row_count", row_count), ("err", err)):
-        if t is not None:
-            _vec(what, t, 1, _INT)
-    a = ResidualNormArgs(T, H, _ptr(x), _CODE[x.dtype], xp, _ptr(residual), _CODE[rt], rp, _ptr(gamma),
-                         _CODE[gamma.dtype], eps, _ptr(out), _CODE[out.dtype], op, _ptr(out_scale), group,
-                         _ptr(residual_out), rop, _ptr(rstd), _ptr(row_list), _ptr(row_count), _ptr(err))
-    _home_call("moe_residual_norm", a, (x, residual, gamma, out, residual_out, rstd, out_scale, row_list, row_count,
-                                        err), stream)
+    _home_call("moe_residual_norm",
+               (T, H, x.data_ptr(), _CODE[x.dtype], xp, rd, _CODE[rt], rp, _vec("gamma", gamma, H, _F32, _BF16),
+                _CODE[gamma.dtype], eps, out.data_ptr(), oc, op, sd, group, rod, rop, _vec("rstd", rstd, T, _F32),
+                _vec("row_list", row_list, T, _I32), _vec("row_count", row_count, 1, _I32), _vec("err", err, 1, _I32)),
+               (x, residual, gamma, out, residual_out, rstd, out_scale, row_list, row_count, err), stream)
 
 
 def moe_residual_norm_backward_workspace_size(H: int) -> int:
@@ -602,19 +603,13 @@ def moe_residual_norm_backward(dout, h, gamma, rstd, dx, dgamma, workspace, dres
     dresidual [T][H] of h's, dgamma [H] f32 (with the workspace); each may be None.  dres [T][H] of h's
     type is added to dx and dresidual."""
     T, H = _shape("dout", dout)
-    _int32("moe_residual_norm_backward", T, H)
     dp = _mat("dout", dout, T, H, _ROWS)
     hp = _mat("h", h, T, H, _ROWS)
-    _vec("gamma", gamma, H, _ROWS)
-    _vec("rstd", rstd, T, _FLT)
-    p = {"dres": H, "dx": H, "dresidual": H}
+    p = []
     for what, t, like in (("dres", dres, h), ("dx", dx, dout), ("dresidual", dresidual, h)):
-        if t is not None:
-            p[what] = _mat(what, t, T, H, (like.dtype,))
-    if dgamma is not None:
-        _vec("dgamma", dgamma, H, _FLT)
-    a = ResidualNormBackwardArgs(T, H, _ptr(dout), _CODE[dout.dtype], dp, _ptr(h), _CODE[h.dtype], hp, _ptr(gamma),
-                                 _CODE[gamma.dtype], _ptr(rstd), _ptr(dres), p["dres"], _ptr(dx), p["dx"],
-                                 _ptr(dresidual), p["dresidual"], _ptr(dgamma), _ptr(workspace),
-                                 _room(workspace))
-    _home_call("moe_residual_norm_backward", a, (dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual), stream)
+        p += (0, H) if t is None else (t.data_ptr(), _mat(what, t, T, H, (like.dtype,)))
+    _home_call("moe_residual_norm_backward",
+               (T, H, dout.data_ptr(), _CODE[dout.dtype], dp, h.data_ptr(), _CODE[h.dtype], hp,
+                _vec("gamma", gamma, H, _F32, _BF16), _CODE[gamma.dtype], _vec("rstd", rstd, T, _F32), *p,
+                _vec("dgamma", dgamma, H, _F32), 0 if workspace is None else workspace.data_ptr(), _room(workspace)),
+               (dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual), stream)

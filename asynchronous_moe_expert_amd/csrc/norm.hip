@@ -8,8 +8,8 @@
 
 namespace moe {
 
-constexpr int kNormT = 256, kNormWaves = kNormT / kWave;
-constexpr int kNormH = 16384;     // longest row: 256 threads x 8 chunks of 8
+constexpr int kNormT = 512, kNormWaves = kNormT / kWave;  // at most
+constexpr int kNormH = 16384;     // longest row: 512 threads x 4 chunks of 8
 constexpr int kPartials = 512;    // rows of the workspace that the sum over tokens goes through
 
 struct NormJob {
@@ -40,18 +40,26 @@ __device__ __forceinline__ void gamma8(const void* gamma, int f32, int64_t at, f
   }
 }
 
-// the workgroup's sum / maximum in every thread; s[] is free again after the next barrier
+// The workgroup's sum / maximum in every thread; s[] is free again after the next barrier.
 __device__ __forceinline__ float group_sum(float v, float* s) {
   v = wave_sum(v);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  float all = s[0];
+  for (int w = 1; w < waves; ++w) all += s[w];
+  return all;
 }
 __device__ __forceinline__ float group_max(float v, float* s) {
   v = wave_max(v);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+  float all = s[0];
+  for (int w = 1; w < waves; ++w) all = fmaxf(all, s[w]);
+  return all;
 }
 
 // the maximum over aligned runs of 4, 8 or 16 lanes
@@ -64,6 +72,13 @@ __device__ __forceinline__ float run_max(float v, int lanes) {
 }
 
 __device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax / 448.f, FLT_MIN) : 1.f; }
+
+// v / s through s's reciprocal and one correction, so that a code next to a border falls where the
+// quotient's own rounding puts it (the product alone moved 1.5 times as many codes)
+__device__ __forceinline__ float over(float v, float s, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, s, v), inv, q);
+}
 
 // A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + 256, ...
 template <int XT, int RT, int OT, int C>
@@ -84,7 +99,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
     float h[C][8], ss = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
       if (at < j.H) {
@@ -109,7 +124,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (at < j.H) {
         if (j.residual_out) st8<RT>((char*)j.residual_out + row_bytes<RT>(t, j.res_out_pitch), at, h[c]);
         float g[8];
@@ -128,7 +143,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
           if (at < j.H) {
             const float inv = 1.f / s;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] *= inv;
+            for (int e = 0; e < 8; ++e) h[c][e] = over(h[c][e], s, inv);
             st8<OT>(out, at, h[c]);
             const int lane = threadIdx.x & (j.group_lanes - 1);
             if (lane == 0) j.out_scale[(int64_t)t * j.groups + at / (j.group_lanes * 8)] = s;
@@ -141,10 +156,10 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
         const float s = scale_of(group_max(amax, s_b[par])), inv = 1.f / s;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const int at = (c * kNormT + (int)threadIdx.x) * 8;
+          const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
           if (at < j.H) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] *= inv;
+            for (int e = 0; e < 8; ++e) h[c][e] = over(h[c][e], s, inv);
             st8<OT>(out, at, h[c]);
           }
         }
@@ -171,28 +186,43 @@ template <int DT, int HT, int C>
 __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   __shared__ float s_a[2][kNormWaves];
   float dg[C][8];
+  Chunk<DT> nd[C];  // the next row on its way
+  Chunk<HT> nh[C], ns[C];
+  float nr = 0.f;
+  auto fetch = [&](int t) {
+    const char* dout = (const char*)j.dout + row_bytes<DT>(t, j.dout_pitch);
+    const char* hr = (const char*)j.h + row_bytes<HT>(t, j.h_pitch);
+    const char* dres = (const char*)j.dres + row_bytes<HT>(t, j.dres_pitch);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
+      if (at < j.H) {
+        nd[c].load(dout, at);
+        nh[c].load(hr, at);
+        if (j.dres) ns[c].load(dres, at);
+      }
+    }
+    nr = j.rstd[t];
+  };
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[c][e] = 0.f;
   int par = 0;
+  fetch(blockIdx.x);
   for (int t = blockIdx.x; t < j.T; t += gridDim.x, par ^= 1) {
-    const char* dout = (const char*)j.dout + row_bytes<DT>(t, j.dout_pitch);
-    const char* hr = (const char*)j.h + row_bytes<HT>(t, j.h_pitch);
-    const float r = j.rstd[t];
+    const float r = nr;
     float xh[C][8], g[C][8], dot = 0.f;
+    Chunk<HT> ds[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) xh[c][e] = g[c][e] = 0.f;
       if (at < j.H) {
-        Chunk<DT> q;
-        q.load(dout, at);
-        q.get(g[c]);
-        Chunk<HT> p;
-        p.load(hr, at);
-        p.get(xh[c]);
+        nd[c].get(g[c]);
+        nh[c].get(xh[c]);
+        ds[c] = ns[c];
         float gm[8];
         gamma8(j.gamma, j.gamma_f32, at, gm);
 #pragma unroll
@@ -204,19 +234,18 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
         }
       }
     }
+    if (t + (int)gridDim.x < j.T) fetch(t + gridDim.x);
     const float mean = group_sum(dot, s_a[par]) / (float)j.H;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (at < j.H) {
         float d[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] = r * (g[c][e] - xh[c][e] * mean);
         if (j.dres) {
-          Chunk<HT> p;
-          p.load((const char*)j.dres + row_bytes<HT>(t, j.dres_pitch), at);
           float f[8];
-          p.get(f);
+          ds[c].get(f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) d[e] += f[e];
         }
@@ -228,28 +257,40 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   if (j.part) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * kNormT + (int)threadIdx.x) * 8;
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (at < j.H) st8<MOE_F32>(j.part + (int64_t)blockIdx.x * j.H, at, dg[c]);
     }
   }
 }
 
-// dgamma[col] = sum of the partial rows: 16 columns per workgroup, the rows in 16 runs
-__global__ __launch_bounds__(kNormT) void norm_dgamma_kernel(const float* __restrict__ part, int rows, int H,
-                                                             float* __restrict__ dgamma) {
-  __shared__ float s[16][17];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, col = blockIdx.x * 16 + cx;
-  float sum = 0.f;
-  if (col < H)
-    for (int r = ry; r < rows; r += 16) sum += part[(int64_t)r * H + col];
-  s[ry][cx] = sum;
-  __syncthreads();
-  if (ry == 0 && col < H) {
-    float all = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) all += s[k][cx];
-    dgamma[col] = all;
+// dgamma[col] = sum of the partial rows: 64 columns per workgroup, four to a thread, the rows dealt
+// to 64 groups of threads.
+__global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* __restrict__ part, int rows, int H,
+                                                           float* __restrict__ dgamma) {
+  __shared__ float s[64][65];
+  const int cx = (threadIdx.x & 15) * 4, ry = threadIdx.x >> 4, col = blockIdx.x * 64 + cx;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  if (col < H) {
+#pragma unroll 8
+    for (int r = ry; r < rows; r += 64) sum += *reinterpret_cast<const f32x4*>(part + (int64_t)r * H + col);
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s[ry][cx + k] = sum[k];
+  __syncthreads();
+  const int c = threadIdx.x >> 4, l = threadIdx.x & 15;  // 16 lanes add a column's 64 groups
+  const float all = sum16((s[l][c] + s[l + 16][c]) + (s[l + 32][c] + s[l + 48][c]));
+  if (l == 0 && blockIdx.x * 64 + c < H) dgamma[blockIdx.x * 64 + c] = all;
+}
+
+// Threads for a row of H and the chunks that each holds (1, 2 or 4): the fewest passes of at most
+// 512 lanes, the lanes spread evenly.
+struct RowShape {
+  unsigned threads;
+  int chunks;
+};
+static RowShape row_shape(int H) {
+  const int chunks = H / 8, c = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4, per = (chunks + c - 1) / c;
+  return {(unsigned)((per + 63) / 64 * 64), c};
 }
 
 static bool norm_pitch_ok(int64_t pitch, int32_t H) { return pitch >= H && pitch <= ((int64_t)1 << 32); }
@@ -259,11 +300,11 @@ static bool norm_types_ok(int a, int b) {
 
 template <int XT, int RT, int OT>
 static int norm_by_width(const NormJob& j, hipStream_t stream) {
+  const RowShape r = row_shape(j.H);
   const unsigned grid = grid_of(j.T);
-  if (j.H <= 2048) return launch(norm_kernel<XT, RT, OT, 1>, grid, kNormT, stream, j);
-  if (j.H <= 4096) return launch(norm_kernel<XT, RT, OT, 2>, grid, kNormT, stream, j);
-  if (j.H <= 8192) return launch(norm_kernel<XT, RT, OT, 4>, grid, kNormT, stream, j);
-  return launch(norm_kernel<XT, RT, OT, 8>, grid, kNormT, stream, j);
+  if (r.chunks == 1) return launch(norm_kernel<XT, RT, OT, 1>, grid, r.threads, stream, j);
+  if (r.chunks == 2) return launch(norm_kernel<XT, RT, OT, 2>, grid, r.threads, stream, j);
+  return launch(norm_kernel<XT, RT, OT, 4>, grid, r.threads, stream, j);
 }
 
 template <int XT, int RT>
@@ -275,10 +316,10 @@ static int norm_by_out(const NormJob& j, int out, hipStream_t stream) {
 
 template <int DT, int HT>
 static int norm_backward_by_width(const NormBackJob& j, unsigned grid, hipStream_t stream) {
-  if (j.H <= 2048) return launch(norm_backward_kernel<DT, HT, 1>, grid, kNormT, stream, j);
-  if (j.H <= 4096) return launch(norm_backward_kernel<DT, HT, 2>, grid, kNormT, stream, j);
-  if (j.H <= 8192) return launch(norm_backward_kernel<DT, HT, 4>, grid, kNormT, stream, j);
-  return launch(norm_backward_kernel<DT, HT, 8>, grid, kNormT, stream, j);
+  const RowShape r = row_shape(j.H);
+  if (r.chunks == 1) return launch(norm_backward_kernel<DT, HT, 1>, grid, r.threads, stream, j);
+  if (r.chunks == 2) return launch(norm_backward_kernel<DT, HT, 2>, grid, r.threads, stream, j);
+  return launch(norm_backward_kernel<DT, HT, 4>, grid, r.threads, stream, j);
 }
 
 }  // namespace moe
@@ -363,6 +404,6 @@ extern "C" int moe_residual_norm_backward(const moe_residual_norm_backward_args*
     if (rc != MOE_OK) return rc;
   }
   if (!a->dgamma) return MOE_OK;
-  return launch(norm_dgamma_kernel, (unsigned)((a->H + 15) / 16), kNormT, stream, (const float*)a->workspace, (int)grid,
+  return launch(norm_dgamma_kernel, (unsigned)((a->H + 63) / 64), 1024, stream, (const float*)a->workspace, (int)grid,
                 a->H, a->dgamma);
 }

@@ -4,6 +4,18 @@
 
 namespace moe {
 
+__device__ __forceinline__ int lane_i32(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+// A value that lane_i32 / lane_f32 reads inside a branch or loop that some lanes do not enter: it is
+// computed here, by every lane, and not moved into the branch.
+__device__ __forceinline__ int all_lanes(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ float all_lanes(float v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 constexpr int kMaxEloc = 256, kMaxK = 32;
 constexpr int kNone = kMaxEloc;  // key of a pair without a row
 
@@ -159,6 +171,13 @@ __global__ void sort_empty_kernel(SortJob j) {
 }
 
 // -------------------------------------------------------------------------- copying rows
+// Threads of a workgroup that takes a row: the fewest passes of at most 512 lanes over its chunks,
+// the lanes spread evenly over them.
+static unsigned row_threads(int chunks) {
+  const int passes = (chunks + 511) / 512, per = (chunks + passes - 1) / passes;
+  return (unsigned)((per + 63) / 64 * 64);
+}
+
 struct CopyJob {
   int K, H, chunks;  // chunks of eight elements in a row
   int group_shift;   // fp8: log2 of the columns per scale, -1 for one per row
@@ -175,43 +194,138 @@ struct SortedType {
   static constexpr int out = DT == MOE_FP8_E4M3 ? MOE_BF16 : DT;
 };
 
-// One chunk of token t's row to its rows p[0 .. K): read once, written K times.
+// A chunk of token t's row on its way: read once, written to the token's K rows.
 template <int DT>
-__device__ __forceinline__ void copy_chunk(const CopyJob& c, int t, int ch, const int* p) {
-  constexpr int OUT = SortedType<DT>::out;
-  constexpr int esz = DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1;
-  const char* row = (const char*)c.x + (int64_t)t * c.x_pitch * esz;
+struct Carried {
+  static constexpr int esz = DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1;
+  static constexpr int OUT = SortedType<DT>::out, osz = OUT == MOE_F32 ? 4 : 2;
   Chunk<DT> q;
-  q.load(row, (int64_t)ch * 8);
-  float f[8];
-  q.get(f);
-  if constexpr (DT == MOE_FP8_E4M3) {
-    const int g = c.group_shift < 0 ? 0 : (ch * 8) >> c.group_shift;
-    const float s = c.x_scale[(int64_t)t * c.groups + g];
+  float s;
+  __device__ __forceinline__ void load(const CopyJob& c, int t, int ch) {
+    q.load((const char*)c.x + (int64_t)t * c.x_pitch * esz, (int64_t)ch * 8);
+    if constexpr (DT == MOE_FP8_E4M3)
+      s = c.x_scale[(int64_t)t * c.groups + (c.group_shift < 0 ? 0 : (ch * 8) >> c.group_shift)];
+  }
+  // position k's row in lane k of p
+  __device__ __forceinline__ void store(const CopyJob& c, int ch, int p) const {
+    float f[8];
+    q.get(f);
+    if constexpr (DT == MOE_FP8_E4M3) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] *= s;
+      for (int k = 0; k < 8; ++k) f[k] *= s;
+    }
+    for (int k = 0; k < c.K; ++k) {
+      const int r = lane_i32(p, k);
+      if (r < 0) continue;
+      char* dst = (char*)c.xs + (int64_t)r * c.xs_pitch * osz;
+      if constexpr (DT == MOE_BF16)
+        *reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8) = q.r;
+      else
+        st8<OUT>(dst, (int64_t)ch * 8, f);
+    }
   }
-  constexpr int osz = OUT == MOE_F32 ? 4 : 2;
-  for (int k = 0; k < c.K; ++k) {
-    const int r = p[k];
-    if (r < 0) continue;
-    char* dst = (char*)c.xs + (int64_t)r * c.xs_pitch * osz;
-    if constexpr (DT == MOE_BF16)
-      *reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8) = q.r;
-    else
-      st8<OUT>(dst, (int64_t)ch * 8, f);
-  }
-}
+};
 
 // A workgroup per token (blockIdx, blockIdx + gridDim, ...).
 template <int DT>
-__global__ __launch_bounds__(256) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
-  __shared__ int s_pos[kMaxK];
+__global__ __launch_bounds__(512) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
+  const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    if (threadIdx.x < c.K) s_pos[threadIdx.x] = pos[(int64_t)t * c.K + threadIdx.x];
+    const int p = all_lanes(lane < c.K ? pos[(int64_t)t * c.K + lane] : -1);
+    for (int ch = threadIdx.x; ch < c.chunks; ch += blockDim.x) {
+      Carried<DT> x;
+      x.load(c, t, ch);
+      x.store(c, ch, p);
+    }
+  }
+}
+
+// Short queues: index and copy in one launch.  A pair's row is the number of pairs with a lower
+// (key, pair), so each token's workgroup stages all n pairs' (key, pair) in LDS, counts those below
+// each of its own K pairs (a wave takes the positions wave, wave + waves, ...) and then copies its
+// row, whose first chunks are loaded meanwhile; the last workgroup writes counts, offsets and what
+// lies past the last row.  No workgroup waits for another.  The count is n T K / 64 wave steps in
+// all, which is why longer queues go through the index launches.
+constexpr int kShort = 4096;
+
+template <int DT>
+__global__ __launch_bounds__(512) void sort_short_kernel(SortJob j, CopyJob c) {
+  __shared__ __attribute__((aligned(16))) uint32_t s_all[kShort];
+  __shared__ int s_pos[kMaxK];
+  __shared__ int s_cnt[kMaxEloc + 1];
+  const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  unsigned bad = 0;
+  if ((int)blockIdx.x < j.T) {
+    const int t = blockIdx.x;
+    Carried<DT> first;
+    if (tid < c.chunks) first.load(c, t, tid);
+    const int padded = (j.n + 255) & ~255;
+    for (int q = tid; q < padded; q += blockDim.x)
+      s_all[q] = q < j.n ? (uint32_t)sort_key(j, q, bad) << 16 | (uint32_t)q : ~0u;
     __syncthreads();
-    for (int ch = threadIdx.x; ch < c.chunks; ch += 256) copy_chunk<DT>(c, t, ch, s_pos);
+    for (int k = wv; k < j.K; k += waves) {
+      const int i = t * j.K + k;
+      const uint32_t mine = s_all[i];
+      int before = 0;
+      for (int q = lane * 4; q < padded; q += 256) {
+        const u32x4 o = *reinterpret_cast<const u32x4*>(&s_all[q]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) before += o[u] < mine;
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+      const int r = (mine >> 16) < kNone ? before : -1;
+      if (lane == 0) {
+        s_pos[k] = r;
+        j.pos[i] = r;
+        if (r >= 0 && j.perm) j.perm[r] = i;
+        if (r >= 0 && j.row_slot) j.row_slot[r] = t;
+      }
+    }
     __syncthreads();
+    const int p = all_lanes(lane < j.K ? s_pos[lane] : -1);
+    if (tid < c.chunks) first.store(c, tid, p);
+    for (int ch = tid + blockDim.x; ch < c.chunks; ch += blockDim.x) {
+      Carried<DT> x;
+      x.load(c, t, ch);
+      x.store(c, ch, p);
+    }
+    return;
+  }
+  for (int e = tid; e <= kMaxEloc; e += blockDim.x) s_cnt[e] = 0;
+  __syncthreads();
+  for (int q = tid; q < j.n; q += blockDim.x) atomicAdd(&s_cnt[sort_key(j, q, bad)], 1);
+  if (bad) atomicOr(j.err, bad);
+  __syncthreads();
+  if (wv != 0) return;
+  int v[4], sum = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[k] = s_cnt[lane * 4 + k];
+    sum += v[k];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(incl, d);
+    if (lane >= d) incl += u;
+  }
+  int run = incl - sum;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int e = lane * 4 + k;
+    if (e < j.E_loc) {
+      j.counts[e] = v[k];
+      j.offsets[e] = run;
+    }
+    run += v[k];
+  }
+  const int total = lane_i32(incl, 63);
+  if (lane == 0) j.offsets[j.E_loc] = total;
+  for (int r = total + lane; r < j.n; r += 64) {
+    if (j.perm) j.perm[r] = -1;
+    if (j.row_slot) j.row_slot[r] = -1;
   }
 }
 
@@ -232,38 +346,55 @@ __device__ __forceinline__ const char* row_at(const void* rows, int64_t r, int64
   return (const char*)rows + r * pitch * (DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1);
 }
 
-// A workgroup per token; each lane sums its chunks over the positions in order.
-template <int RT, int OT>
-__global__ __launch_bounds__(256) void merge_kernel(MergeJob m) {
-  __shared__ int s_pos[kMaxK];
-  __shared__ float s_w[kMaxK];
+// Position k of token t in lane k: its row or -1, and its weight.
+struct Named {
+  int p;
+  float w;
+};
+__device__ __forceinline__ Named named_rows(const int32_t* pos, const float* w, uint32_t* err, int t, int K,
+                                            int64_t n_rows, int lane) {
+  Named r{-1, 0.f};
+  if (lane < K) {
+    const int64_t at = (int64_t)t * K + lane;
+    const int p = pos[at];
+    if (p >= 0 && p < n_rows) r.p = p;
+    else if (p != -1) atomicOr(err, MOE_ERR_ROW_RANGE);
+    r.w = w ? w[at] : 1.f;
+  }
+  r.p = all_lanes(r.p);
+  r.w = all_lanes(r.w);
+  return r;
+}
+
+// A workgroup per token, KB positions at a time: their loads are all issued before the first is
+// used.  Each lane sums its chunk over the positions in order.
+template <int RT, int OT, int KB>
+__global__ __launch_bounds__(512) void merge_kernel(MergeJob m) {
+  const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x; t < m.T; t += gridDim.x) {
-    if (threadIdx.x < m.K) {
-      const int64_t at = (int64_t)t * m.K + threadIdx.x;
-      int p = m.pos[at];
-      if (p < -1 || p >= m.n_rows) {
-        p = -1;
-        atomicOr(m.err, MOE_ERR_ROW_RANGE);
-      }
-      s_pos[threadIdx.x] = p;
-      s_w[threadIdx.x] = m.w ? m.w[at] : 1.f;
-    }
-    __syncthreads();
+    const Named r = named_rows(m.pos, m.w, m.err, t, m.K, m.n_rows, lane);
     char* out = (char*)m.out + (int64_t)t * m.out_pitch * (OT == MOE_F32 ? 4 : 2);
-    for (int ch = threadIdx.x; ch < m.chunks; ch += 256) {
+    for (int ch = threadIdx.x; ch < m.chunks; ch += blockDim.x) {
       float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int k = 0; k < m.K; ++k) {
-        if (s_pos[k] < 0) continue;
-        Chunk<RT> q;
-        q.load(row_at<RT>(m.rows, s_pos[k], m.row_pitch), (int64_t)ch * 8);
-        float f[8];
-        q.get(f);
+      for (int k0 = 0; k0 < m.K; k0 += KB) {
+        Chunk<RT> q[KB];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(s_w[k], f[e], acc[e]);
+        for (int k = 0; k < KB; ++k) {
+          const int p = lane_i32(r.p, k0 + k);
+          if (p >= 0) q[k].load(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          if (lane_i32(r.p, k0 + k) < 0) continue;
+          const float w = lane_f32(r.w, k0 + k);
+          float f[8];
+          q[k].get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, f[e], acc[e]);
+        }
       }
       st8<OT>(out, (int64_t)ch * 8, acc);
     }
-    __syncthreads();
   }
 }
 
@@ -281,53 +412,85 @@ struct MergeBackJob {
   uint32_t* err;
 };
 
-// A workgroup per token, one position after the other.
-template <int DT, int RT>
-__global__ __launch_bounds__(256) void merge_backward_kernel(MergeBackJob m) {
-  __shared__ float s_sum[4];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// A workgroup per token, KB positions at a time; a position's dot product runs through the lane's
+// chunks, the wave's lanes and the waves.
+template <int DT, int RT, int KB>
+__global__ __launch_bounds__(512) void merge_backward_kernel(MergeBackJob m) {
+  __shared__ float s_dot[2][8][KB];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  int par = 0;
   for (int t = blockIdx.x; t < m.T; t += gridDim.x) {
     const char* dout = row_at<DT>(m.dout, t, m.dout_pitch);
-    for (int k = 0; k < m.K; ++k) {
-      const int64_t at = (int64_t)t * m.K + k;
-      const int p = m.pos[at];
-      if (p < 0 || p >= m.n_rows) {
-        if (threadIdx.x == 0) {
-          if (p != -1) atomicOr(m.err, MOE_ERR_ROW_RANGE);
-          if (m.dw) m.dw[at] = 0.f;
-        }
-        continue;
-      }
-      const float w = m.w ? m.w[at] : 1.f;
-      float dot = 0.f;
-      for (int ch = threadIdx.x; ch < m.chunks; ch += 256) {
-        Chunk<DT> q;
-        q.load(dout, (int64_t)ch * 8);
-        float g[8];
-        q.get(g);
-        if (m.dw) {
-          Chunk<RT> y;
-          y.load(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
-          float f[8];
-          y.get(f);
+    const Named r = named_rows(m.pos, m.w, m.err, t, m.K, m.n_rows, lane);
+    for (int k0 = 0; k0 < m.K; k0 += KB, par ^= 1) {
+      float dot[KB];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(g[e], f[e], dot);
+      for (int k = 0; k < KB; ++k) dot[k] = 0.f;
+      for (int ch = threadIdx.x; ch < m.chunks; ch += blockDim.x) {
+        Chunk<RT> q[KB];
+        Chunk<DT> d;
+        d.load(dout, (int64_t)ch * 8);
+        if (m.dw) {
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            const int p = lane_i32(r.p, k0 + k);
+            if (p >= 0) q[k].load(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
+          }
         }
+        float g[8];
+        d.get(g);
         if (m.drows) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= w;
-          st8<RT>((char*)m.drows + (int64_t)p * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, g);
+          for (int k = 0; k < KB; ++k) {
+            const int p = lane_i32(r.p, k0 + k);
+            if (p < 0) continue;
+            const float w = lane_f32(r.w, k0 + k);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = g[e] * w;
+            st8<RT>((char*)m.drows + (int64_t)p * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, f);
+          }
+        }
+        if (m.dw) {
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            if (lane_i32(r.p, k0 + k) < 0) continue;
+            float f[8];
+            q[k].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[k] = fmaf(g[e], f[e], dot[k]);
+          }
         }
       }
-      if (m.dw) {
-        dot = wave_sum(dot);
-        if (lane == 0) s_sum[wv] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) m.dw[at] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
-        __syncthreads();
+      if (!m.dw) continue;
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const float s = wave_sum(dot[k]);
+        if (lane == 0) s_dot[par][wv][k] = s;
+      }
+      __syncthreads();
+      if (threadIdx.x < KB && k0 + (int)threadIdx.x < m.K) {
+        float s = 0.f;
+        for (int v = 0; v < waves; ++v) s += s_dot[par][v][threadIdx.x];
+        m.dw[(int64_t)t * m.K + k0 + threadIdx.x] = s;
       }
     }
   }
+}
+
+template <int RT, int OT>
+static int merge_by_k(const MergeJob& m, hipStream_t stream) {
+  const unsigned grid = grid_of(m.T), block = row_threads(m.chunks);
+  if (m.K <= 2) return launch(merge_kernel<RT, OT, 2>, grid, block, stream, m);
+  if (m.K <= 4) return launch(merge_kernel<RT, OT, 4>, grid, block, stream, m);
+  return launch(merge_kernel<RT, OT, 8>, grid, block, stream, m);
+}
+template <int DT, int RT>
+static int merge_backward_by_k(const MergeBackJob& m, hipStream_t stream) {
+  const unsigned grid = grid_of(m.T), block = row_threads(m.chunks);
+  if (m.K <= 2) return launch(merge_backward_kernel<DT, RT, 2>, grid, block, stream, m);
+  if (m.K <= 4) return launch(merge_backward_kernel<DT, RT, 4>, grid, block, stream, m);
+  return launch(merge_backward_kernel<DT, RT, 8>, grid, block, stream, m);
 }
 
 constexpr int64_t kMaxPitch = (int64_t)1 << 32;
@@ -343,7 +506,7 @@ static bool f32_or_bf16(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 using namespace moe;
 
 extern "C" size_t moe_sort_rows_workspace_size(int32_t n_max) {
-  return n_max > 0 ? (size_t)kSegs * kMaxEloc * sizeof(int32_t) : 0;
+  return n_max > kShort ? (size_t)kSegs * kMaxEloc * sizeof(int32_t) : 0;
 }
 
 static int check_sort(const moe_sort_rows_args* a) {
@@ -365,25 +528,45 @@ static int check_sort(const moe_sort_rows_args* a) {
         !aligned_rows(a->xs, a->xs_pitch, dtype_size(out), 16))
       return MOE_EINVAL_ALIGN;
   }
-  if (!a->workspace || a->workspace_bytes < moe_sort_rows_workspace_size(a->T * a->K)) return MOE_EWORKSPACE;
-  if (!aligned16(a->workspace)) return MOE_EINVAL_ALIGN;
+  const size_t need = moe_sort_rows_workspace_size(a->T * a->K);
+  if (need) {
+    if (!a->workspace || a->workspace_bytes < need) return MOE_EWORKSPACE;
+    if (!aligned16(a->workspace)) return MOE_EINVAL_ALIGN;
+  }
   return MOE_OK;
 }
 
-template <int DT>
-static int copy_rows(const moe_sort_rows_args* a, hipStream_t stream) {
+static CopyJob make_copy_job(const moe_sort_rows_args* a) {
   CopyJob c;
-  c.K = a->K; c.H = a->H; c.chunks = a->H / 8;
+  c.K = a->K; c.H = a->H;
+  c.chunks = a->xs ? a->H / 8 : 0;
   c.group_shift = a->group ? __builtin_ctz((unsigned)a->group) : -1;
   c.groups = a->group ? (a->H + a->group - 1) / a->group : 1;
   c.x = a->x; c.x_pitch = a->x_pitch; c.x_scale = a->x_scale;
   c.xs = a->xs; c.xs_pitch = a->xs_pitch;
-  return launch(sort_copy_kernel<DT>, grid_of(a->T), 256, stream, c, a->T, (const int32_t*)a->pos);
+  return c;
+}
+
+template <int DT>
+static int sort_rows(const moe_sort_rows_args* a, const SortJob& j, hipStream_t stream) {
+  const CopyJob c = make_copy_job(a);
+  const unsigned block = c.chunks ? row_threads(c.chunks) : 256;
+  if (j.n <= kShort) {
+    const unsigned b = block < 256 ? 256 : block;
+    return launch(sort_short_kernel<DT>, (unsigned)j.T + 1, b, stream, j, c);
+  }
+  const int per = (j.n + kSegs - 1) / kSegs, seg_len = (per + kIdx - 1) / kIdx * kIdx;
+  const int segs = (j.n + seg_len - 1) / seg_len;
+  int rc = launch(sort_count_kernel, (unsigned)segs, kIdx, stream, j, seg_len, (int32_t*)a->workspace);
+  if (rc == MOE_OK)
+    rc = launch(sort_place_kernel, (unsigned)segs, kIdx, stream, j, segs, seg_len, (const int32_t*)a->workspace);
+  if (rc != MOE_OK || !c.chunks) return rc;
+  return launch(sort_copy_kernel<DT>, grid_of(j.T), block, stream, c, j.T, (const int32_t*)a->pos);
 }
 
 extern "C" int moe_sort_rows(const moe_sort_rows_args* a, hipStream_t stream) {
   if (!a) return MOE_EINVAL_NULL;
-  int rc = check_sort(a);
+  const int rc = check_sort(a);
   if (rc != MOE_OK) return rc;
   const int n = a->T * a->K;
   SortJob j;
@@ -391,15 +574,9 @@ extern "C" int moe_sort_rows(const moe_sort_rows_args* a, hipStream_t stream) {
   j.expert = a->expert; j.perm = a->perm; j.pos = a->pos; j.counts = a->counts; j.offsets = a->offsets;
   j.row_slot = a->row_slot; j.err = a->err;
   if (n == 0) return launch(sort_empty_kernel, 1, 256, stream, j);
-  const int per = (n + kSegs - 1) / kSegs, seg_len = (per + kIdx - 1) / kIdx * kIdx;
-  const int segs = (n + seg_len - 1) / seg_len;
-  rc = launch(sort_count_kernel, (unsigned)segs, kIdx, stream, j, seg_len, (int32_t*)a->workspace);
-  if (rc != MOE_OK) return rc;
-  rc = launch(sort_place_kernel, (unsigned)segs, kIdx, stream, j, segs, seg_len, (const int32_t*)a->workspace);
-  if (rc != MOE_OK || !a->xs) return rc;
-  if (a->x_dtype == MOE_F32) return copy_rows<MOE_F32>(a, stream);
-  if (a->x_dtype == MOE_BF16) return copy_rows<MOE_BF16>(a, stream);
-  return copy_rows<MOE_FP8_E4M3>(a, stream);
+  if (!a->xs || a->x_dtype == MOE_BF16) return sort_rows<MOE_BF16>(a, j, stream);
+  if (a->x_dtype == MOE_F32) return sort_rows<MOE_F32>(a, j, stream);
+  return sort_rows<MOE_FP8_E4M3>(a, j, stream);
 }
 
 extern "C" int moe_merge_rows(const moe_merge_rows_args* a, hipStream_t stream) {
@@ -418,12 +595,9 @@ extern "C" int moe_merge_rows(const moe_merge_rows_args* a, hipStream_t stream) 
   m.T = a->T; m.K = a->K; m.H = a->H; m.chunks = a->H / 8;
   m.rows = a->rows; m.row_pitch = a->row_pitch; m.n_rows = a->n_rows;
   m.pos = a->pos; m.w = a->w; m.out = a->out; m.out_pitch = a->out_pitch; m.err = a->err;
-  const unsigned grid = grid_of(a->T);
   if (a->row_dtype == MOE_F32)
-    return a->out_dtype == MOE_F32 ? launch(merge_kernel<MOE_F32, MOE_F32>, grid, 256, stream, m)
-                                   : launch(merge_kernel<MOE_F32, MOE_BF16>, grid, 256, stream, m);
-  return a->out_dtype == MOE_F32 ? launch(merge_kernel<MOE_BF16, MOE_F32>, grid, 256, stream, m)
-                                 : launch(merge_kernel<MOE_BF16, MOE_BF16>, grid, 256, stream, m);
+    return a->out_dtype == MOE_F32 ? merge_by_k<MOE_F32, MOE_F32>(m, stream) : merge_by_k<MOE_F32, MOE_BF16>(m, stream);
+  return a->out_dtype == MOE_F32 ? merge_by_k<MOE_BF16, MOE_F32>(m, stream) : merge_by_k<MOE_BF16, MOE_BF16>(m, stream);
 }
 
 extern "C" int moe_merge_rows_backward(const moe_merge_rows_backward_args* a, hipStream_t stream) {
@@ -447,10 +621,9 @@ extern "C" int moe_merge_rows_backward(const moe_merge_rows_backward_args* a, hi
   m.dout = a->dout; m.dout_pitch = a->dout_pitch; m.rows = a->rows; m.row_pitch = a->row_pitch;
   m.n_rows = a->n_rows; m.pos = a->pos; m.w = a->w; m.drows = a->drows; m.drows_pitch = a->drows_pitch;
   m.dw = a->dw; m.err = a->err;
-  const unsigned grid = grid_of(a->T);
   if (a->dout_dtype == MOE_F32)
-    return a->row_dtype == MOE_F32 ? launch(merge_backward_kernel<MOE_F32, MOE_F32>, grid, 256, stream, m)
-                                   : launch(merge_backward_kernel<MOE_F32, MOE_BF16>, grid, 256, stream, m);
-  return a->row_dtype == MOE_F32 ? launch(merge_backward_kernel<MOE_BF16, MOE_F32>, grid, 256, stream, m)
-                                 : launch(merge_backward_kernel<MOE_BF16, MOE_BF16>, grid, 256, stream, m);
+    return a->row_dtype == MOE_F32 ? merge_backward_by_k<MOE_F32, MOE_F32>(m, stream)
+                                   : merge_backward_by_k<MOE_F32, MOE_BF16>(m, stream);
+  return a->row_dtype == MOE_F32 ? merge_backward_by_k<MOE_BF16, MOE_F32>(m, stream)
+                                 : merge_backward_by_k<MOE_BF16, MOE_BF16>(m, stream);
 }
