@@ -6,6 +6,21 @@
 
 namespace moe {
 
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
+// Loads and stores of rows come in two kinds.  NT (non-temporal) ones pass through the caches
+// without staying: they move large arrays faster, but what they wrote is not near for a next kernel.
+template <bool NT, typename V>
+__device__ __forceinline__ V ld(const V* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void st(V* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 // A row is handled in chunks of eight elements: 16 bytes of bf16, two 16-byte runs of fp32, 8
 // bytes of fp8.  ld8 / st8 take the element offset of the chunk from the row's start.
 template <int DT>
@@ -14,8 +29,9 @@ struct Chunk;
 template <>
 struct Chunk<MOE_BF16> {
   u32x4 r;
+  template <bool NT = false>
   __device__ __forceinline__ void load(const void* row, int64_t at) {
-    r = *reinterpret_cast<const u32x4*>((const uint16_t*)row + at);
+    r = ld<NT>(reinterpret_cast<const u32x4*>((const uint16_t*)row + at));
   }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
@@ -29,9 +45,10 @@ struct Chunk<MOE_BF16> {
 template <>
 struct Chunk<MOE_F32> {
   f32x4 a, b;
+  template <bool NT = false>
   __device__ __forceinline__ void load(const void* row, int64_t at) {
-    a = *reinterpret_cast<const f32x4*>((const float*)row + at);
-    b = *reinterpret_cast<const f32x4*>((const float*)row + at + 4);
+    a = ld<NT>(reinterpret_cast<const f32x4*>((const float*)row + at));
+    b = ld<NT>(reinterpret_cast<const f32x4*>((const float*)row + at + 4));
   }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
@@ -44,35 +61,36 @@ struct Chunk<MOE_F32> {
 
 template <>
 struct Chunk<MOE_FP8_E4M3> {
-  uint2 r;
+  u32x2 r;
+  template <bool NT = false>
   __device__ __forceinline__ void load(const void* row, int64_t at) {
-    r = *reinterpret_cast<const uint2*>((const uint8_t*)row + at);
+    r = ld<NT>(reinterpret_cast<const u32x2*>((const uint8_t*)row + at));
   }
   __device__ __forceinline__ void get(float* f) const {  // exact: every code is a bf16 value
-    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(r.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(r.x, true);
-    const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(r.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8(r.y, true);
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(r[0], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(r[0], true);
+    const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(r[1], false), d = __builtin_amdgcn_cvt_pk_f32_fp8(r[1], true);
     f[0] = a[0]; f[1] = a[1]; f[2] = b[0]; f[3] = b[1];
     f[4] = c[0]; f[5] = c[1]; f[6] = d[0]; f[7] = d[1];
   }
 };
 
 // One rounding to the stored type, to nearest even.
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void st8(void* row, int64_t at, const float* f) {
   if constexpr (DT == MOE_F32) {
     float* p = (float*)row + at;
-    *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+    st<NT>(reinterpret_cast<f32x4*>(p), f32x4{f[0], f[1], f[2], f[3]});
+    st<NT>(reinterpret_cast<f32x4*>(p + 4), f32x4{f[4], f[5], f[6], f[7]});
   } else if constexpr (DT == MOE_BF16) {
-    *reinterpret_cast<u32x4*>((uint16_t*)row + at) =
-        u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    st<NT>(reinterpret_cast<u32x4*>((uint16_t*)row + at),
+           u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])});
   } else {
     int lo = 0, hi = 0;
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], lo, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
     hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], hi, false);
     hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], hi, true);
-    *reinterpret_cast<uint2*>((uint8_t*)row + at) = make_uint2((uint32_t)lo, (uint32_t)hi);
+    st<NT>(reinterpret_cast<u32x2*>((uint8_t*)row + at), u32x2{(uint32_t)lo, (uint32_t)hi});
   }
 }
 
@@ -154,6 +172,25 @@ inline bool aligned_rows(const void* p, int64_t pitch, int esz, int to) {
 }
 // rows are read and written in chunks of eight elements, by 16 bytes where a chunk has as many
 inline int chunk_align(int dt) { return dt == MOE_FP8_E4M3 ? 8 : 16; }
+
+// How a call that reads and writes so many bytes of rows goes through the caches: kNear plain,
+// kReadOnce with NT loads, kThrough with NT loads and stores.  Measured on rows of 2880 and 4096 bf16,
+// microseconds alone / with a kernel after it that reads the output:
+//                              kNear        kReadOnce    kThrough
+//   merge      64 MiB moved    11.9 /  19.1  13.8 /  21.1  12.4 /  22.9
+//             112 MiB          26.1 /  33.0  25.0 /  32.6  23.3 /  34.7
+//             225 MiB          49.0 /  61.0  46.6 /  56.3  44.1 /  57.1
+//             450 MiB          94.0 / 115.1  91.6 / 110.3  86.1 / 110.1
+//   norm       64 MiB          12.7 /  21.3  14.9 /  23.5  13.6 /  25.6
+//             128 MiB          26.6 /  37.3  25.1 /  36.7  24.3 /  37.6
+//             256 MiB          47.2 /  63.8  47.9 /  60.4  44.7 /  60.8
+//             512 MiB          91.0 / 122.6  89.9 / 116.2  85.8 / 116.2
+// Below 96 MiB what was written lately is still near and a plain load finds it; from 192 MiB on an
+// output does not stay near anyway (the last-level cache holds 256 MiB).
+enum { kNear = 0, kReadOnce = 1, kThrough = 2 };
+inline int stream_kind(int64_t bytes) {
+  return bytes >= (192ll << 20) ? kThrough : bytes >= (96ll << 20) ? kReadOnce : kNear;
+}
 
 constexpr int kHMaxRows = 1 << 16;  // longest row of the row operators
 

@@ -81,7 +81,7 @@ __device__ __forceinline__ float over(float v, float s, float inv) {
 }
 
 // A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + 256, ...
-template <int XT, int RT, int OT, int C>
+template <int XT, int RT, int OT, int C, int S>
 __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
   __shared__ float s_a[2][kNormWaves], s_b[2][kNormWaves];
   const int rows = j.row_list ? min(j.T, *j.row_count) : j.T;
@@ -104,11 +104,11 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
       for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
       if (at < j.H) {
         Chunk<XT> q;
-        q.load(x, at);
+        q.template load<(S >= kReadOnce)>(x, at);
         q.get(h[c]);
         if (j.residual) {
           Chunk<RT> r;
-          r.load((const char*)j.residual + row_bytes<RT>(t, j.res_pitch), at);
+          r.template load<(S >= kReadOnce)>((const char*)j.residual + row_bytes<RT>(t, j.res_pitch), at);
           float f[8];
           r.get(f);
 #pragma unroll
@@ -126,12 +126,12 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
     for (int c = 0; c < C; ++c) {
       const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (at < j.H) {
-        if (j.residual_out) st8<RT>((char*)j.residual_out + row_bytes<RT>(t, j.res_out_pitch), at, h[c]);
+        if (j.residual_out) st8<RT, S == kThrough>((char*)j.residual_out + row_bytes<RT>(t, j.res_out_pitch), at, h[c]);
         float g[8];
         gamma8(j.gamma, j.gamma_f32, at, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[c][e] *= r * g[e];
-        if constexpr (OT != MOE_FP8_E4M3) st8<OT>(out, at, h[c]);
+        if constexpr (OT != MOE_FP8_E4M3) st8<OT, S == kThrough>(out, at, h[c]);
       }
       if constexpr (OT == MOE_FP8_E4M3) {
         float a = 0.f;
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
             const float inv = 1.f / s;
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[c][e] = over(h[c][e], s, inv);
-            st8<OT>(out, at, h[c]);
+            st8<OT, S == kThrough>(out, at, h[c]);
             const int lane = threadIdx.x & (j.group_lanes - 1);
             if (lane == 0) j.out_scale[(int64_t)t * j.groups + at / (j.group_lanes * 8)] = s;
           }
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
           if (at < j.H) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[c][e] = over(h[c][e], s, inv);
-            st8<OT>(out, at, h[c]);
+            st8<OT, S == kThrough>(out, at, h[c]);
           }
         }
         if (threadIdx.x == 0) j.out_scale[t] = s;
@@ -182,7 +182,7 @@ struct NormBackJob {
 // With xhat = h r and g = dout gamma:  dh = r (g - xhat <g, xhat> / H) + dres,  dgamma = sum_t dout xhat.
 // A workgroup takes the rows blockIdx, blockIdx + gridDim, ... and keeps its share of dgamma in
 // registers.
-template <int DT, int HT, int C>
+template <int DT, int HT, int C, int S>
 __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   __shared__ float s_a[2][kNormWaves];
   float dg[C][8];
@@ -197,9 +197,9 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
     for (int c = 0; c < C; ++c) {
       const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (at < j.H) {
-        nd[c].load(dout, at);
-        nh[c].load(hr, at);
-        if (j.dres) ns[c].load(dres, at);
+        nd[c].template load<(S >= kReadOnce)>(dout, at);
+        nh[c].template load<(S >= kReadOnce)>(hr, at);
+        if (j.dres) ns[c].template load<(S >= kReadOnce)>(dres, at);
       }
     }
     nr = j.rstd[t];
@@ -249,8 +249,8 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) d[e] += f[e];
         }
-        if (j.dx) st8<DT>((char*)j.dx + row_bytes<DT>(t, j.dx_pitch), at, d);
-        if (j.dresidual) st8<HT>((char*)j.dresidual + row_bytes<HT>(t, j.dresidual_pitch), at, d);
+        if (j.dx) st8<DT, S == kThrough>((char*)j.dx + row_bytes<DT>(t, j.dx_pitch), at, d);
+        if (j.dresidual) st8<HT, S == kThrough>((char*)j.dresidual + row_bytes<HT>(t, j.dresidual_pitch), at, d);
       }
     }
   }
@@ -298,13 +298,22 @@ static bool norm_types_ok(int a, int b) {
   return (a == MOE_BF16 && (b == MOE_BF16 || b == MOE_F32)) || (a == MOE_F32 && b == MOE_F32);
 }
 
+template <int XT, int RT, int OT, int C>
+static int norm_launch(const NormJob& j, unsigned threads, hipStream_t stream) {
+  const int rs = dtype_size(RT) * ((j.residual != nullptr) + (j.residual_out != nullptr));
+  const unsigned grid = grid_of(j.T);
+  switch (stream_kind((int64_t)j.T * j.H * (dtype_size(XT) + dtype_size(OT) + rs))) {
+    case kThrough: return launch(norm_kernel<XT, RT, OT, C, kThrough>, grid, threads, stream, j);
+    case kReadOnce: return launch(norm_kernel<XT, RT, OT, C, kReadOnce>, grid, threads, stream, j);
+    default: return launch(norm_kernel<XT, RT, OT, C, kNear>, grid, threads, stream, j);
+  }
+}
 template <int XT, int RT, int OT>
 static int norm_by_width(const NormJob& j, hipStream_t stream) {
   const RowShape r = row_shape(j.H);
-  const unsigned grid = grid_of(j.T);
-  if (r.chunks == 1) return launch(norm_kernel<XT, RT, OT, 1>, grid, r.threads, stream, j);
-  if (r.chunks == 2) return launch(norm_kernel<XT, RT, OT, 2>, grid, r.threads, stream, j);
-  return launch(norm_kernel<XT, RT, OT, 4>, grid, r.threads, stream, j);
+  if (r.chunks == 1) return norm_launch<XT, RT, OT, 1>(j, r.threads, stream);
+  if (r.chunks == 2) return norm_launch<XT, RT, OT, 2>(j, r.threads, stream);
+  return norm_launch<XT, RT, OT, 4>(j, r.threads, stream);
 }
 
 template <int XT, int RT>
@@ -314,12 +323,21 @@ static int norm_by_out(const NormJob& j, int out, hipStream_t stream) {
   return norm_by_width<XT, RT, MOE_FP8_E4M3>(j, stream);
 }
 
+template <int DT, int HT, int C>
+static int norm_backward_launch(const NormBackJob& j, unsigned grid, unsigned threads, hipStream_t stream) {
+  const int hs = dtype_size(HT) * (1 + (j.dres != nullptr) + (j.dresidual != nullptr));
+  switch (stream_kind((int64_t)j.T * j.H * (dtype_size(DT) * (1 + (j.dx != nullptr)) + hs))) {
+    case kThrough: return launch(norm_backward_kernel<DT, HT, C, kThrough>, grid, threads, stream, j);
+    case kReadOnce: return launch(norm_backward_kernel<DT, HT, C, kReadOnce>, grid, threads, stream, j);
+    default: return launch(norm_backward_kernel<DT, HT, C, kNear>, grid, threads, stream, j);
+  }
+}
 template <int DT, int HT>
 static int norm_backward_by_width(const NormBackJob& j, unsigned grid, hipStream_t stream) {
   const RowShape r = row_shape(j.H);
-  if (r.chunks == 1) return launch(norm_backward_kernel<DT, HT, 1>, grid, r.threads, stream, j);
-  if (r.chunks == 2) return launch(norm_backward_kernel<DT, HT, 2>, grid, r.threads, stream, j);
-  return launch(norm_backward_kernel<DT, HT, 4>, grid, r.threads, stream, j);
+  if (r.chunks == 1) return norm_backward_launch<DT, HT, 1>(j, grid, r.threads, stream);
+  if (r.chunks == 2) return norm_backward_launch<DT, HT, 2>(j, grid, r.threads, stream);
+  return norm_backward_launch<DT, HT, 4>(j, grid, r.threads, stream);
 }
 
 }  // namespace moe

@@ -67,62 +67,36 @@ __global__ __launch_bounds__(kIdx) void sort_count_kernel(SortJob j, int seg_len
 
 __global__ __launch_bounds__(kIdx) void sort_place_kernel(SortJob j, int segs, int seg_len,
                                                           const int32_t* __restrict__ ws) {
-  __shared__ int s_run[kMaxEloc];   // next row of each expert in this segment
+  __shared__ int s_run[kMaxEloc];  // next row of each expert in this segment
   __shared__ int s_all[kMaxEloc];
   __shared__ int s_wcnt[kIdxWaves][kMaxEloc + 1];
   __shared__ int s_total;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, seg = blockIdx.x;
-  for (int e = tid; e < kMaxEloc; e += kIdx) s_run[e] = s_all[e] = 0;
-  __syncthreads();
-  // column sums: thread (g, e) takes the segments g, g + 4, ...
-  {
-    const int e = tid & (kMaxEloc - 1);
-    int before = 0, all = 0;
-    if (e < j.E_loc) {
-      for (int s = tid / kMaxEloc; s < segs; s += kIdx / kMaxEloc) {
-        const int c = ws[s * j.E_loc + e];
-        all += c;
-        before += s < seg ? c : 0;
-      }
-      atomicAdd(&s_run[e], before);
-      atomicAdd(&s_all[e], all);
-    }
-  }
-  __syncthreads();
-  if (wv == 0) {  // exclusive scan over the experts, four per lane
-    int v[4], sum = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = s_all[lane * 4 + k];
-      sum += v[k];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int t = __shfl_up(incl, d);
-      if (lane >= d) incl += t;
-    }
-    int run = incl - sum;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = lane * 4 + k;
-      if (seg == 0 && e < j.E_loc) {
-        j.counts[e] = v[k];
-        j.offsets[e] = run;
-      }
-      s_run[e] += run;
-      run += v[k];
-    }
-    if (lane == 63) {
-      s_total = incl;
-      if (seg == 0) j.offsets[j.E_loc] = incl;
-    }
-  }
   const int lo = seg * seg_len, hi = min(j.n, lo + seg_len);
+  unsigned bad = 0;  // the count has reported these
+  int key = lo + tid < hi ? sort_key(j, lo + tid, bad) : kNone;
+  // column sums: thread (g, e) takes the segments g, g + 4, ..., eight loads at a time
+  const int col = tid & (kMaxEloc - 1);
+  int before = 0, all = 0;
+  if (col < j.E_loc) {
+    for (int s0 = tid / kMaxEloc; s0 < segs; s0 += 8 * (kIdx / kMaxEloc)) {
+      int c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int s = s0 + u * (kIdx / kMaxEloc);
+        c[u] = s < segs ? ws[s * j.E_loc + col] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        all += c[u];
+        before += s0 + u * (kIdx / kMaxEloc) < seg ? c[u] : 0;
+      }
+    }
+  }
+  for (int e = tid; e < kMaxEloc; e += kIdx) s_run[e] = s_all[e] = 0;
   for (int c0 = lo; c0 < hi; c0 += kIdx) {
     const int i = c0 + tid;
-    unsigned bad = 0;
-    const int key = i < hi ? sort_key(j, i, bad) : kNone;
+    if (c0 > lo) key = i < hi ? sort_key(j, i, bad) : kNone;
     for (int x = tid; x < kIdxWaves * (kMaxEloc + 1); x += kIdx) (&s_wcnt[0][0])[x] = 0;
     uint64_t peers = ~0ull;
 #pragma unroll
@@ -134,20 +108,52 @@ __global__ __launch_bounds__(kIdx) void sort_place_kernel(SortJob j, int segs, i
     const int rank = __popcll(peers & ((1ull << lane) - 1ull));
     __syncthreads();
     if (key < kNone && rank == 0) s_wcnt[wv][key] = __popcll(peers);
+    if (c0 == lo && col < j.E_loc) {
+      atomicAdd(&s_run[col], before);
+      atomicAdd(&s_all[col], all);
+    }
     __syncthreads();
-    if (tid < j.E_loc) {
-      int run = s_run[tid];
+    if (c0 == lo && wv == 0) {  // exclusive scan over the experts, four per lane
+      int v[4], sum = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = s_all[lane * 4 + k];
+        sum += v[k];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int t = __shfl_up(incl, d);
+        if (lane >= d) incl += t;
+      }
+      int run = incl - sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = lane * 4 + k;
+        if (seg == 0 && e < j.E_loc) {
+          j.counts[e] = v[k];
+          j.offsets[e] = run;
+        }
+        s_run[e] += run;
+        run += v[k];
+      }
+      if (lane == 63) {
+        s_total = incl;
+        if (seg == 0) j.offsets[j.E_loc] = incl;
+      }
+    }
+    int chunk = 0;  // this chunk's pairs of expert e = tid - 256, whose waves' counts become offsets
+    if (tid >= kMaxEloc && tid < 2 * kMaxEloc) {
 #pragma unroll
       for (int w = 0; w < kIdxWaves; ++w) {
-        const int cnt = s_wcnt[w][tid];
-        s_wcnt[w][tid] = run;
-        run += cnt;
+        const int cnt = s_wcnt[w][tid - kMaxEloc];
+        s_wcnt[w][tid - kMaxEloc] = chunk;
+        chunk += cnt;
       }
-      s_run[tid] = run;
     }
     __syncthreads();
     if (key < kNone) {
-      const int r = s_wcnt[wv][key] + rank;
+      const int r = s_run[key] + s_wcnt[wv][key] + rank;
       j.pos[i] = r;
       if (j.perm) j.perm[r] = i;
       if (j.row_slot) j.row_slot[r] = i / j.K;
@@ -158,7 +164,9 @@ __global__ __launch_bounds__(kIdx) void sort_place_kernel(SortJob j, int segs, i
       if (j.perm) j.perm[i] = -1;
       if (j.row_slot) j.row_slot[i] = -1;
     }
+    if (c0 + kIdx >= hi) break;
     __syncthreads();
+    if (tid >= kMaxEloc && tid < 2 * kMaxEloc) s_run[tid - kMaxEloc] += chunk;
   }
 }
 
@@ -194,8 +202,9 @@ struct SortedType {
   static constexpr int out = DT == MOE_FP8_E4M3 ? MOE_BF16 : DT;
 };
 
-// A chunk of token t's row on its way: read once, written to the token's K rows.
-template <int DT>
+// A chunk of token t's row on its way: read once, written to the token's K rows (NT: by
+// non-temporal stores).
+template <int DT, bool NT>
 struct Carried {
   static constexpr int esz = DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1;
   static constexpr int OUT = SortedType<DT>::out, osz = OUT == MOE_F32 ? 4 : 2;
@@ -219,21 +228,21 @@ struct Carried {
       if (r < 0) continue;
       char* dst = (char*)c.xs + (int64_t)r * c.xs_pitch * osz;
       if constexpr (DT == MOE_BF16)
-        *reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8) = q.r;
+        st<NT>(reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8), q.r);
       else
-        st8<OUT>(dst, (int64_t)ch * 8, f);
+        st8<OUT, NT>(dst, (int64_t)ch * 8, f);
     }
   }
 };
 
 // A workgroup per token (blockIdx, blockIdx + gridDim, ...).
-template <int DT>
+template <int DT, bool NT>
 __global__ __launch_bounds__(512) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
   const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
     const int p = all_lanes(lane < c.K ? pos[(int64_t)t * c.K + lane] : -1);
     for (int ch = threadIdx.x; ch < c.chunks; ch += blockDim.x) {
-      Carried<DT> x;
+      Carried<DT, NT> x;
       x.load(c, t, ch);
       x.store(c, ch, p);
     }
@@ -258,7 +267,7 @@ __global__ __launch_bounds__(512) void sort_short_kernel(SortJob j, CopyJob c) {
   unsigned bad = 0;
   if ((int)blockIdx.x < j.T) {
     const int t = blockIdx.x;
-    Carried<DT> first;
+    Carried<DT, false> first;
     if (tid < c.chunks) first.load(c, t, tid);
     const int padded = (j.n + 255) & ~255;
     for (int q = tid; q < padded; q += blockDim.x)
@@ -287,7 +296,7 @@ __global__ __launch_bounds__(512) void sort_short_kernel(SortJob j, CopyJob c) {
     const int p = all_lanes(lane < j.K ? s_pos[lane] : -1);
     if (tid < c.chunks) first.store(c, tid, p);
     for (int ch = tid + blockDim.x; ch < c.chunks; ch += blockDim.x) {
-      Carried<DT> x;
+      Carried<DT, false> x;
       x.load(c, t, ch);
       x.store(c, ch, p);
     }
@@ -368,7 +377,7 @@ __device__ __forceinline__ Named named_rows(const int32_t* pos, const float* w, 
 
 // A workgroup per token, KB positions at a time: their loads are all issued before the first is
 // used.  Each lane sums its chunk over the positions in order.
-template <int RT, int OT, int KB>
+template <int RT, int OT, int KB, int S>
 __global__ __launch_bounds__(512) void merge_kernel(MergeJob m) {
   const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x; t < m.T; t += gridDim.x) {
@@ -381,7 +390,7 @@ __global__ __launch_bounds__(512) void merge_kernel(MergeJob m) {
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
           const int p = lane_i32(r.p, k0 + k);
-          if (p >= 0) q[k].load(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
+          if (p >= 0) q[k].template load<(S >= kReadOnce)>(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
@@ -393,7 +402,7 @@ __global__ __launch_bounds__(512) void merge_kernel(MergeJob m) {
           for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, f[e], acc[e]);
         }
       }
-      st8<OT>(out, (int64_t)ch * 8, acc);
+      st8<OT, S == kThrough>(out, (int64_t)ch * 8, acc);
     }
   }
 }
@@ -414,7 +423,7 @@ struct MergeBackJob {
 
 // A workgroup per token, KB positions at a time; a position's dot product runs through the lane's
 // chunks, the wave's lanes and the waves.
-template <int DT, int RT, int KB>
+template <int DT, int RT, int KB, int S>
 __global__ __launch_bounds__(512) void merge_backward_kernel(MergeBackJob m) {
   __shared__ float s_dot[2][8][KB];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -429,12 +438,12 @@ __global__ __launch_bounds__(512) void merge_backward_kernel(MergeBackJob m) {
       for (int ch = threadIdx.x; ch < m.chunks; ch += blockDim.x) {
         Chunk<RT> q[KB];
         Chunk<DT> d;
-        d.load(dout, (int64_t)ch * 8);
+        d.template load<(S >= kReadOnce)>(dout, (int64_t)ch * 8);
         if (m.dw) {
 #pragma unroll
           for (int k = 0; k < KB; ++k) {
             const int p = lane_i32(r.p, k0 + k);
-            if (p >= 0) q[k].load(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
+            if (p >= 0) q[k].template load<(S >= kReadOnce)>(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
           }
         }
         float g[8];
@@ -448,7 +457,7 @@ __global__ __launch_bounds__(512) void merge_backward_kernel(MergeBackJob m) {
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = g[e] * w;
-            st8<RT>((char*)m.drows + (int64_t)p * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, f);
+            st8<RT, S == kThrough>((char*)m.drows + (int64_t)p * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, f);
           }
         }
         if (m.dw) {
@@ -478,19 +487,38 @@ __global__ __launch_bounds__(512) void merge_backward_kernel(MergeBackJob m) {
   }
 }
 
+template <int RT, int OT, int KB>
+static int merge_launch(const MergeJob& m, hipStream_t stream) {
+  const int64_t bytes = (int64_t)m.T * m.H * (m.K * dtype_size(RT) + dtype_size(OT));
+  const unsigned grid = grid_of(m.T), block = row_threads(m.chunks);
+  switch (stream_kind(bytes)) {
+    case kThrough: return launch(merge_kernel<RT, OT, KB, kThrough>, grid, block, stream, m);
+    case kReadOnce: return launch(merge_kernel<RT, OT, KB, kReadOnce>, grid, block, stream, m);
+    default: return launch(merge_kernel<RT, OT, KB, kNear>, grid, block, stream, m);
+  }
+}
 template <int RT, int OT>
 static int merge_by_k(const MergeJob& m, hipStream_t stream) {
+  if (m.K <= 2) return merge_launch<RT, OT, 2>(m, stream);
+  if (m.K <= 4) return merge_launch<RT, OT, 4>(m, stream);
+  return merge_launch<RT, OT, 8>(m, stream);
+}
+template <int DT, int RT, int KB>
+static int merge_backward_launch(const MergeBackJob& m, hipStream_t stream) {
+  const int sides = (m.dw != nullptr) + (m.drows != nullptr);
+  const int64_t bytes = (int64_t)m.T * m.H * (m.K * sides * dtype_size(RT) + dtype_size(DT));
   const unsigned grid = grid_of(m.T), block = row_threads(m.chunks);
-  if (m.K <= 2) return launch(merge_kernel<RT, OT, 2>, grid, block, stream, m);
-  if (m.K <= 4) return launch(merge_kernel<RT, OT, 4>, grid, block, stream, m);
-  return launch(merge_kernel<RT, OT, 8>, grid, block, stream, m);
+  switch (stream_kind(bytes)) {
+    case kThrough: return launch(merge_backward_kernel<DT, RT, KB, kThrough>, grid, block, stream, m);
+    case kReadOnce: return launch(merge_backward_kernel<DT, RT, KB, kReadOnce>, grid, block, stream, m);
+    default: return launch(merge_backward_kernel<DT, RT, KB, kNear>, grid, block, stream, m);
+  }
 }
 template <int DT, int RT>
 static int merge_backward_by_k(const MergeBackJob& m, hipStream_t stream) {
-  const unsigned grid = grid_of(m.T), block = row_threads(m.chunks);
-  if (m.K <= 2) return launch(merge_backward_kernel<DT, RT, 2>, grid, block, stream, m);
-  if (m.K <= 4) return launch(merge_backward_kernel<DT, RT, 4>, grid, block, stream, m);
-  return launch(merge_backward_kernel<DT, RT, 8>, grid, block, stream, m);
+  if (m.K <= 2) return merge_backward_launch<DT, RT, 2>(m, stream);
+  if (m.K <= 4) return merge_backward_launch<DT, RT, 4>(m, stream);
+  return merge_backward_launch<DT, RT, 8>(m, stream);
 }
 
 constexpr int64_t kMaxPitch = (int64_t)1 << 32;
@@ -561,7 +589,14 @@ static int sort_rows(const moe_sort_rows_args* a, const SortJob& j, hipStream_t 
   if (rc == MOE_OK)
     rc = launch(sort_place_kernel, (unsigned)segs, kIdx, stream, j, segs, seg_len, (const int32_t*)a->workspace);
   if (rc != MOE_OK || !c.chunks) return rc;
-  return launch(sort_copy_kernel<DT>, grid_of(j.T), block, stream, c, j.T, (const int32_t*)a->pos);
+  // NT stores from where the rows do not stay near (stream_kind), but plain loads: x is a Kth of the
+  // bytes and was written just before.  65536 rows of 2880 bf16 91 us, 101 with plain stores, 104 with
+  // NT loads too; 32768 rows 44, 54 and 54, equal once a reader of xs follows (95); 16384 rows 26, 31
+  // and 30, with a reader 53, 49 and 53.
+  const int64_t bytes = ((int64_t)j.n * (DT == MOE_F32 ? 4 : 2) + (int64_t)j.T * dtype_size(DT)) * a->H;
+  return launch(stream_kind(bytes) == kThrough ? sort_copy_kernel<DT, true> : sort_copy_kernel<DT, false>,
+                grid_of(j.T), block, stream,
+                c, j.T, (const int32_t*)a->pos);
 }
 
 extern "C" int moe_sort_rows(const moe_sort_rows_args* a, hipStream_t stream) {
