@@ -1,9 +1,10 @@
 // moe_route, moe_route_backward: choice of experts and router weights from logits, and the
 // logits' gradient.
 //
-// A token belongs to one row of 16 lanes (four tokens per wave), lane l holding the logits of
-// experts l V .. l V + V - 1, V = 1, 2, 4, ... 32 the smallest that covers E.  Reductions stay
-// inside the row, as DPP operands.
+// A token belongs to one row of 16 lanes (four tokens per wave), which holds its logits in runs of
+// W = min(V, 4) experts: lane l has e = (v / W) 16 W + l W + v % W for v < V, V = 1, 2, 4, ... 32 the
+// smallest that covers E, so that a load covers 64 consecutive logits.  Reductions stay inside the
+// row, as DPP operands.
 #include <float.h>
 #include <math.h>
 
@@ -16,7 +17,7 @@ constexpr int kRouteT = 256;               // threads per workgroup
 constexpr int kRouteTok = kRouteT / 16;    // tokens per workgroup
 
 struct RouteJob {
-  int T, E, K, dtype, vec, score, renorm;
+  int T, E, K, dtype, vec, vec_bias, score, renorm;
   int64_t pitch;
   float scale;
   const void* logits;
@@ -26,40 +27,70 @@ __device__ __forceinline__ float logit_at(const RouteJob& j, int64_t at) {
   return j.dtype == MOE_F32 ? ((const float*)j.logits)[at] : bf16_to_f32(((const uint16_t*)j.logits)[at]);
 }
 
-// The lane's V logits (NaN past E).  vec: rows start on 16 bytes and E is whole chunks, so that a
-// chunk of 16 bytes is either all inside the row or all past it.
 template <int V>
-__device__ __forceinline__ void load_logits(const RouteJob& j, int t, int e0, float* l) {
+__device__ __forceinline__ int expert_of(int lane, int v) {
+  constexpr int W = V < 4 ? V : 4;
+  return (v / W) * (16 * W) + lane * W + v % W;
+}
+
+// The lane's V logits (NaN past E).  vec: runs of four start on their own size, and E is whole runs.
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteJob& j, int t, int lane, float* l) {
   const int64_t row = (int64_t)t * j.pitch;
   if constexpr (V >= 4) {
-    if (j.vec && j.dtype == MOE_F32) {
+    if (j.vec) {
+      if (j.dtype == MOE_F32) {
 #pragma unroll
-      for (int v = 0; v < V; v += 4) {
-        f32x4 q = {NAN, NAN, NAN, NAN};
-        if (e0 + v < j.E) q = *reinterpret_cast<const f32x4*>((const float*)j.logits + row + e0 + v);
+        for (int v = 0; v < V; v += 4) {
+          const int e = expert_of<V>(lane, v);
+          f32x4 q = {NAN, NAN, NAN, NAN};
+          if (e < j.E) q = *reinterpret_cast<const f32x4*>((const float*)j.logits + row + e);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) l[v + k] = q[k];
-      }
-      return;
-    }
-  }
-  if constexpr (V >= 8) {
-    if (j.vec && j.dtype == MOE_BF16) {
+          for (int k = 0; k < 4; ++k) l[v + k] = q[k];
+        }
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; v += 8) {
-        u32x4 q = {~0u, ~0u, ~0u, ~0u};  // bf16 NaN
-        if (e0 + v < j.E) q = *reinterpret_cast<const u32x4*>((const uint16_t*)j.logits + row + e0 + v);
+        for (int v = 0; v < V; v += 4) {
+          const int e = expert_of<V>(lane, v);
+          u32x2 q = {~0u, ~0u};  // bf16 NaN
+          if (e < j.E) q = *reinterpret_cast<const u32x2*>((const uint16_t*)j.logits + row + e);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          l[v + 2 * k] = __uint_as_float(q[k] << 16);
-          l[v + 2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+          for (int k = 0; k < 2; ++k) {
+            l[v + 2 * k] = __uint_as_float(q[k] << 16);
+            l[v + 2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+          }
         }
       }
       return;
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = e0 + v < j.E ? logit_at(j, row + e0 + v) : NAN;
+  for (int v = 0; v < V; ++v) {
+    const int e = expert_of<V>(lane, v);
+    l[v] = e < j.E ? logit_at(j, row + e) : NAN;
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_bias(const RouteJob& j, const float* bias, int lane, float* b) {
+  if constexpr (V >= 4) {
+    if (j.vec_bias) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const int e = expert_of<V>(lane, v);
+        f32x4 q = {0.f, 0.f, 0.f, 0.f};
+        if (e < j.E) q = *reinterpret_cast<const f32x4*>(bias + e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[v + k] = q[k];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = expert_of<V>(lane, v);
+    b[v] = e < j.E ? bias[e] : 0.f;
+  }
 }
 
 // exp(l - m) with NaN and -inf as 0, and equal shares where the largest is +inf
@@ -80,6 +111,11 @@ __device__ __forceinline__ uint32_t order_key(float score) {
   if (!(score > -INFINITY)) return 0u;
   const uint32_t u = __float_as_uint(score + 0.f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// the score of a key (not of 0)
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float(key ^ (~(uint32_t)((int32_t)key >> 31) | 0x80000000u));
 }
 
 // The chosen position's share of the weights before `scale`: position lane (and lane + 16) of the
@@ -108,60 +144,91 @@ __device__ __forceinline__ Shares chosen_shares(const RouteJob& j, const float* 
   return s;
 }
 
+// l becomes exp(l - m), z their sum over the token.  The exponential is v_exp_f32 of a product: off
+// by |l - m| 2^-24 relative, as the subtraction's own rounding of large logits is.
 template <int V>
-__device__ __forceinline__ void softmax_of_all(const float* l, float& m, float& z) {
+__device__ __forceinline__ void softmax_of_all(float* l, float& m, float& z) {
   m = -INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);  // fmaxf passes over NaN
   m = max16(m);
   z = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) z += part_of(l[v], m);
+  for (int v = 0; v < V; ++v) {
+    const float e = m == INFINITY ? (l[v] == INFINITY ? 1.f : 0.f)
+                                  : __builtin_amdgcn_exp2f((l[v] - m) * 1.44269504f);
+    l[v] = l[v] > -INFINITY ? e : 0.f;
+    z += l[v];
+  }
   z = sum16(z);
 }
 
-// K rounds, each taking the row's largest key: the maximum of the lane's own, then of the 16
-// lanes; the lowest expert that has it (lanes hold ascending experts) is struck out by its owner.
+// A candidate as one number: the score's order in bits 30..61 and 511 - e below, so that the larger
+// of two is the larger score, or the lower expert of equal ones.  Read as a double it is positive
+// and finite, and the order of such doubles is that of their bits: v_max_f64 compares both parts in
+// one instruction (a 32-bit maximum and a search for its lowest expert took half as long again).
+struct Candidate {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Candidate larger(Candidate a, Candidate b) {
+  double x = __hiloint2double((int)a.hi, (int)a.lo), r;
+  const double y = __hiloint2double((int)b.hi, (int)b.lo);
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+  return {(uint32_t)__double2hiint(r), (uint32_t)__double2loint(r)};
+}
+template <int CTRL>
+__device__ __forceinline__ Candidate larger_dpp(Candidate a) {
+  return larger(a, {dpp_u32<CTRL>(a.hi), dpp_u32<CTRL>(a.lo)});
+}
+
+// K rounds, each taking the row's largest candidate: the maximum of the lane's own, then of the 16
+// lanes; its owner strikes it out.
 template <int V>
 __global__ __launch_bounds__(kRouteT) void route_kernel(RouteJob j, const float* __restrict__ bias,
                                                         int32_t* __restrict__ expert, float* __restrict__ w) {
   const int t = blockIdx.x * kRouteTok + (threadIdx.x >> 4), lane = threadIdx.x & 15;
   if (t >= j.T) return;  // whole rows of 16 lanes leave; no barrier follows
-  const int e0 = lane * V;
   float l[V];
-  uint32_t key[V];
-  load_logits<V>(j, t, e0, l);
+  Candidate c[V];
+  load_logits<V>(j, t, lane, l);
+  float b[V];
+  if (bias) load_bias<V>(j, bias, lane, b);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float s = l[v];
-    if (bias && e0 + v < j.E) s = s + bias[e0 + v];
-    key[v] = order_key(s);
+    const int e = expert_of<V>(lane, v);
+    const uint32_t key = order_key(bias ? l[v] + b[v] : l[v]);
+    c[v] = {key >> 2, key << 30 | (uint32_t)(kRouteE - 1 - e)};
   }
   int ce[2] = {-1, -1};
+  float lc[2] = {0.f, 0.f};
   for (int k = 0; k < j.K; ++k) {
-    uint32_t best = 0;
+    Candidate m[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) best = max(best, key[v]);
-    best = max16u(best);
-    uint32_t at = ~0u;
+    for (int v = 0; v < V; ++v) m[v] = c[v];
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) at = key[v] == best ? (uint32_t)(e0 + v) : at;
-    at = min16u(at);
+    for (int d = 1; d < V; d <<= 1)
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = at == (uint32_t)(e0 + v) ? 0u : key[v];
-    const int e = best ? (int)at : -1;
+      for (int v = 0; v + d < V; v += 2 * d) m[v] = larger(m[v], m[v + d]);
+    Candidate best = larger_dpp<kDppXor1>(m[0]);
+    best = larger_dpp<kDppXor2>(best);
+    best = larger_dpp<kDppHalfMirror>(best);
+    best = larger_dpp<kDppMirror>(best);
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v].hi = c[v].lo == best.lo ? 0u : c[v].hi;
+    const int e = best.hi ? kRouteE - 1 - (int)(best.lo & (kRouteE - 1)) : -1;
     if (lane == (k & 15)) {
-      if (k < 16) ce[0] = e;
-      else ce[1] = e;
+      const float score = key_value(best.hi << 2 | best.lo >> 30);
+      if (k < 16) { ce[0] = e; lc[0] = score; }
+      else { ce[1] = e; lc[1] = score; }
     }
   }
-  float m = 0.f, z = 0.f, lc[2];
+  float m = 0.f, z = 0.f;
   bool there[2];
   if (j.score == MOE_SOFTMAX && !j.renorm) softmax_of_all<V>(l, m, z);
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     there[r] = ce[r] >= 0;
-    lc[r] = there[r] ? logit_at(j, (int64_t)t * j.pitch + ce[r]) : 0.f;
+    if (bias && there[r]) lc[r] = logit_at(j, (int64_t)t * j.pitch + ce[r]);
   }
   const Shares s = chosen_shares(j, lc, there, m, z);
 #pragma unroll
@@ -182,10 +249,9 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RouteJob j, const float*
 template <int V>
 __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, const int32_t* __restrict__ expert,
                                                                  const float* __restrict__ dw, void* dlogits,
-                                                                 int64_t dpitch, uint32_t* err) {
+                                                                 int64_t dpitch, int vec_out, uint32_t* err) {
   const int t = blockIdx.x * kRouteTok + (threadIdx.x >> 4), lane = threadIdx.x & 15;
   if (t >= j.T) return;
-  const int e0 = lane * V;
   const bool all = j.score == MOE_SOFTMAX && !j.renorm;
   int ce[2];
   float lc[2], v[2], dl[2];
@@ -202,7 +268,7 @@ __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, con
   if (bad) atomicOr(err, MOE_ERR_EXPERT_NONLOCAL);
   float l[V], m = 0.f, z = 0.f;
   if (all) {
-    load_logits<V>(j, t, e0, l);
+    load_logits<V>(j, t, lane, l);
     softmax_of_all<V>(l, m, z);
   }
   const Shares s = chosen_shares(j, lc, there, m, z);
@@ -214,20 +280,37 @@ __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, con
     if (j.score == MOE_SIGMOID) dl[r] *= sigmoid(-lc[r]);
   }
   float d[V];
+  const float each = all && z > 0.f ? -vp / z : 0.f;
 #pragma unroll
-  for (int q = 0; q < V; ++q) d[q] = all && z > 0.f ? -(part_of(l[q], m) / z) * vp : 0.f;
+  for (int q = 0; q < V; ++q) d[q] = all ? l[q] * each : 0.f;
   for (int k = 0; k < j.K; ++k) {
     const int e = __shfl(k < 16 ? ce[0] : ce[1], k & 15, 16);
     const float g = __shfl(k < 16 ? dl[0] : dl[1], k & 15, 16);
 #pragma unroll
-    for (int q = 0; q < V; ++q) d[q] += e == e0 + q ? g : 0.f;
+    for (int q = 0; q < V; ++q) d[q] += e == expert_of<V>(lane, q) ? g : 0.f;
   }
   const int64_t row = (int64_t)t * dpitch;
+  if constexpr (V >= 4) {
+    if (vec_out) {
+#pragma unroll
+      for (int q = 0; q < V; q += 4) {
+        const int e = expert_of<V>(lane, q);
+        if (e >= j.E) continue;
+        if (j.dtype == MOE_F32)
+          *reinterpret_cast<f32x4*>((float*)dlogits + row + e) = f32x4{d[q], d[q + 1], d[q + 2], d[q + 3]};
+        else
+          *reinterpret_cast<u32x2*>((uint16_t*)dlogits + row + e) =
+              u32x2{pack_bf16x2(d[q], d[q + 1]), pack_bf16x2(d[q + 2], d[q + 3])};
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int q = 0; q < V; ++q) {
-    if (e0 + q >= j.E) continue;
-    if (j.dtype == MOE_F32) ((float*)dlogits)[row + e0 + q] = d[q];
-    else ((uint16_t*)dlogits)[row + e0 + q] = f32_to_bf16(d[q]);
+    const int e = expert_of<V>(lane, q);
+    if (e >= j.E) continue;
+    if (j.dtype == MOE_F32) ((float*)dlogits)[row + e] = d[q];
+    else ((uint16_t*)dlogits)[row + e] = f32_to_bf16(d[q]);
   }
 }
 
@@ -240,13 +323,18 @@ static int check_route(int32_t T, int32_t E, int32_t K, int32_t dtype, int64_t p
   return MOE_OK;
 }
 
+static bool runs_of_four(const void* rows, int64_t pitch, int E, int esz) {
+  return E % 4 == 0 && aligned_rows(rows, pitch, esz, 4 * esz);
+}
+
 static RouteJob make_route_job(int32_t T, int32_t E, int32_t K, int32_t dtype, int64_t pitch, int32_t score,
                                int32_t renorm, float scale, const void* logits) {
   const int esz = dtype_size(dtype);
   RouteJob j;
   j.T = T; j.E = E; j.K = K; j.dtype = dtype; j.score = score; j.renorm = renorm;
   j.pitch = pitch; j.scale = scale; j.logits = logits;
-  j.vec = aligned_rows(logits, pitch, esz, 16) && (E * esz) % 16 == 0;
+  j.vec = runs_of_four(logits, pitch, E, esz);
+  j.vec_bias = 0;
   return j;
 }
 
@@ -273,7 +361,8 @@ template <int V>
 struct RouteBackward {
   static int go(const RouteJob& j, const moe_route_backward_args* a, hipStream_t stream) {
     return launch(route_backward_kernel<V>, (unsigned)((a->T + kRouteTok - 1) / kRouteTok), kRouteT, stream, j,
-                  a->expert, a->dw, a->dlogits, a->dlogits_pitch, a->err);
+                  a->expert, a->dw, a->dlogits, a->dlogits_pitch,
+                  (int)runs_of_four(a->dlogits, a->dlogits_pitch, a->E, dtype_size(a->dtype)), a->err);
   }
 };
 
@@ -288,7 +377,8 @@ extern "C" int moe_route(const moe_route_args* a, hipStream_t stream) {
   if (a->T == 0) return MOE_OK;
   if (!a->logits || !a->expert || !a->w) return MOE_EINVAL_NULL;
   if ((uintptr_t)a->logits % dtype_size(a->dtype)) return MOE_EINVAL_ALIGN;
-  const RouteJob j = make_route_job(a->T, a->E, a->K, a->dtype, a->pitch, a->score, a->renorm, a->scale, a->logits);
+  RouteJob j = make_route_job(a->T, a->E, a->K, a->dtype, a->pitch, a->score, a->renorm, a->scale, a->logits);
+  j.vec_bias = runs_of_four(a->bias, a->E, a->E, 4);
   return by_width<Route>(a->E, j, a, stream);
 }
 
