@@ -353,6 +353,14 @@ _HOME = {"moe_route": _packer(RouteArgs), "moe_route_backward": _packer(RouteBac
          "moe_merge_rows_backward": _packer(MergeRowsBackwardArgs), "moe_residual_norm": _packer(ResidualNormArgs),
          "moe_residual_norm_backward": _packer(ResidualNormBackwardArgs)}
 
+_home: dict = {}  # name -> (pack, the library's function)
+
+
+def _home_entry(name: str):
+    _home[name] = entry = _HOME[name].pack, getattr(load(), name)
+    return entry
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -414,8 +422,9 @@ def _home_call(name: str, values, tensors, stream) -> None:
     """One call of the library on the device that its tensors are on.  With a stream other than
     the current one, the tensors are recorded on it, so that the allocator keeps them until the
     call's work is done."""
+    pack, fn = _home.get(name) or _home_entry(name)
     try:
-        args = _HOME[name].pack(*values)
+        args = pack(*values)
     except (struct.error, OverflowError, TypeError) as e:
         raise MoeError(f"{name}: an argument is over the documented limits ({e})") from None
     at = tensors[0].get_device()
@@ -424,7 +433,6 @@ def _home_call(name: str, values, tensors, stream) -> None:
             raise MoeError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     if at < 0:
         raise MoeError(f"{name}: tensors must be on a GPU, got {tensors[0].device}")
-    fn = getattr(_lib or load(), name)
     handle = current = _raw_stream(at)
     if stream is not None:
         where = getattr(stream, "device", None)

@@ -121,27 +121,29 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // The chosen position's share of the weights before `scale`: position lane (and lane + 16) of the
 // row in each lane, l[] its logit, there[] whether it names an expert.  For softmax over all
 // experts m and z are given; otherwise they are taken over the chosen.
-struct Shares {
-  float p[2];
-};
-__device__ __forceinline__ Shares chosen_shares(const RouteJob& j, const float* l, const bool* there, float m_all,
-                                                float z_all) {
-  Shares s;
+template <int R>
+__device__ __forceinline__ void chosen_shares(const RouteJob& j, const float* l, const bool* there, float m_all,
+                                              float z_all, float* p) {
   if (j.score == MOE_SIGMOID && !j.renorm) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) s.p[r] = there[r] ? sigmoid(l[r]) : 0.f;
-    return s;
+    for (int r = 0; r < R; ++r) p[r] = there[r] ? sigmoid(l[r]) : 0.f;
+    return;
   }
-  float v[2];
+  float v[R], m = -INFINITY, z = 0.f;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) v[r] = !there[r] ? -INFINITY : j.score == MOE_SIGMOID ? log_sigmoid(l[r]) : l[r];
-  const float m = j.renorm ? max16(fmaxf(v[0], v[1])) : m_all;
+  for (int r = 0; r < R; ++r) {
+    v[r] = !there[r] ? -INFINITY : j.score == MOE_SIGMOID ? log_sigmoid(l[r]) : l[r];
+    m = fmaxf(m, v[r]);
+  }
+  m = j.renorm ? max16(m) : m_all;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) s.p[r] = part_of(v[r], m);
-  const float z = j.renorm ? sum16(s.p[0] + s.p[1]) : z_all;
+  for (int r = 0; r < R; ++r) {
+    p[r] = part_of(v[r], m);
+    z += p[r];
+  }
+  z = j.renorm ? sum16(z) : z_all;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) s.p[r] = z > 0.f ? s.p[r] / z : 0.f;
-  return s;
+  for (int r = 0; r < R; ++r) p[r] = z > 0.f ? p[r] / z : 0.f;
 }
 
 // l becomes exp(l - m), z their sum over the token.  The exponential is v_exp_f32 of a product: off
@@ -181,11 +183,76 @@ __device__ __forceinline__ Candidate larger_dpp(Candidate a) {
   return larger(a, {dpp_u32<CTRL>(a.hi), dpp_u32<CTRL>(a.lo)});
 }
 
-// K rounds, each taking the row's largest candidate: the maximum of the lane's own, then of the 16
-// lanes; its owner strikes it out.
-template <int V>
+__device__ __forceinline__ Candidate smaller(Candidate a, Candidate b) {
+  double x = __hiloint2double((int)a.hi, (int)a.lo), r;
+  const double y = __hiloint2double((int)b.hi, (int)b.lo);
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+  return {(uint32_t)__double2hiint(r), (uint32_t)__double2loint(r)};
+}
+__device__ __forceinline__ void order(Candidate& a, Candidate& b) {  // the larger first
+  const Candidate x = larger(a, b);
+  b = smaller(a, b);
+  a = x;
+}
+
+// The N largest of a row's candidates, descending, in every lane: sorting networks of N = 4 or 8.
+// Two descending lists a, b have their N largest in max(a[i], b[N - 1 - i]), which rises and falls
+// once and is sorted by halving.
+template <int N>
+__device__ __forceinline__ void sort_halving(Candidate* a) {
+#pragma unroll
+  for (int d = N / 2; d; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(i & d)) order(a[i], a[i + d]);
+}
+template <int N>
+__device__ __forceinline__ void sort_all(Candidate* a) {  // odd-even merge sort
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int k = p; k; k >>= 1)
+#pragma unroll
+      for (int i = k & (p - 1); i + k < N; i += 2 * k)
+#pragma unroll
+        for (int q = 0; q < k; ++q)
+          if (i + q + k < N && (i + q) / (2 * p) == (i + q + k) / (2 * p)) order(a[i + q], a[i + q + k]);
+}
+template <int N, int CTRL>
+__device__ __forceinline__ void merge_dpp(Candidate* a) {
+  Candidate m[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    m[i] = larger(a[i], {dpp_u32<CTRL>(a[N - 1 - i].hi), dpp_u32<CTRL>(a[N - 1 - i].lo)});
+  sort_halving<N>(m);
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = m[i];
+}
+template <int V, int N>
+__device__ __forceinline__ void largest_sorted(const Candidate* c, Candidate* a) {
+#pragma unroll
+  for (int g = 0; g < V; g += N) {
+    Candidate b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = g + i < V ? c[g + i] : Candidate{0u, 0u};
+    sort_all<N>(b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = g ? larger(a[i], b[N - 1 - i]) : b[i];
+    if (g) sort_halving<N>(a);
+  }
+  merge_dpp<N, kDppXor1>(a);
+  merge_dpp<N, kDppXor2>(a);
+  merge_dpp<N, kDppHalfMirror>(a);
+  merge_dpp<N, kDppMirror>(a);
+}
+
+// N = 4, 8: the N >= K largest by sorting networks.  N = 0 (K > 8): K rounds, each taking the row's
+// largest candidate, the maximum of the lane's own and then of the 16 lanes, which its owner strikes
+// out.
+template <int V, int N>
 __global__ __launch_bounds__(kRouteT) void route_kernel(RouteJob j, const float* __restrict__ bias,
                                                         int32_t* __restrict__ expert, float* __restrict__ w) {
+  constexpr int R = N ? 1 : 2;  // positions per lane
   const int t = blockIdx.x * kRouteTok + (threadIdx.x >> 4), lane = threadIdx.x & 15;
   if (t >= j.T) return;  // whole rows of 16 lanes leave; no barrier follows
   float l[V];
@@ -199,44 +266,55 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RouteJob j, const float*
     const uint32_t key = order_key(bias ? l[v] + b[v] : l[v]);
     c[v] = {key >> 2, key << 30 | (uint32_t)(kRouteE - 1 - e)};
   }
-  int ce[2] = {-1, -1};
-  float lc[2] = {0.f, 0.f};
-  for (int k = 0; k < j.K; ++k) {
-    Candidate m[V];
+  Candidate mine[R];
 #pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = c[v];
+  for (int r = 0; r < R; ++r) mine[r] = {0u, 0u};
+  if constexpr (N > 0) {
+    Candidate a[N];
+    largest_sorted<V, N>(c, a);
 #pragma unroll
-    for (int d = 1; d < V; d <<= 1)
+    for (int k = 0; k < N; ++k)
+      if (lane == k) mine[0] = a[k];
+  } else {
+    for (int k = 0; k < j.K; ++k) {
+      Candidate m[V];
 #pragma unroll
-      for (int v = 0; v + d < V; v += 2 * d) m[v] = larger(m[v], m[v + d]);
-    Candidate best = larger_dpp<kDppXor1>(m[0]);
-    best = larger_dpp<kDppXor2>(best);
-    best = larger_dpp<kDppHalfMirror>(best);
-    best = larger_dpp<kDppMirror>(best);
+      for (int v = 0; v < V; ++v) m[v] = c[v];
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v].hi = c[v].lo == best.lo ? 0u : c[v].hi;
-    const int e = best.hi ? kRouteE - 1 - (int)(best.lo & (kRouteE - 1)) : -1;
-    if (lane == (k & 15)) {
-      const float score = key_value(best.hi << 2 | best.lo >> 30);
-      if (k < 16) { ce[0] = e; lc[0] = score; }
-      else { ce[1] = e; lc[1] = score; }
+      for (int d = 1; d < V; d <<= 1)
+#pragma unroll
+        for (int v = 0; v + d < V; v += 2 * d) m[v] = larger(m[v], m[v + d]);
+      Candidate best = larger_dpp<kDppXor1>(m[0]);
+      best = larger_dpp<kDppXor2>(best);
+      best = larger_dpp<kDppHalfMirror>(best);
+      best = larger_dpp<kDppMirror>(best);
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v].hi = c[v].lo == best.lo ? 0u : c[v].hi;
+      if (lane == (k & 15)) {
+        if (k < 16) mine[0] = best;
+        else mine[1] = best;
+      }
     }
   }
-  float m = 0.f, z = 0.f;
-  bool there[2];
+  float m = 0.f, z = 0.f, lc[R];
+  bool there[R];
+  int ce[R];
   if (j.score == MOE_SOFTMAX && !j.renorm) softmax_of_all<V>(l, m, z);
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    there[r] = ce[r] >= 0;
+  for (int r = 0; r < R; ++r) {
+    there[r] = mine[r].hi != 0 && lane + 16 * r < j.K;
+    ce[r] = there[r] ? kRouteE - 1 - (int)(mine[r].lo & (kRouteE - 1)) : -1;
+    lc[r] = there[r] ? key_value(mine[r].hi << 2 | mine[r].lo >> 30) : 0.f;
     if (bias && there[r]) lc[r] = logit_at(j, (int64_t)t * j.pitch + ce[r]);
   }
-  const Shares s = chosen_shares(j, lc, there, m, z);
+  float p[R];
+  chosen_shares<R>(j, lc, there, m, z, p);
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < R; ++r) {
     const int k = lane + 16 * r;
     if (k < j.K) {
       expert[(int64_t)t * j.K + k] = ce[r];
-      w[(int64_t)t * j.K + k] = j.scale * s.p[r];
+      w[(int64_t)t * j.K + k] = j.scale * p[r];
     }
   }
 }
@@ -246,18 +324,18 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RouteJob j, const float*
 //   softmax over all:         dl_e = p_e (sum of v_j over j that name e - <v, p>)
 //   sigmoid:                  dl_j = v_j p_j sigma(-l_j)
 //   sigmoid over the chosen:  dl_j = p_j (v_j - <v, p>) sigma(-l_j)
-template <int V>
+template <int V, int R>
 __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, const int32_t* __restrict__ expert,
                                                                  const float* __restrict__ dw, void* dlogits,
                                                                  int64_t dpitch, int vec_out, uint32_t* err) {
   const int t = blockIdx.x * kRouteTok + (threadIdx.x >> 4), lane = threadIdx.x & 15;
   if (t >= j.T) return;
   const bool all = j.score == MOE_SOFTMAX && !j.renorm;
-  int ce[2];
-  float lc[2], v[2], dl[2];
-  bool there[2], bad = false;
+  int ce[R];
+  float lc[R], v[R], dl[R], p[R];
+  bool there[R], bad = false;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < R; ++r) {
     const int k = lane + 16 * r;
     ce[r] = k < j.K ? expert[(int64_t)t * j.K + k] : -1;
     there[r] = ce[r] >= 0 && ce[r] < j.E;
@@ -271,12 +349,14 @@ __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, con
     load_logits<V>(j, t, lane, l);
     softmax_of_all<V>(l, m, z);
   }
-  const Shares s = chosen_shares(j, lc, there, m, z);
-  const bool alone = j.score == MOE_SIGMOID && !j.renorm;
-  const float vp = alone ? 0.f : sum16(v[0] * s.p[0] + v[1] * s.p[1]);
+  chosen_shares<R>(j, lc, there, m, z, p);
+  float vp = 0.f;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    dl[r] = s.p[r] * (all ? v[r] : v[r] - vp);
+  for (int r = 0; r < R; ++r) vp = fmaf(v[r], p[r], vp);
+  vp = j.score == MOE_SIGMOID && !j.renorm ? 0.f : sum16(vp);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    dl[r] = p[r] * (all ? v[r] : v[r] - vp);
     if (j.score == MOE_SIGMOID) dl[r] *= sigmoid(-lc[r]);
   }
   float d[V];
@@ -284,8 +364,8 @@ __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, con
 #pragma unroll
   for (int q = 0; q < V; ++q) d[q] = all ? l[q] * each : 0.f;
   for (int k = 0; k < j.K; ++k) {
-    const int e = __shfl(k < 16 ? ce[0] : ce[1], k & 15, 16);
-    const float g = __shfl(k < 16 ? dl[0] : dl[1], k & 15, 16);
+    const int e = __shfl(k < 16 ? ce[0] : ce[R - 1], k & 15, 16);
+    const float g = __shfl(k < 16 ? dl[0] : dl[R - 1], k & 15, 16);
 #pragma unroll
     for (int q = 0; q < V; ++q) d[q] += e == expert_of<V>(lane, q) ? g : 0.f;
   }
@@ -352,17 +432,19 @@ static int by_width(int E, A... a) {
 template <int V>
 struct Route {
   static int go(const RouteJob& j, const moe_route_args* a, hipStream_t stream) {
-    return launch(route_kernel<V>, (unsigned)((a->T + kRouteTok - 1) / kRouteTok), kRouteT, stream, j, a->bias,
-                  a->expert, a->w);
+    const unsigned grid = (unsigned)((a->T + kRouteTok - 1) / kRouteTok);
+    auto kernel = a->K <= 4 ? route_kernel<V, 4> : a->K <= 8 ? route_kernel<V, 8> : route_kernel<V, 0>;
+    return launch(kernel, grid, kRouteT, stream, j, a->bias, a->expert, a->w);
   }
 };
 
 template <int V>
 struct RouteBackward {
   static int go(const RouteJob& j, const moe_route_backward_args* a, hipStream_t stream) {
-    return launch(route_backward_kernel<V>, (unsigned)((a->T + kRouteTok - 1) / kRouteTok), kRouteT, stream, j,
-                  a->expert, a->dw, a->dlogits, a->dlogits_pitch,
-                  (int)runs_of_four(a->dlogits, a->dlogits_pitch, a->E, dtype_size(a->dtype)), a->err);
+    const int vec_out = runs_of_four(a->dlogits, a->dlogits_pitch, a->E, dtype_size(a->dtype));
+    return launch(a->K <= 16 ? route_backward_kernel<V, 1> : route_backward_kernel<V, 2>,
+                  (unsigned)((a->T + kRouteTok - 1) / kRouteTok), kRouteT, stream, j, a->expert, a->dw, a->dlogits,
+                  a->dlogits_pitch, vec_out, a->err);
   }
 };
 
