@@ -96,26 +96,37 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
       }
     }
     const char* x = (const char*)j.x + row_bytes<XT>(t, j.x_pitch);
+    // G chunks' loads before the first use: one chunk after the other took 85 instead of 81 us at
+    // 16384 x 4096 bf16 (C = 1), four at once 86 instead of 82 at 4096 x 16384 (C = 4)
+    constexpr int G = C <= 2 ? C : 1;
     float h[C][8], ss = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
+    for (int c0 = 0; c0 < C; c0 += G) {
+      Chunk<XT> q[G];
+      Chunk<RT> o[G];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
-      if (at < j.H) {
-        Chunk<XT> q;
-        q.template load<(S >= kReadOnce)>(x, at);
-        q.get(h[c]);
+      for (int c = 0; c < G; ++c) {
+        const int at = ((c0 + c) * (int)blockDim.x + (int)threadIdx.x) * 8;
+        if (at < j.H) {
+          q[c].template load<(S >= kReadOnce)>(x, at);
+          if (j.residual) o[c].template load<(S >= kReadOnce)>((const char*)j.residual + row_bytes<RT>(t, j.res_pitch), at);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        float* hc = h[c0 + c];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hc[e] = 0.f;
+        if (((c0 + c) * (int)blockDim.x + (int)threadIdx.x) * 8 >= j.H) continue;
+        q[c].get(hc);
         if (j.residual) {
-          Chunk<RT> r;
-          r.template load<(S >= kReadOnce)>((const char*)j.residual + row_bytes<RT>(t, j.res_pitch), at);
           float f[8];
-          r.get(f);
+          o[c].get(f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[c][e] += f[e];
+          for (int e = 0; e < 8; ++e) hc[e] += f[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(hc[e], hc[e], ss);
       }
     }
     const float r = 1.f / sqrtf(group_sum(ss, s_a[par]) / (float)j.H + j.eps);

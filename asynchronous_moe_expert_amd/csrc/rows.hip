@@ -240,8 +240,11 @@ template <int DT, bool NT>
 __global__ __launch_bounds__(512) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
   const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    Carried<DT, NT> first;  // on its way while the positions are looked up
+    if ((int)threadIdx.x < c.chunks) first.load(c, t, threadIdx.x);
     const int p = all_lanes(lane < c.K ? pos[(int64_t)t * c.K + lane] : -1);
-    for (int ch = threadIdx.x; ch < c.chunks; ch += blockDim.x) {
+    if ((int)threadIdx.x < c.chunks) first.store(c, threadIdx.x, p);
+    for (int ch = threadIdx.x + blockDim.x; ch < c.chunks; ch += blockDim.x) {
       Carried<DT, NT> x;
       x.load(c, t, ch);
       x.store(c, ch, p);
