@@ -5,7 +5,6 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct
 
 import torch
 
@@ -324,128 +323,49 @@ def combine_call(a: CombineArgs, part: str = "release", stream=None) -> None:
 
 
 # ------------------------------------------------------------------ the home rank's side
-# These calls check their tensors (device, type, shape, stride) before marshalling: a view that
-# the kernels cannot address is refused with a MoeError, and tensors on another device than the
-# current one are worked on where they are.  A decode step's calls take the GPU 3-5 us each, so
-# the host path is kept short: the argument struct is packed as bytes in the struct's own layout
-# (0.4 us; a ctypes.Structure takes four times as long to fill), the checks test for what is right
-# first, and the current stream's handle is read directly (0.1 us; a torch.cuda.Stream object
-# 1.9 us).  moe_residual_norm of 64 rows: 9.7 us a call before, 3.0 us of them the launch itself.
+# The checks of these calls' tensors (device, type, shape, stride) and their argument structs are
+# made by the compiled module _marshal, which costs a call 0.3 us where the same in Python took
+# 2-5 us beside a launch of 3 us.  Tensors on another device than the current one are worked on
+# where they are.
 
-_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
-_ROWS = (_F32, _BF16)
-_FP8 = (torch.uint8, torch.float8_e4m3fn)
-_ROWS8 = _ROWS + _FP8
-_CODE = {_F32: MOE_F32, _BF16: MOE_BF16, torch.uint8: MOE_FP8_E4M3, torch.float8_e4m3fn: MOE_FP8_E4M3}
-
-
-def _packer(cls) -> struct.Struct:
-    """Packs the fields of an argument struct in its native layout."""
-    chars = {_i32: "i", _i64: "q", _p: "P", C.c_size_t: "N", C.c_float: "f"}
-    s = struct.Struct("@" + "".join(chars[t] for _, t in cls._fields_) + "0P")
-    if s.size != C.sizeof(cls):
-        raise MoeError(f"packed layout of {cls.__name__}: {s.size} bytes, {C.sizeof(cls)} expected")
-    return s
-
-
-_HOME = {"moe_route": _packer(RouteArgs), "moe_route_backward": _packer(RouteBackwardArgs),
-         "moe_sort_rows": _packer(SortRowsArgs), "moe_merge_rows": _packer(MergeRowsArgs),
-         "moe_merge_rows_backward": _packer(MergeRowsBackwardArgs), "moe_residual_norm": _packer(ResidualNormArgs),
-         "moe_residual_norm_backward": _packer(ResidualNormBackwardArgs)}
-
-_home: dict = {}  # name -> (pack, the library's function)
-
-
-def _home_entry(name: str):
-    _home[name] = entry = _HOME[name].pack, getattr(load(), name)
-    return entry
-
-
+_marshal = None
+_HOME = ("moe_route", "moe_route_backward", "moe_sort_rows", "moe_merge_rows", "moe_merge_rows_backward",
+         "moe_residual_norm", "moe_residual_norm_backward")
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _mat(what: str, t, rows: int, cols: int, types) -> int:
-    """A [rows][cols] device tensor of one of `types` whose rows are contiguous; its pitch."""
-    if t.dtype not in types:
-        raise MoeError(f"{what}: unsupported dtype {t.dtype}")
-    if t.shape != (rows, cols):
-        raise MoeError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    s0, s1 = t.stride()
-    if s1 == 1 and s0 >= cols and rows > 1:
-        return s0
-    if s1 != 1 and cols > 1:
-        raise MoeError(f"{what}: the elements of a row must be contiguous")
-    if rows > 1 and s0 < cols:
-        raise MoeError(f"{what}: rows overlap (stride {s0} for {cols} elements)")
-    return s0 if rows > 1 else cols
+def _home():
+    """The module _marshal, with the library's entry points."""
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise MoeError(f"_marshal.so could not be loaded ({e}); build it with "
+                           "`python -m asynchronous_moe_expert_amd.build`") from None
+        m.setup(MoeError, *(C.cast(getattr(lib, name), _p).value for name in ("moe_strerror",) + _HOME))
+        _marshal = m
+    return _marshal
 
 
-def _vec(what: str, t, n: int, *types) -> int:
-    """A contiguous device tensor of one of `types` with at least n elements; its address, 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype not in types:
-        raise MoeError(f"{what}: unsupported dtype {t.dtype}")
-    if t.numel() < n:
-        raise MoeError(f"{what}: {t.numel()} elements, at least {n} expected")
-    if not t.is_contiguous():
-        raise MoeError(f"{what}: must be contiguous")
-    return t.data_ptr()
-
-
-def _each(what: str, t, T: int, K: int, dtype) -> int:
-    """A contiguous device tensor of shape (T, K); its address."""
-    if t.dtype is not dtype or t.shape != (T, K) or not t.is_contiguous():
-        _mat(what, t, T, K, (dtype,))
-        _vec(what, t, T * K, dtype)
-    return t.data_ptr()
-
-
-def _shape(what: str, t) -> tuple[int, int]:
-    s = t.shape
-    if len(s) != 2:
-        raise MoeError(f"{what}: {len(s)} dimensions, 2 expected")
-    return s
-
-
-def _room(workspace) -> int:
-    if workspace is None:
-        return 0
-    if not workspace.is_contiguous():
-        raise MoeError("workspace: must be contiguous")
-    return workspace.numel() * workspace.element_size()
-
-
-def _home_call(name: str, values, tensors, stream) -> None:
-    """One call of the library on the device that its tensors are on.  With a stream other than
-    the current one, the tensors are recorded on it, so that the allocator keeps them until the
-    call's work is done."""
-    pack, fn = _home.get(name) or _home_entry(name)
-    try:
-        args = pack(*values)
-    except (struct.error, OverflowError, TypeError) as e:
-        raise MoeError(f"{name}: an argument is over the documented limits ({e})") from None
+def _elsewhere(call, args, tensors, stream) -> None:
+    """A call on a given stream, or with tensors that are not on the current device.  On a stream
+    other than the current one the tensors are recorded, so that the allocator keeps them until
+    the call's work is done."""
     at = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise MoeError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     if at < 0:
-        raise MoeError(f"{name}: tensors must be on a GPU, got {tensors[0].device}")
-    handle = current = _raw_stream(at)
-    if stream is not None:
-        where = getattr(stream, "device", None)
-        if where is not None and where.index != at:
-            raise MoeError(f"{name}: a stream of {where} for tensors on {tensors[0].device}")
-        handle = _stream(stream)
-    if _device() == at:
-        rc = fn(args, handle)
-    else:
-        with torch.cuda.device(at):
-            rc = fn(args, handle)
-    if rc != 0:
-        _check(rc, name)
+        call(*args, 0)  # refuses: not on a GPU
+        return
+    where = getattr(stream, "device", None)
+    if where is not None and where.index != at:
+        raise MoeError(f"a stream of {where} for tensors on {tensors[0].device}")
+    current = _raw_stream(at)
+    handle = current if stream is None else _stream(stream)
+    with torch.cuda.device(at):
+        call(*args, handle)
     if handle != current:
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(handle, device=at) if handle else torch.cuda.default_stream(at)
@@ -454,121 +374,66 @@ def _home_call(name: str, values, tensors, stream) -> None:
                 t.record_stream(stream)
 
 
-def _score(score, renorm) -> tuple[int, int]:
-    if score not in (MOE_SOFTMAX, MOE_SIGMOID):
-        raise MoeError(f"score must be MOE_SOFTMAX or MOE_SIGMOID, got {score!r}")
-    return score, 1 if renorm else 0
-
-
 def moe_route(logits, expert, w, bias=None, score: int = MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
               stream=None) -> None:
     """logits [T][E] (f32 or bf16); out: expert [T][K] int32, w [T][K] f32."""
-    T, E = _shape("logits", logits)
-    K = _shape("expert", expert)[1]
-    pitch = _mat("logits", logits, T, E, _ROWS)
-    score, renorm = _score(score, renorm)
-    _home_call("moe_route", (T, E, K, logits.data_ptr(), _CODE[logits.dtype], pitch, _vec("bias", bias, E, _F32), score,
-                             renorm, scale, _each("expert", expert, T, K, _I32), _each("w", w, T, K, _F32)),
-               (logits, expert, w, bias), stream)
+    call, at = (_marshal or _home()).moe_route, logits.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(logits, expert, w, bias, score, renorm, scale, _raw_stream(at))
+    else:
+        _elsewhere(call, (logits, expert, w, bias, score, renorm, scale), (logits, expert, w, bias), stream)
 
 
 def moe_route_backward(logits, expert, dw, dlogits, err, score: int = MOE_SOFTMAX, renorm: bool = True,
                        scale: float = 1.0, stream=None) -> None:
     """expert [T][K] as moe_route gave it, dw [T][K] f32; out: dlogits [T][E] of the logits' type."""
-    T, E = _shape("logits", logits)
-    K = _shape("expert", expert)[1]
-    pitch = _mat("logits", logits, T, E, _ROWS)
-    dpitch = _mat("dlogits", dlogits, T, E, (logits.dtype,))
-    score, renorm = _score(score, renorm)
-    _home_call("moe_route_backward",
-               (T, E, K, logits.data_ptr(), _CODE[logits.dtype], pitch, _each("expert", expert, T, K, _I32),
-                _each("dw", dw, T, K, _F32), score, renorm, scale, dlogits.data_ptr(), dpitch,
-                _vec("err", err, 1, _I32)), (logits, expert, dw, dlogits, err), stream)
+    call, at = (_marshal or _home()).moe_route_backward, logits.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(logits, expert, dw, dlogits, err, score, renorm, scale, _raw_stream(at))
+    else:
+        t = (logits, expert, dw, dlogits, err)
+        _elsewhere(call, t + (score, renorm, scale), t, stream)
 
 
 def moe_sort_rows_workspace_size(n_max: int) -> int:
     return load().moe_sort_rows_workspace_size(n_max)
 
 
-def _groups(H: int, group: int) -> int:
-    if group not in (0, 32, 64, 128):
-        raise MoeError(f"group must be 0, 32, 64 or 128, got {group}")
-    return (H + group - 1) // group if group else 1
-
-
 def moe_sort_rows(expert, E_loc: int, x, xs, perm, pos, counts, offsets, err, workspace, expert_base: int = 0,
                   row_slot=None, x_scale=None, group: int = 0, stream=None) -> None:
     """expert [T][K] int32; x [T][H] (f32, bf16, or fp8 with x_scale [T][groups] f32), xs [T * K][H]
     of x's type (bf16 for fp8); xs None: the index alone (x may be None then).  perm and row_slot
-    are optional."""
-    T, K = _shape("expert", expert)
-    n = T * K
-    H, code, xp, xsp, xd, xsd, sd = 8, MOE_BF16, 8, 8, 0, 0, 0
-    if xs is not None:
-        if x is None:
-            raise MoeError("x: required with xs")
-        H = _shape("xs", xs)[1]
-        xp = _mat("x", x, T, H, _ROWS8)
-        code = _CODE[x.dtype]
-        xsp = _mat("xs", xs, n, H, (_BF16,) if code == MOE_FP8_E4M3 else (x.dtype,))
-        xd, xsd = x.data_ptr(), xs.data_ptr()
-        if code == MOE_FP8_E4M3:
-            if x_scale is None:
-                raise MoeError("x_scale: required for fp8 rows")
-            sd = _vec("x_scale", x_scale, T * _groups(H, group), _F32)
-        else:
-            x_scale = None
+    are optional, and so is the workspace where moe_sort_rows_workspace_size(T * K) is 0."""
+    call, at = (_marshal or _home()).moe_sort_rows, expert.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(expert, E_loc, x, xs, perm, pos, counts, offsets, err, workspace, expert_base, row_slot, x_scale, group,
+             _raw_stream(at))
     else:
-        x = x_scale = None
-    _home_call("moe_sort_rows",
-               (T, K, H, expert_base, E_loc, _each("expert", expert, T, K, _I32), xd, code, xp, sd, group, xsd, xsp,
-                _vec("perm", perm, n, _I32), _vec("pos", pos, n, _I32), _vec("counts", counts, E_loc, _I32),
-                _vec("offsets", offsets, E_loc + 1, _I32), _vec("row_slot", row_slot, n, _I32),
-                _vec("err", err, 1, _I32), 0 if workspace is None else workspace.data_ptr(), _room(workspace)),
-               (expert, x, xs, perm, pos, counts, offsets, err, workspace, row_slot, x_scale), stream)
-
-
-def _positions(pos, w, T: int) -> tuple[int, int, int]:
-    """pos: int32, T x K elements in token order ([T][K] or flat), w f32 like it or None; K and their
-    addresses."""
-    n = pos.numel()
-    K = n // T if T else (pos.shape[-1] if pos.dim() > 1 else 1)
-    if n != T * K:
-        raise MoeError(f"pos: {n} elements are not a whole number for each of {T} tokens")
-    if w is not None and w.numel() != n:
-        raise MoeError(f"w: {w.numel()} elements, {n} expected")
-    return K, _vec("pos", pos, n, _I32), _vec("w", w, n, _F32)
+        _elsewhere(call, (expert, E_loc, x, xs, perm, pos, counts, offsets, err, workspace, expert_base, row_slot,
+                          x_scale, group),
+                   (expert, x, xs, perm, pos, counts, offsets, err, workspace, row_slot, x_scale), stream)
 
 
 def moe_merge_rows(rows, pos, w, out, err, stream=None) -> None:
     """rows [n_rows][H]; pos (int32) and w (f32, or None: 1) [T][K]; out [T][H].  f32 or bf16 each.
     With the gradient of moe_sort_rows' xs as rows and w None, out is the gradient of its x."""
-    T, H = _shape("out", out)
-    K, posd, wd = _positions(pos, w, T)
-    n_rows = _shape("rows", rows)[0]
-    rp = _mat("rows", rows, n_rows, H, _ROWS)
-    op = _mat("out", out, T, H, _ROWS)
-    _home_call("moe_merge_rows", (T, K, H, rows.data_ptr(), _CODE[rows.dtype], rp, n_rows, posd, wd, out.data_ptr(),
-                                  _CODE[out.dtype], op, _vec("err", err, 1, _I32)), (rows, pos, w, out, err), stream)
+    call, at = (_marshal or _home()).moe_merge_rows, rows.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(rows, pos, w, out, err, _raw_stream(at))
+    else:
+        t = (rows, pos, w, out, err)
+        _elsewhere(call, t, t, stream)
 
 
 def moe_merge_rows_backward(dout, rows, pos, w, drows, dw, err, stream=None) -> None:
     """dout [T][H]; rows and drows [n_rows][H] of one type; pos, w and dw [T][K].  drows or dw (and
     then rows) may be None."""
-    T, H = _shape("dout", dout)
-    K, posd, wd = _positions(pos, w, T)
-    dp = _mat("dout", dout, T, H, _ROWS)
-    one = rows if rows is not None else drows
-    if one is None or (drows is None and dw is None) or (dw is not None and rows is None):
-        raise MoeError("moe_merge_rows_backward: drows, or dw with rows, must be given")
-    n_rows, rp, drp, rd, drd = _shape("rows", one)[0], H, H, 0, 0
-    if rows is not None:
-        rp, rd = _mat("rows", rows, n_rows, H, _ROWS), rows.data_ptr()
-    if drows is not None:
-        drp, drd = _mat("drows", drows, n_rows, H, (rows.dtype,) if rows is not None else _ROWS), drows.data_ptr()
-    _home_call("moe_merge_rows_backward",
-               (T, K, H, dout.data_ptr(), _CODE[dout.dtype], dp, rd, _CODE[one.dtype], rp, n_rows, posd, wd, drd, drp,
-                _vec("dw", dw, T * K, _F32), _vec("err", err, 1, _I32)), (dout, rows, pos, w, drows, dw, err), stream)
+    call, at = (_marshal or _home()).moe_merge_rows_backward, dout.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(dout, rows, pos, w, drows, dw, err, _raw_stream(at))
+    else:
+        t = (dout, rows, pos, w, drows, dw, err)
+        _elsewhere(call, t, t, stream)
 
 
 def moe_residual_norm(x, residual, gamma, eps: float, out, residual_out=None, rstd=None, out_scale=None,
@@ -576,29 +441,13 @@ def moe_residual_norm(x, residual, gamma, eps: float, out, residual_out=None, rs
     """x, residual (optional) [T][H]; gamma [H]; out [T][H] f32, bf16 or fp8 (then out_scale [T][groups]
     f32).  Optional outputs: residual_out [T][H], rstd [T].  row_list [T], row_count [1] (int32): only
     these rows, with err."""
-    T, H = _shape("x", x)
-    xp = _mat("x", x, T, H, _ROWS)
-    op = _mat("out", out, T, H, _ROWS8)
-    rt, rp, rop, rd, rod, sd = x.dtype, H, H, 0, 0, 0
-    if residual is not None:
-        rt = residual.dtype
-        rp, rd = _mat("residual", residual, T, H, _ROWS), residual.data_ptr()
-    if residual_out is not None:
-        if residual is None:
-            rt = residual_out.dtype
-        rop, rod = _mat("residual_out", residual_out, T, H, (rt,) if residual is not None else _ROWS), residual_out.data_ptr()
-    oc = _CODE[out.dtype]
-    if oc == MOE_FP8_E4M3:
-        if out_scale is None:
-            raise MoeError("out_scale: required for fp8 output")
-        sd = _vec("out_scale", out_scale, T * _groups(H, group), _F32)
+    call, at = (_marshal or _home()).moe_residual_norm, x.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(x, residual, gamma, eps, out, residual_out, rstd, out_scale, group, row_list, row_count, err,
+             _raw_stream(at))
     else:
-        out_scale = None
-    _home_call("moe_residual_norm",
-               (T, H, x.data_ptr(), _CODE[x.dtype], xp, rd, _CODE[rt], rp, _vec("gamma", gamma, H, _F32, _BF16),
-                _CODE[gamma.dtype], eps, out.data_ptr(), oc, op, sd, group, rod, rop, _vec("rstd", rstd, T, _F32),
-                _vec("row_list", row_list, T, _I32), _vec("row_count", row_count, 1, _I32), _vec("err", err, 1, _I32)),
-               (x, residual, gamma, out, residual_out, rstd, out_scale, row_list, row_count, err), stream)
+        _elsewhere(call, (x, residual, gamma, eps, out, residual_out, rstd, out_scale, group, row_list, row_count, err),
+                   (x, residual, gamma, out, residual_out, rstd, out_scale, row_list, row_count, err), stream)
 
 
 def moe_residual_norm_backward_workspace_size(H: int) -> int:
@@ -610,14 +459,9 @@ def moe_residual_norm_backward(dout, h, gamma, rstd, dx, dgamma, workspace, dres
     """dout [T][H], h [T][H] (the forward's residual_out, or x), rstd [T]; out: dx [T][H] of dout's type,
     dresidual [T][H] of h's, dgamma [H] f32 (with the workspace); each may be None.  dres [T][H] of h's
     type is added to dx and dresidual."""
-    T, H = _shape("dout", dout)
-    dp = _mat("dout", dout, T, H, _ROWS)
-    hp = _mat("h", h, T, H, _ROWS)
-    p = []
-    for what, t, like in (("dres", dres, h), ("dx", dx, dout), ("dresidual", dresidual, h)):
-        p += (0, H) if t is None else (t.data_ptr(), _mat(what, t, T, H, (like.dtype,)))
-    _home_call("moe_residual_norm_backward",
-               (T, H, dout.data_ptr(), _CODE[dout.dtype], dp, h.data_ptr(), _CODE[h.dtype], hp,
-                _vec("gamma", gamma, H, _F32, _BF16), _CODE[gamma.dtype], _vec("rstd", rstd, T, _F32), *p,
-                _vec("dgamma", dgamma, H, _F32), 0 if workspace is None else workspace.data_ptr(), _room(workspace)),
-               (dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual), stream)
+    call, at = (_marshal or _home()).moe_residual_norm_backward, dout.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual, _raw_stream(at))
+    else:
+        t = (dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual)
+        _elsewhere(call, t, t, stream)

@@ -1,14 +1,19 @@
-"""Builds libmoestep.so (HIP kernels + C ABI) in-tree for gfx950 with hipcc."""
+"""Builds libmoestep.so (HIP kernels + C ABI) in-tree for gfx950 with hipcc, and _marshal.so (the
+binding's compiled part, host code only) with g++."""
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmoestep.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -25,21 +30,50 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
 
 
-def build(verbose: bool = False) -> str:
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = LIB + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), *sources(), "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     msgs = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if noise not in l)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msgs}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{msgs}")
     if msgs.strip() and verbose:
         print(msgs, file=sys.stderr)
-    os.replace(tmp, LIB)
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles every source (side by side) and links; each file is put in its place whole."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    compiled = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(prefix="moestep_") as tmp, \
+            concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(tmp, os.path.basename(f) + ".o") for f in sources()]
+        jobs = [pool.submit(_run, [hipcc, *compiled, "-I", os.path.join(ROOT, "include"), "-c", f, "-o", o], verbose)
+                for f, o in zip(sources(), objects)]
+        jobs.append(pool.submit(build_marshal, verbose))
+        for j in jobs:
+            j.result()
+        _run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", LIB + ".tmp"], verbose)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
+
+
+def build_marshal(verbose: bool = False) -> str:
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(at, "include"),
+           "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(PKG, "csrc", "marshal.cpp"), "-o", tmp,
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    _run(cmd, verbose)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

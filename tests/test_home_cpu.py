@@ -15,9 +15,9 @@ P = 4096  # an aligned address that no refused call touches
 
 @pytest.fixture(scope="module")
 def lib():
-    if not os.path.exists(M.LIB_PATH):
-        from asynchronous_moe_expert_amd import build
+    from asynchronous_moe_expert_amd import build
 
+    if not (os.path.exists(M.LIB_PATH) and os.path.exists(build.MARSHAL)):
         build.build()
     return M.load()
 
@@ -105,7 +105,7 @@ def _t(*shape, dtype=torch.bfloat16):
     return torch.zeros(*shape, dtype=dtype)
 
 
-def test_binding_refuses_what_the_kernels_cannot_address():
+def test_binding_refuses_what_the_kernels_cannot_address(lib):
     i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
     err = _t(1, dtype=i32)
     e, w, l = _t(4, 2, dtype=i32), _t(4, 2, dtype=f32), _t(4, 16, dtype=f32)
