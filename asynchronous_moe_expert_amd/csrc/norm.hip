@@ -73,11 +73,28 @@ __device__ __forceinline__ float run_max(float v, int lanes) {
 
 __device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax / 448.f, FLT_MIN) : 1.f; }
 
-// v / s through s's reciprocal and one correction, so that a code next to a border falls where the
-// quotient's own rounding puts it (the product alone moved 1.5 times as many codes)
+// v / s through s's reciprocal and one correction (the quotient's own rounding)
 __device__ __forceinline__ float over(float v, float s, float inv) {
   const float q = v * inv;
   return fmaf(fmaf(-q, s, v), inv, q);
+}
+
+// How a group's values become 8-bit codes.  r scales all of a row, so it cancels in y / scale: the
+// code of z = h gamma is z (448 / max|z|), two roundings where y / scale has six, and fewer codes
+// fall on the wrong side of a border (of 201 million codes 2782 are not those of a 64-bit
+// evaluation, 4455 with y / scale in fp32).  z is used while r and the group's max|z| are of ordinary size
+// (`plain` rows: 2^-40 <= r <= 2^40); other rows hold y itself, and groups past the limits go
+// through y / scale.
+struct Coding {
+  float scale, mul, inv;  // inv != 0: through y = value * mul, over(y, scale, inv)
+  __device__ __forceinline__ float operator()(float v) const {
+    return inv == 0.f ? v * mul : over(v * mul, scale, inv);
+  }
+};
+__device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
+  if (plain && amax >= 0x1p-60f && amax <= 0x1p80f) return {amax * r / 448.f, 448.f / amax, 0.f};
+  const float back = plain ? r : 1.f, s = scale_of(amax * back);
+  return {s, back, 1.f / s};
 }
 
 // A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + 256, ...
@@ -132,6 +149,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
     const float r = 1.f / sqrtf(group_sum(ss, s_a[par]) / (float)j.H + j.eps);
     if (j.rstd && threadIdx.x == 0) j.rstd[t] = r;
     char* out = (char*)j.out + row_bytes<OT>(t, j.out_pitch);
+    const bool plain = OT == MOE_FP8_E4M3 && r >= 0x1p-40f && r <= 0x1p40f;
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -141,7 +159,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
         float g[8];
         gamma8(j.gamma, j.gamma_f32, at, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[c][e] *= r * g[e];
+        for (int e = 0; e < 8; ++e) h[c][e] *= plain ? g[e] : r * g[e];
         if constexpr (OT != MOE_FP8_E4M3) st8<OT, S == kThrough>(out, at, h[c]);
       }
       if constexpr (OT == MOE_FP8_E4M3) {
@@ -150,31 +168,30 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
         for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(h[c][e]));
         amax = fmaxf(amax, a);
         if (j.group_lanes) {
-          const float s = scale_of(run_max(a, j.group_lanes));
+          const Coding coded = coding_of(run_max(a, j.group_lanes), r, plain);
           if (at < j.H) {
-            const float inv = 1.f / s;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] = over(h[c][e], s, inv);
+            for (int e = 0; e < 8; ++e) h[c][e] = coded(h[c][e]);
             st8<OT, S == kThrough>(out, at, h[c]);
             const int lane = threadIdx.x & (j.group_lanes - 1);
-            if (lane == 0) j.out_scale[(int64_t)t * j.groups + at / (j.group_lanes * 8)] = s;
+            if (lane == 0) j.out_scale[(int64_t)t * j.groups + at / (j.group_lanes * 8)] = coded.scale;
           }
         }
       }
     }
     if constexpr (OT == MOE_FP8_E4M3) {
       if (!j.group_lanes) {
-        const float s = scale_of(group_max(amax, s_b[par])), inv = 1.f / s;
+        const Coding coded = coding_of(group_max(amax, s_b[par]), r, plain);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
           if (at < j.H) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] = over(h[c][e], s, inv);
+            for (int e = 0; e < 8; ++e) h[c][e] = coded(h[c][e]);
             st8<OT, S == kThrough>(out, at, h[c]);
           }
         }
-        if (threadIdx.x == 0) j.out_scale[t] = s;
+        if (threadIdx.x == 0) j.out_scale[t] = coded.scale;
       }
     }
     par ^= 1;
