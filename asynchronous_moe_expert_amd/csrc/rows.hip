@@ -256,9 +256,14 @@ __global__ __launch_bounds__(512) void sort_copy_kernel(CopyJob c, int T, const 
 // (key, pair), so each token's workgroup stages all n pairs' (key, pair) in LDS, counts those below
 // each of its own K pairs (a wave takes the positions wave, wave + waves, ...) and then copies its
 // row, whose first chunks are loaded meanwhile; the last workgroup writes counts, offsets and what
-// lies past the last row.  No workgroup waits for another.  The count is n T K / 64 wave steps in
-// all, which is why longer queues go through the index launches.
-constexpr int kShort = 4096;
+// lies past the last row.  No workgroup waits for another.  Every token stages and counts n pairs,
+// so the work grows with T n, and past 2^22 the index launches take over.  Microseconds short / long,
+// rows of 2880 bf16 (K = 8: 4096): 300 tokens x 4 4.6 / 9.0, 512 x 4 6.1 / 9.9, 1000 x 4 10.5 / 12.1,
+// 2000 x 1 9.9 / 11.9, 512 x 8 11.4 / 13.5; 1500 x 4 19.9 / 14.4, 4000 x 1 23.1 / 16.8, 1000 x 8 19.9 / 18.3.
+constexpr int kShort = 4096;            // pairs that the LDS staging holds
+constexpr int64_t kShortWork = 1 << 22;
+constexpr int kShortAny = 2048;         // pairs that are short whatever K is
+static_assert((int64_t)kShortAny * kShortAny <= kShortWork, "");
 
 template <int DT>
 __global__ __launch_bounds__(512) void sort_short_kernel(SortJob j, CopyJob c) {
@@ -537,7 +542,7 @@ static bool f32_or_bf16(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 using namespace moe;
 
 extern "C" size_t moe_sort_rows_workspace_size(int32_t n_max) {
-  return n_max > kShort ? (size_t)kSegs * kMaxEloc * sizeof(int32_t) : 0;
+  return n_max > kShortAny ? (size_t)kSegs * kMaxEloc * sizeof(int32_t) : 0;
 }
 
 static int check_sort(const moe_sort_rows_args* a) {
@@ -582,7 +587,7 @@ template <int DT>
 static int sort_rows(const moe_sort_rows_args* a, const SortJob& j, hipStream_t stream) {
   const CopyJob c = make_copy_job(a);
   const unsigned block = c.chunks ? row_threads(c.chunks) : 256;
-  if (j.n <= kShort) {
+  if (j.n <= kShort && (int64_t)j.T * j.n <= kShortWork) {
     const unsigned b = block < 256 ? 256 : block;
     return launch(sort_short_kernel<DT>, (unsigned)j.T + 1, b, stream, j, c);
   }

@@ -191,7 +191,8 @@ def choices(rng, T, K, E, kind="some"):
 
 SORTS = [(1, 1, 1, 8, "some"), (1, 8, 256, 64, "some"), (3, 2, 5, 2056, "one"), (64, 4, 128, 2880, "some"),
          (257, 4, 8, 512, "skewed"), (511, 8, 60, 136, "some"), (513, 8, 60, 136, "skewed"), (1025, 1, 7, 72, "one"),
-         (2000, 6, 256, 264, "skewed"), (70001, 2, 33, 8, "some"), (9000, 32, 200, 16, "skewed"), (700, 16, 8, 40, "one")]
+         (2000, 6, 256, 264, "skewed"), (70001, 2, 33, 8, "some"), (9000, 32, 200, 16, "skewed"), (700, 16, 8, 40, "one"), (2048, 1, 64, 24, "some"), (2049, 1, 64, 24, "skewed"),
+         (1024, 4, 128, 4104, "some"), (128, 32, 256, 72, "skewed"), (300000, 1, 256, 8, "skewed")]
 
 
 @pytest.mark.parametrize("T,K,E,H,kind", SORTS)

@@ -97,7 +97,9 @@ def test_workspace_refusals_of_long_queues(lib):
         assert lib.moe_sort_rows(C.byref(a), None) == WORKSPACE
     a = N.SortRowsArgs(**dict(SORT, T=1 << 19, K=2, workspace=P + 4))
     assert lib.moe_sort_rows(C.byref(a), None) == ALIGN
-    assert M.moe_sort_rows_workspace_size(0) == 0 and M.moe_sort_rows_workspace_size(1 << 24) <= 1 << 18
+    a = N.SortRowsArgs(**dict(SORT, T=2049, K=1, workspace=0))
+    assert lib.moe_sort_rows(C.byref(a), None) == WORKSPACE
+    assert M.moe_sort_rows_workspace_size(0) == M.moe_sort_rows_workspace_size(2048) == 0 and M.moe_sort_rows_workspace_size(1 << 24) <= 1 << 18
     assert M.moe_residual_norm_backward_workspace_size(2880) == 2048 * 2880
 
 
