@@ -22,7 +22,7 @@ __device__ __forceinline__ void st(V* p, V v) {
 }
 
 // A row is handled in chunks of eight elements: 16 bytes of bf16, two 16-byte runs of fp32, 8
-// bytes of fp8.  ld8 / st8 take the element offset of the chunk from the row's start.
+// bytes of fp8.  load and st8 take the element offset of the chunk from the row's start.
 template <int DT>
 struct Chunk;
 

@@ -92,7 +92,7 @@ class Call {
   float real() {
     const double v = PyFloat_AsDouble(a_[i_++]);
     if (v == -1.0 && PyErr_Occurred()) throw Refused{};
-    if (std::isfinite(v) && std::fabs(v) > FLT_MAX) refuse("a number of %s is over the documented limits", "that size");
+    if (std::isfinite(v) && std::fabs(v) > FLT_MAX) refuse("a number that fp32 cannot hold");
     return (float)v;
   }
 

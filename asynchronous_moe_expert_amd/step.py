@@ -203,6 +203,8 @@ class ExpertLayer:
         self.how = dict(score=score, renorm=renorm, scale=scale)
         dev = torch.device(device)
         n = max(T_max * K, 1)
+        if T_max < 0 or n > 1 << 24:
+            raise N.MoeError(f"ExpertLayer: T_max {T_max} with K {K} is over the documented limits")
         self._expert = torch.empty(n, dtype=torch.int32, device=dev)
         self._w = torch.empty(n, dtype=torch.float32, device=dev)
         self.pos = torch.empty(n, dtype=torch.int32, device=dev)
@@ -223,18 +225,26 @@ class ExpertLayer:
         return self.E
 
     def run(self, x, logits, out, bias=None, stream=None) -> None:
-        """x [T][H] in act_dtype, logits [T][E]; out [T][H]: sum_j w_j E_j(x)."""
+        """x [T][H] in act_dtype (for bf16 under 2 GiB, as gather-on-load asks), logits [T][E];
+        out [T][H]: sum_j w_j E_j(x)."""
+        if x.device != self.y.device:
+            raise N.MoeError(f"ExpertLayer: x on {x.device}, the layer on {self.y.device}")
+        if torch.cuda.current_device() != self.y.device.index:
+            with torch.cuda.device(self.y.device):
+                return self.run(x, logits, out, bias=bias, stream=stream)
         T = x.shape[0]
         n = T * self.K
         if T > self.T_max:
             raise N.MoeError(f"ExpertLayer: {T} tokens, built for {self.T_max}")
-        if x.shape[1] != self.H or x.dtype != _TORCH[self.act_dtype] or logits.shape[0] != T:
+        if x.shape != (T, self.H) or x.stride(1) != 1 or x.dtype != _TORCH[self.act_dtype] or logits.shape != (T, self.E):
             raise N.MoeError(f"ExpertLayer: x {tuple(x.shape)} {x.dtype} with logits {tuple(logits.shape)}")
         self.expert, self.w = self._expert[:n].view(T, self.K), self._w[:n].view(T, self.K)
         N.moe_route(logits, self.expert, self.w, bias=bias, stream=stream, **self.how)
         N.moe_sort_rows(self.expert, self.E, None, None, None, self.pos, self.counts, self.offsets, self.err,
                         self.sort_ws, row_slot=self.row_slot, stream=stream)
         if n:
+            if hasattr(stream, "cuda_stream"):
+                x.record_stream(stream)
             N.moe_expert_ffn_grouped(n, self.E, self.H, self.I, self.act_dtype, self.w_dtype, None, self.offsets,
                                      self.w_gu, self.w_d, self.y, self.workspace, self.s_gate, self.s_up, self.s_down,
                                      stream=stream, gather=(None, None, x, self.row_slot))

@@ -363,7 +363,8 @@ size_t moe_combine_noalloc_max_arrivals(void);
  *     side by side) take one each.  Its contents need no preparation and mean nothing afterwards.
  *   - Every sum is fp32 in a fixed order: the same inputs give the same bits.
  *   - Rows are [T][pitch], pitch >= the row's length in elements; fp32 and bf16 rows are 16-byte
- *     aligned (pointer and pitch), fp8 rows 8-byte.  H is a multiple of 8 and at most 65536.
+ *     aligned (pointer and pitch), fp8 rows 8-byte; other arrays are aligned as their elements.
+ *     H is a multiple of 8 and at most 65536.
  *   - Sizes are limited to T * K <= 2^24 and T <= 2^24; offsets of elements are 64 bits wide.
  *   - A call with T = 0 writes what does not depend on a token (counts, offsets, dgamma).
  */

@@ -49,6 +49,25 @@ def test_expert_layer(act, wt, T, E, K, H, I):
     ref = O.merge_rows(y, pos.reshape(T, K), weight)
     assert not ref[3].any()
     assert row_rel_err(decode_tensor(out), ref) <= TOL["fp8" if wt == "fp8" else act]
+    # on another stream, and with fewer tokens from a wider buffer
+    s = torch.cuda.Stream()
+    wide = torch.zeros(7, H + 64, dtype=tdt, device="cuda")
+    wide[:, :H] = x[:7]
+    few, again = torch.empty(7, H, dtype=tdt, device="cuda"), torch.empty_like(out)
+    s.wait_stream(torch.cuda.current_stream())
+    layer.run(x, logits, again, stream=s)
+    s.synchronize()
+    assert torch.equal(again, out)
+    layer.run(wide[:, :H], logits[:7], few)
+    assert row_rel_err(decode_tensor(few), ref[:7]) <= TOL["fp8" if wt == "fp8" else act]
+    layer.run(x[:0], logits[:0], out[:0])
+    torch.cuda.synchronize()
+    assert not layer.offsets.any()
+    for bad in (torch.empty(H, T, dtype=tdt, device="cuda").t(), x[:5], x[:, :H - 8], x.double()):
+        with pytest.raises(M.MoeError, match="logits"):
+            layer.run(bad, logits, out)
+    with pytest.raises(M.MoeError, match="layer on"):
+        layer.run(x.cpu(), logits, out)
     with pytest.raises(M.MoeError, match="tokens"):
         layer.run(torch.empty(T + 6, H, dtype=tdt, device="cuda"), logits, out)
 
@@ -280,3 +299,110 @@ def test_offsets_past_32_bits():
     M.moe_route(logits, e1, w1)
     M.moe_route(logits.clone(), e2, w2)
     assert torch.equal(e1, e2) and torch.equal(w1, w2)
+
+
+# Calls that move 96 MiB of rows or more read them non-temporally, from 192 MiB on they write so too.
+LARGE = [(5000, 4, 2880), (9600, 4, 2880)]
+
+
+@pytest.mark.parametrize("T,K,H", LARGE)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_large_calls_give_the_bits_of_small_ones(T, K, H, dtype):
+    T = T // 2 if dtype == F32 else T
+    print("large calls", T, K, H, dtype, flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    e = lambda *s, dt=F32: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    n, E, err = T * K, 64, e(1, dt=I32)
+    expert = torch.randint(-1, E, (T, K), generator=g, device="cuda", dtype=I32)
+    x, xs, perm, pos = r(T, H), e(n, H, dt=dtype), e(n, dt=I32), e(n, dt=I32)
+    counts, offsets, slot, ws = e(E, dt=I32), e(E + 1, dt=I32), e(n, dt=I32), e(1 << 18, dt=torch.uint8)
+    M.moe_sort_rows(expert, E, x, xs, perm, pos, counts, offsets, err, ws, row_slot=slot)
+    total = int(offsets[E])
+    assert total == int((expert >= 0).sum()) and torch.equal(xs[:total], x[slot[:total].long()]) and not xs[total:].any()
+    w, out, part = torch.rand(T, K, generator=g, device="cuda"), e(T, H, dt=dtype), e(300, H, dt=dtype)
+    M.moe_merge_rows(xs, pos, w, out, err)
+    dout, drows, dw, dw2 = r(T, H), e(n, H, dt=dtype), e(T, K), e(300, K)
+    M.moe_merge_rows_backward(dout, xs, pos, w, drows, dw, err)
+    small = e(n, H, dt=dtype)
+    for a in range(0, T, 300):
+        b = min(T, a + 300)
+        p = pos[a * K:b * K]
+        M.moe_merge_rows(xs, p, w[a:b], part[:b - a], err)
+        M.moe_merge_rows_backward(dout[a:b], xs, p, w[a:b], small, dw2[:b - a], err)
+        assert torch.equal(part[:b - a], out[a:b]) and torch.equal(dw2[:b - a], dw[a:b])
+    assert torch.equal(small, drows) and sync_err(err) == 0
+
+
+@pytest.mark.parametrize("T", [3500, 9000, 14000])
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (BF16, torch.float8_e4m3fn), (F32, F32)])
+def test_large_norms_give_the_bits_of_small_ones(T, dtype, out_dtype):
+    H, group = 4096, 128
+    T = T // 2 if dtype == F32 else T
+    print("large norms", T, dtype, out_dtype, flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    z = lambda *s, dt=dtype: torch.zeros(*s, dtype=torch.uint8 if dt.itemsize == 1 else dt, device="cuda").view(dt)  # noqa: E731
+    x, res, gamma = r(T, H), r(T, H), r(H)
+    fp8 = out_dtype.itemsize == 1
+    out, ro, rstd, sc = z(T, H, dt=out_dtype), z(T, H), z(T, dt=F32), z(T, H // group, dt=F32) if fp8 else None
+    M.moe_residual_norm(x, res, gamma, 1e-5, out, residual_out=ro, rstd=rstd, out_scale=sc, group=group)
+    dout, dx, dgamma, ws = r(T, H), z(T, H), z(H, dt=F32), z(2048 * H, dt=torch.uint8)
+    M.moe_residual_norm_backward(dout, ro, gamma, rstd, dx, dgamma, ws, dres=res)
+    for a in range(0, T, 500):
+        b = min(T, a + 500)
+        o2, ro2, rs2, sc2 = z(b - a, H, dt=out_dtype), z(b - a, H), z(b - a, dt=F32), z(b - a, H // group, dt=F32) if fp8 else None
+        M.moe_residual_norm(x[a:b], res[a:b], gamma, 1e-5, o2, residual_out=ro2, rstd=rs2, out_scale=sc2, group=group)
+        dx2 = z(b - a, H)
+        M.moe_residual_norm_backward(dout[a:b], ro[a:b], gamma, rstd[a:b], dx2, None, None, dres=res[a:b])
+        assert torch.equal(o2.view(torch.uint8) if fp8 else o2, out[a:b].view(torch.uint8) if fp8 else out[a:b])
+        assert torch.equal(ro2, ro[a:b]) and torch.equal(rs2, rstd[a:b]) and torch.equal(dx2, dx[a:b])
+        assert not fp8 or torch.equal(sc2, sc[a:b])
+    ref, size = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 1000):
+        t = dout[a:a + 1000].double() * ro[a:a + 1000].double() * rstd[a:a + 1000].double()[:, None]
+        ref += t.sum(0)
+        size += t.abs().sum(0)
+    # runs of ceil(T / 512) tokens, then 512 partial sums in runs of 8 and a tree; 3 roundings a term
+    assert ((dgamma.double() - ref).abs() <= (-(-T // 512) + 20) * 2.0 ** -24 * size).all()
+
+
+def test_the_largest_number_of_tokens():
+    """T K = 2^24 pairs in every operator, rows of 8 columns."""
+    T, H = 1 << 24, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    e = lambda *s, dt=F32: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    err, ws = e(1, dt=I32), e(1 << 18, dt=torch.uint8)
+    logits = torch.randn(T, 2, generator=g, device="cuda")
+    expert, w = e(T, 1, dt=I32), e(T, 1)
+    M.moe_route(logits, expert, w, renorm=False)
+    assert torch.equal(expert[:, 0].long(), (logits[:, 1] > logits[:, 0]).long())
+    dl = e(T, 2)
+    M.moe_route_backward(logits, expert, w, dl, err, renorm=False)
+    assert (dl.sum(1).abs() <= 2.0 ** -20).all()  # the two gradients of a softmax of two cancel
+    del dl, logits
+    wide = torch.randint(0, 256, (T, 1), generator=g, device="cuda", dtype=I32)
+    x, xs = torch.randn(T, H, generator=g, device="cuda").to(BF16), e(T, H, dt=BF16)
+    perm, pos, counts, offsets = e(T, dt=I32), e(T, dt=I32), e(256, dt=I32), e(257, dt=I32)
+    M.moe_sort_rows(wide, 256, x, xs, perm, pos, counts, offsets, err, ws)
+    order = torch.sort(wide[:, 0], stable=True).indices
+    assert torch.equal(perm.long(), order) and torch.equal(xs, x[order])
+    assert torch.equal(counts.long(), torch.bincount(wide[:, 0].long(), minlength=256))
+    out, dw = e(T, H, dt=BF16), e(T, 1)
+    M.moe_merge_rows(xs, pos, None, out, err)
+    assert torch.equal(out, x)
+    M.moe_merge_rows_backward(x, xs, pos, None, out, dw, err)
+    assert torch.equal(out, xs)
+    gamma, rstd, dgamma = torch.ones(H, device="cuda"), e(T), e(H)
+    M.moe_residual_norm(x, None, gamma, 1e-5, out, rstd=rstd)
+    few = e(1000, H, dt=BF16)
+    M.moe_residual_norm(x[-1000:], None, gamma, 1e-5, few)
+    assert torch.equal(out[-1000:], few)
+    M.moe_residual_norm_backward(out, x, gamma, rstd, xs, dgamma, e(2048 * H, dt=torch.uint8))
+    ref = (out.double() * x.double() * rstd.double()[:, None]).sum(0)
+    # terms of one sign in chains of 2^15: off by 2^15 2^-24 at most, and 30 additions and roundings more
+    assert ((dgamma.double() - ref).abs() <= (2 ** 15 + 30) * 2.0 ** -24 * ref.abs()).all()
+    assert sync_err(err) == 0
