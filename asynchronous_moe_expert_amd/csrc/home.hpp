@@ -174,22 +174,26 @@ inline bool aligned_rows(const void* p, int64_t pitch, int esz, int to) {
 inline int chunk_align(int dt) { return dt == MOE_FP8_E4M3 ? 8 : 16; }
 
 // How a call that reads and writes so many bytes of rows goes through the caches: kNear plain,
-// kReadOnce with NT loads, kThrough with NT loads and stores.  Measured on rows of 2880 and 4096 bf16,
-// microseconds alone / with a kernel after it that reads the output:
-//                              kNear        kReadOnce    kThrough
-//   merge      64 MiB moved    11.9 /  19.1  13.8 /  21.1  12.4 /  22.9
-//             112 MiB          26.1 /  33.0  25.0 /  32.6  23.3 /  34.7
-//             225 MiB          49.0 /  61.0  46.6 /  56.3  44.1 /  57.1
-//             450 MiB          94.0 / 115.1  91.6 / 110.3  86.1 / 110.1
-//   norm       64 MiB          12.7 /  21.3  14.9 /  23.5  13.6 /  25.6
-//             128 MiB          26.6 /  37.3  25.1 /  36.7  24.3 /  37.6
-//             256 MiB          47.2 /  63.8  47.9 /  60.4  44.7 /  60.8
-//             512 MiB          91.0 / 122.6  89.9 / 116.2  85.8 / 116.2
-// Below 96 MiB what was written lately is still near and a plain load finds it; from 192 MiB on an
-// output does not stay near anyway (the last-level cache holds 256 MiB).
+// kReadOnce with NT loads, kThrough with NT loads and stores.  Measured, microseconds alone / with a
+// kernel after it that reads the output (merge: four rows of 2880 bf16 per token; norm: 4096 bf16 with
+// its residual in and out):
+//                              kNear          kReadOnce      kThrough
+//   merge      56 MiB moved    11.9 /  19.0   13.7 /  21.1   12.5 /  23.0
+//             112 MiB          26.7 /  33.3   24.9 /  32.5   23.3 /  34.6
+//             225 MiB          49.4 /  60.1   46.4 /  56.7   44.1 /  57.4
+//             450 MiB          94.5 / 115.1   90.9 / 109.8   85.7 / 109.5
+//   its      101 MiB           23.0 /  31.9   20.9 /  31.5   21.7 /  35.2
+//   gradient 202 MiB           44.1 /  64.4   37.0 /  56.9   41.0 /  64.8
+//            405 MiB           85.0 / 120.7   84.4 / 119.4   80.2 / 123.4
+//   norm       64 MiB          12.4 /  20.9   14.5 /  23.0   13.5 /  24.9
+//             128 MiB          26.4 /  37.0   25.0 /  36.4   24.0 /  37.5
+//             256 MiB          48.2 /  63.9   48.6 /  60.1   44.5 /  60.9
+//             512 MiB          93.3 / 122.7   91.6 / 116.7   85.5 / 116.2
+// Below 96 MiB what was written lately is still near and a plain load finds it; from about 256 MiB on,
+// which the last-level cache holds, an output does not stay near anyway.
 enum { kNear = 0, kReadOnce = 1, kThrough = 2 };
 inline int stream_kind(int64_t bytes) {
-  return bytes >= (192ll << 20) ? kThrough : bytes >= (96ll << 20) ? kReadOnce : kNear;
+  return bytes >= (220ll << 20) ? kThrough : bytes >= (96ll << 20) ? kReadOnce : kNear;
 }
 
 constexpr int kHMaxRows = 1 << 16;  // longest row of the row operators

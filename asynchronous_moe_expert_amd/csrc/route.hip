@@ -168,7 +168,7 @@ __device__ __forceinline__ void softmax_of_all(float* l, float& m, float& z) {
 // A candidate as one number: the score's order in bits 30..61 and 511 - e below, so that the larger
 // of two is the larger score, or the lower expert of equal ones.  Read as a double it is positive
 // and finite, and the order of such doubles is that of their bits: v_max_f64 compares both parts in
-// one instruction (a 32-bit maximum and a search for its lowest expert took half as long again).
+// one instruction.
 struct Candidate {
   uint32_t hi, lo;
 };
@@ -195,6 +195,10 @@ __device__ __forceinline__ void order(Candidate& a, Candidate& b) {  // the larg
   a = x;
 }
 
+// Bound by its instructions: 16384 tokens x 256 fp32, top-8, sigmoid with bias move 18 MB (4 us) and
+// take 6.8 us; K rounds of a maximum over the row took 10.3, and with a 32-bit maximum, a search for its
+// lowest expert and lanes that each loaded 64 consecutive bytes 17.0.  A small call (64 tokens) is
+// launch and latency, 2.8 us.
 // The N largest of a row's candidates, descending, in every lane: sorting networks of N = 4 or 8.
 // Two descending lists a, b have their N largest in max(a[i], b[N - 1 - i]), which rises and falls
 // once and is sorted by halving.

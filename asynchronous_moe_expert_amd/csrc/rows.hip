@@ -598,9 +598,10 @@ static int sort_rows(const moe_sort_rows_args* a, const SortJob& j, hipStream_t 
     rc = launch(sort_place_kernel, (unsigned)segs, kIdx, stream, j, segs, seg_len, (const int32_t*)a->workspace);
   if (rc != MOE_OK || !c.chunks) return rc;
   // NT stores from where the rows do not stay near (stream_kind), but plain loads: x is a Kth of the
-  // bytes and was written just before.  65536 rows of 2880 bf16 91 us, 101 with plain stores, 104 with
-  // NT loads too; 32768 rows 44, 54 and 54, equal once a reader of xs follows (95); 16384 rows 26, 31
-  // and 30, with a reader 53, 49 and 53.
+  // bytes and was written just before (NT loads too took 104 us where plain ones take 91).  Rows of
+  // 2880 bf16 to four experts each, microseconds plain / NT stores, alone and with a reader of xs
+  // after it: 16384 rows 30.0 / 25.1 and 48.0 / 52.0, 32768 rows 51.7 / 42.5 and 94.3 / 92.8, 65536 rows
+  // 95.6 / 87.1 and 181.4 / 173.9.
   const int64_t bytes = ((int64_t)j.n * (DT == MOE_F32 ? 4 : 2) + (int64_t)j.T * dtype_size(DT)) * a->H;
   return launch(stream_kind(bytes) == kThrough ? sort_copy_kernel<DT, true> : sort_copy_kernel<DT, false>,
                 grid_of(j.T), block, stream,
