@@ -87,8 +87,14 @@ __device__ __forceinline__ float over(float v, float s, float inv) {
 // through y / scale.
 struct Coding {
   float scale, mul, inv;  // inv != 0: through y = value * mul, over(y, scale, inv)
-  __device__ __forceinline__ float operator()(float v) const {
-    return inv == 0.f ? v * mul : over(v * mul, scale, inv);
+  __device__ __forceinline__ void operator()(float* v) const {
+    if (__ballot(inv != 0.f) == 0) {  // the wave's groups are all ordinary
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= mul;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = inv == 0.f ? v[e] * mul : over(v[e] * mul, scale, inv);
   }
 };
 __device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
@@ -97,9 +103,14 @@ __device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
   return {s, back, 1.f / s};
 }
 
+// Bound by memory: 16384 x 4096 bf16 with the residual, 8 bits out, 470 MB in 80 us (5.9 TB/s); 8192 x
+// 2880, bf16 out, 189 MB in 32 us.  The fp8 outputs' arithmetic shows as well (84 us before the
+// ordinary groups had their own branch).  A call of 64 rows is launch and latency, 4.0 us.  Rows of
+// four chunks per thread in bf16 are held to six waves per SIMD, three workgroups per CU (4096 x 16384
+// to 8 bits 82 us, 85 with two); in fp32 that would spill (98 instead of 89 us).
 // A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + 256, ...
 template <int XT, int RT, int OT, int C, int S>
-__global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
+__global__ __launch_bounds__(kNormT, RT == MOE_BF16 ? 6 : 4) void norm_kernel(NormJob j) {
   __shared__ float s_a[2][kNormWaves], s_b[2][kNormWaves];
   const int rows = j.row_list ? min(j.T, *j.row_count) : j.T;
   int par = 0;
@@ -150,6 +161,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
     if (j.rstd && threadIdx.x == 0) j.rstd[t] = r;
     char* out = (char*)j.out + row_bytes<OT>(t, j.out_pitch);
     const bool plain = OT == MOE_FP8_E4M3 && r >= 0x1p-40f && r <= 0x1p40f;
+    const float pre = plain ? 1.f : r;
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -159,7 +171,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
         float g[8];
         gamma8(j.gamma, j.gamma_f32, at, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[c][e] *= plain ? g[e] : r * g[e];
+        for (int e = 0; e < 8; ++e) h[c][e] *= pre * g[e];
         if constexpr (OT != MOE_FP8_E4M3) st8<OT, S == kThrough>(out, at, h[c]);
       }
       if constexpr (OT == MOE_FP8_E4M3) {
@@ -170,8 +182,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
         if (j.group_lanes) {
           const Coding coded = coding_of(run_max(a, j.group_lanes), r, plain);
           if (at < j.H) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] = coded(h[c][e]);
+            coded(h[c]);
             st8<OT, S == kThrough>(out, at, h[c]);
             const int lane = threadIdx.x & (j.group_lanes - 1);
             if (lane == 0) j.out_scale[(int64_t)t * j.groups + at / (j.group_lanes * 8)] = coded.scale;
@@ -186,8 +197,7 @@ __global__ __launch_bounds__(kNormT) void norm_kernel(NormJob j) {
         for (int c = 0; c < C; ++c) {
           const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
           if (at < j.H) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] = coded(h[c][e]);
+            coded(h[c]);
             st8<OT, S == kThrough>(out, at, h[c]);
           }
         }
@@ -207,15 +217,20 @@ struct NormBackJob {
   float* part;  // [gridDim.x][H] sums over this workgroup's tokens, or NULL
 };
 
-// With xhat = h r and g = dout gamma:  dh = r (g - xhat <g, xhat> / H) + dres,  dgamma = sum_t dout xhat.
-// A workgroup takes the rows blockIdx, blockIdx + gridDim, ... and keeps its share of dgamma in
-// registers.
+// With r = rstd, g = dout gamma:
+//   dh = r g - h r^2 <r g, h> / H + dres,  dgamma = sum_t (dout r) h
+// so that dout r is formed once and serves both.  A workgroup takes the rows blockIdx, blockIdx +
+// gridDim, ... , the next row's loads in flight, and keeps its share of dgamma in registers.
+// 8191 x 2880 bf16, 189 MB: 34 us (5.6 TB/s) and 4.7 us for the sum of the 512 shares; the arithmetic
+// is half of that time (36 us with h r and gamma formed anew for each row).  256 workgroups 46 us in
+// all, 512 40 before that change, 1024 39 with twice the workspace; a second row in flight changes nothing.
 template <int DT, int HT, int C, int S>
 __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   __shared__ float s_a[2][kNormWaves];
   float dg[C][8];
   Chunk<DT> nd[C];  // the next row on its way
-  Chunk<HT> nh[C], ns[C];
+  constexpr bool kDresAhead = C <= 2 || HT == MOE_BF16;  // four fp32 chunks more would spill
+  Chunk<HT> nh[C], ns[kDresAhead ? C : 1];
   float nr = 0.f;
   auto fetch = [&](int t) {
     const char* dout = (const char*)j.dout + row_bytes<DT>(t, j.dout_pitch);
@@ -227,7 +242,9 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
       if (at < j.H) {
         nd[c].template load<(S >= kReadOnce)>(dout, at);
         nh[c].template load<(S >= kReadOnce)>(hr, at);
-        if (j.dres) ns[c].template load<(S >= kReadOnce)>(dres, at);
+        if constexpr (kDresAhead) {
+          if (j.dres) ns[c].template load<(S >= kReadOnce)>(dres, at);
+        }
       }
     }
     nr = j.rstd[t];
@@ -236,46 +253,57 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[c][e] = 0.f;
+  constexpr bool kGammaHeld = C == 1;  // two chunks' took 87 instead of 83 us at 8192 x 7168 bf16
+  float gm[kGammaHeld ? C : 1][8];
+  if constexpr (kGammaHeld) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
+      if (at < j.H) gamma8(j.gamma, j.gamma_f32, at, gm[c]);
+    }
+  }
   int par = 0;
   fetch(blockIdx.x);
   for (int t = blockIdx.x; t < j.T; t += gridDim.x, par ^= 1) {
     const float r = nr;
-    float xh[C][8], g[C][8], dot = 0.f;
-    Chunk<HT> ds[C];
+    float h[C][8], rg[C][8], dot = 0.f;
+    Chunk<HT> ds[kDresAhead ? C : 1];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xh[c][e] = g[c][e] = 0.f;
       if (at < j.H) {
-        nd[c].get(g[c]);
-        nh[c].get(xh[c]);
-        ds[c] = ns[c];
-        float gm[8];
-        gamma8(j.gamma, j.gamma_f32, at, gm);
+        nd[c].get(rg[c]);
+        nh[c].get(h[c]);
+        if constexpr (kDresAhead) ds[c] = ns[c];
+        if constexpr (!kGammaHeld) gamma8(j.gamma, j.gamma_f32, at, gm[0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          xh[c][e] *= r;
-          dg[c][e] = fmaf(g[c][e], xh[c][e], dg[c][e]);
-          g[c][e] *= gm[e];
-          dot = fmaf(g[c][e], xh[c][e], dot);
+          const float a = rg[c][e] * r;
+          dg[c][e] = fmaf(a, h[c][e], dg[c][e]);
+          rg[c][e] = a * gm[kGammaHeld ? c : 0][e];
+          dot = fmaf(rg[c][e], h[c][e], dot);
         }
       }
     }
     if (t + (int)gridDim.x < j.T) fetch(t + gridDim.x);
-    const float mean = group_sum(dot, s_a[par]) / (float)j.H;
+    const float back = group_sum(dot, s_a[par]) / (float)j.H * (r * r);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (at < j.H) {
         float d[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = r * (g[c][e] - xh[c][e] * mean);
         if (j.dres) {
-          float f[8];
-          ds[c].get(f);
+          if constexpr (kDresAhead) {
+            ds[c].get(d);
+          } else {
+            ds[0].template load<(S >= kReadOnce)>((const char*)j.dres + row_bytes<HT>(t, j.dres_pitch), at);
+            ds[0].get(d);
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] += f[e];
+          for (int e = 0; e < 8; ++e) d[e] = fmaf(-h[c][e], back, rg[c][e] + d[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = fmaf(-h[c][e], back, rg[c][e]);
         }
         if (j.dx) st8<DT, S == kThrough>((char*)j.dx + row_bytes<DT>(t, j.dx_pitch), at, d);
         if (j.dresidual) st8<HT, S == kThrough>((char*)j.dresidual + row_bytes<HT>(t, j.dresidual_pitch), at, d);
