@@ -1,7 +1,8 @@
 """MI355X-native expert step of asynchronous expert-parallel MoE serving.
 
 libmoestep.so (HIP kernels for gfx950 behind a C ABI, include/moe_step.h) does the work;
-this package binds it (ctypes) and strings the three calls together on one stream.
+this package binds it (ctypes, and the compiled module _marshal for the home rank's operators)
+and strings the calls together on one stream.
 """
 from ._native import (  # noqa: F401
     ERR_DUPLICATE,

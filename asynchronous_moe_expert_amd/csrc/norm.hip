@@ -108,7 +108,7 @@ __device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
 // ordinary groups had their own branch).  A call of 64 rows is launch and latency, 4.0 us.  Rows of
 // four chunks per thread in bf16 are held to six waves per SIMD, three workgroups per CU (4096 x 16384
 // to 8 bits 82 us, 85 with two); in fp32 that would spill (98 instead of 89 us).
-// A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + 256, ...
+// A workgroup per row (rows blockIdx, blockIdx + gridDim, ...); thread i holds the chunks i, i + blockDim, ...
 template <int XT, int RT, int OT, int C, int S>
 __global__ __launch_bounds__(kNormT, RT == MOE_BF16 ? 6 : 4) void norm_kernel(NormJob j) {
   __shared__ float s_a[2][kNormWaves], s_b[2][kNormWaves];

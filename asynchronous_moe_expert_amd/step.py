@@ -194,7 +194,9 @@ class ExpertLayer:
     grouped FFN gathers its rows from x through row_slot, moe_merge_rows applies the weights.
 
     After run() the buffers hold what a caller may want further on: expert and w ([T][K]), pos,
-    counts and offsets as moe_sort_rows gives them, y (the experts' rows, before the weights)."""
+    counts and offsets as moe_sort_rows gives them, y (the experts' rows, before the weights).  They
+    belong to one run at a time: runs on several streams, or captured graphs that are replayed side
+    by side, take a layer object each (the packed weights may be shared)."""
 
     def __init__(self, E: int, H: int, I: int, K: int, act_dtype: int, w_dtype: int, T_max: int, device="cuda",
                  score: int = N.MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0):

@@ -66,7 +66,7 @@ def within(got, ref, tol, what=""):
 # ------------------------------------------------------------------------------------------ route
 def hard_logits(rng, T, E, dtype):
     """Normal rows, and by turns: ties, all -inf, NaN and -inf among numbers, the type's lowest value
-    as a mask, nothing but it, very large ones, signed zeros."""
+    as a mask, nothing but it, very large ones, signed zeros, one or two +inf."""
     l = rng.standard_normal((T, E)) * 2
     low = torch.finfo(dtype).min
     for t in range(T):
@@ -86,6 +86,8 @@ def hard_logits(rng, T, E, dtype):
             l[t] *= 40
         elif kind == 7:
             l[t] = rng.choice([0.0, -0.0, -1.0], E)
+        elif kind == 8:
+            l[t, rng.integers(0, E, 2)] = np.inf
     return l
 
 
