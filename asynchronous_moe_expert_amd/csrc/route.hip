@@ -323,6 +323,12 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RouteJob j, const float*
   }
 }
 
+// LDS accesses of a wave before it come before those after it (the hardware keeps them in order)
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // With p the shares and v = scale dw:
 //   softmax over the chosen:  dl_j = p_j (v_j - <v, p>)
 //   softmax over all:         dl_e = p_e (sum of v_j over j that name e - <v, p>)
@@ -367,11 +373,41 @@ __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, con
   const float each = all && z > 0.f ? -vp / z : 0.f;
 #pragma unroll
   for (int q = 0; q < V; ++q) d[q] = all ? l[q] * each : 0.f;
-  for (int k = 0; k < j.K; ++k) {
-    const int e = __shfl(k < 16 ? ce[0] : ce[R - 1], k & 15, 16);
-    const float g = __shfl(k < 16 ? dl[0] : dl[R - 1], k & 15, 16);
+  // the chosen experts' part through the token's row in LDS, which only its own 16 lanes touch: each
+  // position marks its expert, and where none finds another's mark no expert is named twice and
+  // each writes its value (forward and gradient of 16384 x 256, top-8: 17.0 us; 18.9 with every position
+  // held against every expert, as the other branch does)
+  constexpr int W = V < 4 ? V : 4;
+  __shared__ __attribute__((aligned(16))) float s_row[kRouteTok][16 * V];
+  float* mine = s_row[threadIdx.x >> 4];
 #pragma unroll
-    for (int q = 0; q < V; ++q) d[q] += e == expert_of<V>(lane, q) ? g : 0.f;
+  for (int q = 0; q < V; q += W)
+#pragma unroll
+    for (int k = 0; k < W; ++k) mine[expert_of<V>(lane, q) + k] = 0.f;
+  wave_order();
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (there[r]) mine[ce[r]] = (float)(1 + lane + 16 * r);
+  wave_order();
+  bool twice = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (there[r]) twice |= mine[ce[r]] != (float)(1 + lane + 16 * r);
+  wave_order();
+  if (__ballot(twice) == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (there[r]) mine[ce[r]] = dl[r];
+    wave_order();
+#pragma unroll
+    for (int q = 0; q < V; ++q) d[q] += mine[expert_of<V>(lane, q)];
+  } else {  // in the order of the positions
+    for (int k = 0; k < j.K; ++k) {
+      const int e = __shfl(k < 16 ? ce[0] : ce[R - 1], k & 15, 16);
+      const float g = __shfl(k < 16 ? dl[0] : dl[R - 1], k & 15, 16);
+#pragma unroll
+      for (int q = 0; q < V; ++q) d[q] += e == expert_of<V>(lane, q) ? g : 0.f;
+    }
   }
   const int64_t row = (int64_t)t * dpitch;
   if constexpr (V >= 4) {
