@@ -486,8 +486,8 @@ int moe_merge_rows(const moe_merge_rows_args* args, hipStream_t stream);
  *   drows[pos[t][j]][:] = w[t][j] * dout[t][:]     (row_dtype; may be NULL)
  *   dw[t][j]            = <dout[t], rows[pos[t][j]]>, 0 where pos gives no row   (fp32 [T][K]; may
  *                         be NULL, then rows may be too)
- * Each row belongs to one (t, j), as in moe_sort_rows' pos: drows of a row that several name holds
- * the product of one of them.  Rows that none names are left as they were.  pos outside
+ * Each row belongs to one (t, j), as in moe_sort_rows' pos: where several name a row, each element
+ * of its drows is the product of one of them, and which is not determined.  Rows that none names are left as they were.  pos outside
  * [-1, n_rows) as in moe_merge_rows.  At least one of drows and dw is given. */
 typedef struct moe_merge_rows_backward_args {
   int32_t T, K, H;
