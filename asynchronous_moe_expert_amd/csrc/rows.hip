@@ -379,10 +379,12 @@ __device__ __forceinline__ Named named_rows(const int32_t* pos, const float* w, 
   Named r{-1, 0.f};
   if (lane < K) {
     const int64_t at = (int64_t)t * K + lane;
-    const int p = pos[at];
-    if (p >= 0 && p < n_rows) r.p = p;
-    else if (p != -1) atomicOr(err, MOE_ERR_ROW_RANGE);
+    r.p = pos[at];
     r.w = w ? w[at] : 1.f;
+  }
+  if (r.p < 0 || r.p >= n_rows) {
+    if (r.p != -1) atomicOr(err, MOE_ERR_ROW_RANGE);
+    r.p = -1;
   }
   r.p = all_lanes(r.p);
   r.w = all_lanes(r.w);
