@@ -62,6 +62,23 @@ __device__ __forceinline__ float group_max(float v, float* s) {
   return all;
 }
 
+// group_sum of the row group `sub` of a workgroup that holds several rows, tpr threads to each
+template <bool MANY>
+__device__ __forceinline__ float rows_sum(float v, float* s, int sub, int tpr) {
+  if constexpr (!MANY) {
+    return group_sum(v, s);
+  } else {
+    v = wave_sum(v);
+    const int waves = tpr >> 6;
+    if (waves == 1) return v;
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float all = s[sub * waves];
+    for (int w = 1; w < waves; ++w) all += s[sub * waves + w];
+    return all;
+  }
+}
+
 // the maximum over aligned runs of 4, 8 or 16 lanes
 __device__ __forceinline__ float run_max(float v, int lanes) {
   v = fmaxf(v, dpp_f32<kDppXor1>(v));
@@ -209,7 +226,7 @@ __global__ __launch_bounds__(kNormT, RT == MOE_BF16 ? 6 : 4) void norm_kernel(No
 }
 
 struct NormBackJob {
-  int T, H, gamma_f32;
+  int T, H, gamma_f32, row_threads;
   const void *dout, *h, *gamma, *dres;
   int64_t dout_pitch, h_pitch, dres_pitch, dx_pitch, dresidual_pitch;
   const float* rstd;
@@ -224,9 +241,17 @@ struct NormBackJob {
 // 8191 x 2880 bf16, 189 MB: 34 us (5.6 TB/s) and 4.7 us for the sum of the 512 shares; the arithmetic
 // is half of that time (36 us with h r and gamma formed anew for each row).  256 workgroups 46 us in
 // all, 512 40 before that change, 1024 39 with twice the workspace; a second row in flight changes nothing.
-template <int DT, int HT, int C, int S>
+// MANY (C = 1): several rows at a time in a workgroup, row_threads threads to a row, so that short rows
+// still fill the waves.  16384 rows of 64 columns 24 us one at a time, 9.7 with eight; of 512 25 and
+// 15.5, of 1024 37 and 27 (four), of 1536 42.5 and 39.4 (two), but of 2048 48.5 and 49.7 (two).
+template <int DT, int HT, int C, int S, bool MANY>
 __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   __shared__ float s_a[2][kNormWaves];
+  __shared__ float s_share[MANY ? kNormT * 8 : 1];
+  static_assert(!MANY || C == 1, "");
+  const int tpr = MANY ? j.row_threads : (int)blockDim.x;  // threads to a row
+  const int sub = MANY ? (int)threadIdx.x / tpr : 0, lt = (int)threadIdx.x - sub * tpr;
+  const int many = MANY ? (int)blockDim.x / tpr : 1, step = (int)gridDim.x * many;
   float dg[C][8];
   Chunk<DT> nd[C];  // the next row on its way
   constexpr bool kDresAhead = C <= 2 || HT == MOE_BF16;  // four fp32 chunks more would spill
@@ -238,7 +263,7 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
     const char* dres = (const char*)j.dres + row_bytes<HT>(t, j.dres_pitch);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
+      const int at = (c * tpr + lt) * 8;
       if (at < j.H) {
         nd[c].template load<(S >= kReadOnce)>(dout, at);
         nh[c].template load<(S >= kReadOnce)>(hr, at);
@@ -258,20 +283,23 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   if constexpr (kGammaHeld) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
+      const int at = (c * tpr + lt) * 8;
       if (at < j.H) gamma8(j.gamma, j.gamma_f32, at, gm[c]);
     }
   }
   int par = 0;
-  fetch(blockIdx.x);
-  for (int t = blockIdx.x; t < j.T; t += gridDim.x, par ^= 1) {
+  if ((int)blockIdx.x * many + sub < j.T) fetch(blockIdx.x * many + sub);
+  // every thread takes as many turns as the workgroup's first row does
+  for (int t0 = blockIdx.x * many; t0 < j.T; t0 += step, par ^= 1) {
+    const int t = t0 + sub;
+    const bool there = !MANY || t < j.T;
     const float r = nr;
     float h[C][8], rg[C][8], dot = 0.f;
     Chunk<HT> ds[kDresAhead ? C : 1];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
-      if (at < j.H) {
+      const int at = (c * tpr + lt) * 8;
+      if (there && at < j.H) {
         nd[c].get(rg[c]);
         nh[c].get(h[c]);
         if constexpr (kDresAhead) ds[c] = ns[c];
@@ -285,12 +313,12 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
         }
       }
     }
-    if (t + (int)gridDim.x < j.T) fetch(t + gridDim.x);
-    const float back = group_sum(dot, s_a[par]) / (float)j.H * (r * r);
+    if (t + step < j.T) fetch(t + step);
+    const float back = rows_sum<MANY>(dot, s_a[par], sub, tpr) / (float)j.H * (r * r);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
-      if (at < j.H) {
+      const int at = (c * tpr + lt) * 8;
+      if (there && at < j.H) {
         float d[8];
         if (j.dres) {
           if constexpr (kDresAhead) {
@@ -310,10 +338,21 @@ __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
       }
     }
   }
+  if constexpr (MANY) {  // the rows' shares of dgamma together, in the order of the rows
+    if (!j.part) return;
+    if (lt * 8 < j.H) st8<MOE_F32>(s_share + sub * j.H, lt * 8, dg[0]);
+    __syncthreads();
+    for (int col = threadIdx.x; col < j.H; col += blockDim.x) {
+      float sum = 0.f;
+      for (int q = 0; q < many; ++q) sum += s_share[q * j.H + col];
+      j.part[(int64_t)blockIdx.x * j.H + col] = sum;
+    }
+    return;
+  }
   if (j.part) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = (c * (int)blockDim.x + (int)threadIdx.x) * 8;
+      const int at = (c * tpr + lt) * 8;
       if (at < j.H) st8<MOE_F32>(j.part + (int64_t)blockIdx.x * j.H, at, dg[c]);
     }
   }
@@ -379,21 +418,32 @@ static int norm_by_out(const NormJob& j, int out, hipStream_t stream) {
   return norm_by_width<XT, RT, MOE_FP8_E4M3>(j, stream);
 }
 
-template <int DT, int HT, int C>
+template <int DT, int HT, int C, bool MANY>
 static int norm_backward_launch(const NormBackJob& j, unsigned grid, unsigned threads, hipStream_t stream) {
   const int hs = dtype_size(HT) * (1 + (j.dres != nullptr) + (j.dresidual != nullptr));
   switch (stream_kind((int64_t)j.T * j.H * (dtype_size(DT) * (1 + (j.dx != nullptr)) + hs))) {
-    case kThrough: return launch(norm_backward_kernel<DT, HT, C, kThrough>, grid, threads, stream, j);
-    case kReadOnce: return launch(norm_backward_kernel<DT, HT, C, kReadOnce>, grid, threads, stream, j);
-    default: return launch(norm_backward_kernel<DT, HT, C, kNear>, grid, threads, stream, j);
+    case kThrough: return launch(norm_backward_kernel<DT, HT, C, kThrough, MANY>, grid, threads, stream, j);
+    case kReadOnce: return launch(norm_backward_kernel<DT, HT, C, kReadOnce, MANY>, grid, threads, stream, j);
+    default: return launch(norm_backward_kernel<DT, HT, C, kNear, MANY>, grid, threads, stream, j);
   }
 }
+
+// rows that a workgroup of the gradient takes at a time: one up to kPartials rows, which then have a
+// workgroup each, and from 1537 columns on
+static int norm_backward_many(int T, int H) {
+  const RowShape r = row_shape(H);
+  return r.threads > 192 || r.chunks > 1 || T <= kPartials ? 1 : kNormT / (int)r.threads;
+}
+
 template <int DT, int HT>
-static int norm_backward_by_width(const NormBackJob& j, unsigned grid, hipStream_t stream) {
+static int norm_backward_by_width(NormBackJob& j, unsigned grid, hipStream_t stream) {
   const RowShape r = row_shape(j.H);
-  if (r.chunks == 1) return norm_backward_launch<DT, HT, 1>(j, grid, r.threads, stream);
-  if (r.chunks == 2) return norm_backward_launch<DT, HT, 2>(j, grid, r.threads, stream);
-  return norm_backward_launch<DT, HT, 4>(j, grid, r.threads, stream);
+  const int many = norm_backward_many(j.T, j.H);
+  j.row_threads = (int)r.threads;
+  if (many > 1) return norm_backward_launch<DT, HT, 1, true>(j, grid, r.threads * many, stream);
+  if (r.chunks == 1) return norm_backward_launch<DT, HT, 1, false>(j, grid, r.threads, stream);
+  if (r.chunks == 2) return norm_backward_launch<DT, HT, 2, false>(j, grid, r.threads, stream);
+  return norm_backward_launch<DT, HT, 4, false>(j, grid, r.threads, stream);
 }
 
 }  // namespace moe
@@ -462,7 +512,8 @@ extern "C" int moe_residual_norm_backward(const moe_residual_norm_backward_args*
       if (!aligned16(a->workspace)) return MOE_EINVAL_ALIGN;
     }
   }
-  const unsigned grid = (unsigned)(a->T < kPartials ? a->T : kPartials);
+  const int many = norm_backward_many(a->T, a->H), units = (a->T + many - 1) / many;
+  const unsigned grid = (unsigned)(units < kPartials ? units : kPartials);
   if (a->T > 0) {
     NormBackJob j;
     j.T = a->T; j.H = a->H; j.gamma_f32 = a->gamma_dtype == MOE_F32;

@@ -471,7 +471,7 @@ def test_residual_norm_not_finite_and_tiny():
     assert np.isfinite(o[0]).all() and (s[0] == np.float32(1 / 448)).all() and np.isfinite(val(f32)[[0, 3, 4, 5]]).all()
 
 
-@pytest.mark.parametrize("T,H", NORMS + [(1500, 264)])
+@pytest.mark.parametrize("T,H", NORMS + [(1500, 264), (513, 1032), (2049, 8), (1027, 1536)])
 @pytest.mark.parametrize("dt,ht", TYPES)
 def test_residual_norm_backward(T, H, dt, ht):
     rng = np.random.default_rng(T + H + 5)
