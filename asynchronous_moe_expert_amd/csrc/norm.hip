@@ -101,21 +101,22 @@ __device__ __forceinline__ float over(float v, float s, float inv) {
 // fall on the wrong side of a border (of 201 million codes 2782 are not those of a 64-bit
 // evaluation, 4455 with y / scale in fp32).  z is used while r and the group's max|z| are of ordinary size
 // (`plain` rows: 2^-40 <= r <= 2^40); other rows hold y itself, and groups past the limits go
-// through y / scale.
+// through y / scale, which makes every code of a group with an infinite y NaN.
+constexpr float kOrdinary = -1.f;  // no reciprocal of a scale is negative; that of an infinite one is 0
 struct Coding {
-  float scale, mul, inv;  // inv != 0: through y = value * mul, over(y, scale, inv)
+  float scale, mul, inv;  // inv != kOrdinary: through y = value * mul, over(y, scale, inv)
   __device__ __forceinline__ void operator()(float* v) const {
-    if (__ballot(inv != 0.f) == 0) {  // the wave's groups are all ordinary
+    if (__ballot(inv != kOrdinary) == 0) {  // the wave's groups are all ordinary
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= mul;
       return;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = inv == 0.f ? v[e] * mul : over(v[e] * mul, scale, inv);
+    for (int e = 0; e < 8; ++e) v[e] = inv == kOrdinary ? v[e] * mul : over(v[e] * mul, scale, inv);
   }
 };
 __device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
-  if (plain && amax >= 0x1p-60f && amax <= 0x1p80f) return {amax * r / 448.f, 448.f / amax, 0.f};
+  if (plain && amax >= 0x1p-60f && amax <= 0x1p80f) return {amax * r / 448.f, 448.f / amax, kOrdinary};
   const float back = plain ? r : 1.f, s = scale_of(amax * back);
   return {s, back, 1.f / s};
 }
