@@ -248,7 +248,7 @@ struct NormBackJob {
 template <int DT, int HT, int C, int S, bool MANY>
 __global__ __launch_bounds__(kNormT) void norm_backward_kernel(NormBackJob j) {
   __shared__ float s_a[2][kNormWaves];
-  __shared__ float s_share[MANY ? kNormT * 8 : 1];
+  __shared__ __attribute__((aligned(16))) float s_share[MANY ? kNormT * 8 : 4];
   static_assert(!MANY || C == 1, "");
   const int tpr = MANY ? j.row_threads : (int)blockDim.x;  // threads to a row
   const int sub = MANY ? (int)threadIdx.x / tpr : 0, lt = (int)threadIdx.x - sub * tpr;
