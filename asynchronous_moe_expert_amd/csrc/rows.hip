@@ -4,17 +4,10 @@
 
 namespace moe {
 
+// lane_i32 and lane_f32 stand only where every lane of the wave is active: a lane that a branch has
+// switched off need not hold its value.  Loops over a row's chunks therefore run the same number of
+// turns in every lane, and a lane past the row's end leaves out the loads and stores alone.
 __device__ __forceinline__ int lane_i32(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
-// A value that lane_i32 / lane_f32 reads inside a branch or loop that some lanes do not enter: it is
-// computed here, by every lane, and not moved into the branch.
-__device__ __forceinline__ int all_lanes(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-__device__ __forceinline__ float all_lanes(float v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
 
 constexpr int kMaxEloc = 256, kMaxK = 32;
 constexpr int kNone = kMaxEloc;  // key of a pair without a row
@@ -218,8 +211,8 @@ struct Carried {
     if constexpr (DT == MOE_FP8_E4M3)
       s = c.x_scale[(int64_t)t * c.groups + (c.group_shift < 0 ? 0 : (ch * 8) >> c.group_shift)];
   }
-  // position k's row in lane k of p
-  __device__ __forceinline__ void store(const CopyJob& c, int ch, int p) const {
+  // position k's row in lane k of p; called by whole waves, `there` where the lane has a chunk
+  __device__ __forceinline__ void store(const CopyJob& c, int ch, int p, bool there) const {
     float f[8];
     q.get(f);
     if constexpr (DT == MOE_FP8_E4M3) {
@@ -230,10 +223,12 @@ struct Carried {
       const int r = lane_i32(p, k);
       if (r < 0) continue;
       char* dst = (char*)c.xs + (int64_t)r * c.xs_pitch * osz;
-      if constexpr (DT == MOE_BF16)
-        st<NT>(reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8), q.r);
-      else
-        st8<OUT, NT>(dst, (int64_t)ch * 8, f);
+      if (there) {
+        if constexpr (DT == MOE_BF16)
+          st<NT>(reinterpret_cast<u32x4*>((uint16_t*)dst + (int64_t)ch * 8), q.r);
+        else
+          st8<OUT, NT>(dst, (int64_t)ch * 8, f);
+      }
     }
   }
 };
@@ -246,14 +241,14 @@ template <int DT, bool NT>
 __global__ __launch_bounds__(512) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
   const int lane = threadIdx.x & 63;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    Carried<DT, NT> first;  // on its way while the positions are looked up
-    if ((int)threadIdx.x < c.chunks) first.load(c, t, threadIdx.x);
-    const int p = all_lanes(lane < c.K ? pos[(int64_t)t * c.K + lane] : -1);
-    if ((int)threadIdx.x < c.chunks) first.store(c, threadIdx.x, p);
-    for (int ch = threadIdx.x + blockDim.x; ch < c.chunks; ch += blockDim.x) {
-      Carried<DT, NT> x;
-      x.load(c, t, ch);
-      x.store(c, ch, p);
+    Carried<DT, NT> x;  // on its way while the positions are looked up
+    if ((int)threadIdx.x < c.chunks) x.load(c, t, threadIdx.x);
+    const int p = lane < c.K ? pos[(int64_t)t * c.K + lane] : -1;
+    x.store(c, threadIdx.x, p, (int)threadIdx.x < c.chunks);
+    for (int c0 = blockDim.x; c0 < c.chunks; c0 += blockDim.x) {
+      const int ch = c0 + threadIdx.x;
+      if (ch < c.chunks) x.load(c, t, ch);
+      x.store(c, ch, p, ch < c.chunks);
     }
   }
 }
@@ -281,8 +276,8 @@ __global__ __launch_bounds__(512) void sort_short_kernel(SortJob j, CopyJob c) {
   unsigned bad = 0;
   if ((int)blockIdx.x < j.T) {
     const int t = blockIdx.x;
-    Carried<DT, false> first;
-    if (tid < c.chunks) first.load(c, t, tid);
+    Carried<DT, false> x;
+    if (tid < c.chunks) x.load(c, t, tid);
     const int padded = (j.n + 255) & ~255;
     for (int q = tid; q < padded; q += blockDim.x)
       s_all[q] = q < j.n ? (uint32_t)sort_key(j, q, bad) << 16 | (uint32_t)q : ~0u;
@@ -307,12 +302,12 @@ __global__ __launch_bounds__(512) void sort_short_kernel(SortJob j, CopyJob c) {
       }
     }
     __syncthreads();
-    const int p = all_lanes(lane < j.K ? s_pos[lane] : -1);
-    if (tid < c.chunks) first.store(c, tid, p);
-    for (int ch = tid + blockDim.x; ch < c.chunks; ch += blockDim.x) {
-      Carried<DT, false> x;
-      x.load(c, t, ch);
-      x.store(c, ch, p);
+    const int p = lane < j.K ? s_pos[lane] : -1;
+    if (c.chunks) x.store(c, tid, p, tid < c.chunks);
+    for (int c0 = blockDim.x; c0 < c.chunks; c0 += blockDim.x) {
+      const int ch = c0 + tid;
+      if (ch < c.chunks) x.load(c, t, ch);
+      x.store(c, ch, p, ch < c.chunks);
     }
     return;
   }
@@ -386,8 +381,6 @@ __device__ __forceinline__ Named named_rows(const int32_t* pos, const float* w, 
     if (r.p != -1) atomicOr(err, MOE_ERR_ROW_RANGE);
     r.p = -1;
   }
-  r.p = all_lanes(r.p);
-  r.w = all_lanes(r.w);
   return r;
 }
 
@@ -401,26 +394,34 @@ __global__ __launch_bounds__(512) void merge_kernel(MergeJob m) {
   for (int t = blockIdx.x; t < m.T; t += gridDim.x) {
     const Named r = named_rows(m.pos, m.w, m.err, t, m.K, m.n_rows, lane);
     char* out = (char*)m.out + (int64_t)t * m.out_pitch * (OT == MOE_F32 ? 4 : 2);
-    for (int ch = threadIdx.x; ch < m.chunks; ch += blockDim.x) {
+    for (int c0 = 0; c0 < m.chunks; c0 += blockDim.x) {
+      const int ch = c0 + threadIdx.x;
+      const bool there = ch < m.chunks;
       float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k0 = 0; k0 < m.K; k0 += KB) {
-        Chunk<RT> q[KB];
+        int p[KB];
+        float w[KB];
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-          const int p = lane_i32(r.p, k0 + k);
-          if (p >= 0) q[k].template load<(S >= kReadOnce)>(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
+          p[k] = lane_i32(r.p, k0 + k);
+          w[k] = lane_f32(r.w, k0 + k);
         }
+        if (there) {
+          Chunk<RT> q[KB];
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-          if (lane_i32(r.p, k0 + k) < 0) continue;
-          const float w = lane_f32(r.w, k0 + k);
-          float f[8];
-          q[k].get(f);
+          for (int k = 0; k < KB; ++k)
+            if (p[k] >= 0) q[k].template load<(S >= kReadOnce)>(row_at<RT>(m.rows, p[k], m.row_pitch), (int64_t)ch * 8);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, f[e], acc[e]);
+          for (int k = 0; k < KB; ++k) {
+            if (p[k] < 0) continue;
+            float f[8];
+            q[k].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[k], f[e], acc[e]);
+          }
         }
       }
-      st8<OT, S == kThrough>(out, (int64_t)ch * 8, acc);
+      if (there) st8<OT, S == kThrough>(out, (int64_t)ch * 8, acc);
     }
   }
 }
@@ -451,38 +452,39 @@ __global__ __launch_bounds__(512) void merge_backward_kernel(MergeBackJob m) {
     const char* dout = row_at<DT>(m.dout, t, m.dout_pitch);
     const Named r = named_rows(m.pos, m.w, m.err, t, m.K, m.n_rows, lane);
     for (int k0 = 0; k0 < m.K; k0 += KB, par ^= 1) {
-      float dot[KB];
+      float dot[KB], w[KB];
+      int p[KB];
 #pragma unroll
-      for (int k = 0; k < KB; ++k) dot[k] = 0.f;
+      for (int k = 0; k < KB; ++k) {
+        dot[k] = 0.f;
+        p[k] = lane_i32(r.p, k0 + k);
+        w[k] = lane_f32(r.w, k0 + k);
+      }
       for (int ch = threadIdx.x; ch < m.chunks; ch += blockDim.x) {
         Chunk<RT> q[KB];
         Chunk<DT> d;
         d.template load<(S >= kReadOnce)>(dout, (int64_t)ch * 8);
         if (m.dw) {
 #pragma unroll
-          for (int k = 0; k < KB; ++k) {
-            const int p = lane_i32(r.p, k0 + k);
-            if (p >= 0) q[k].template load<(S >= kReadOnce)>(row_at<RT>(m.rows, p, m.row_pitch), (int64_t)ch * 8);
-          }
+          for (int k = 0; k < KB; ++k)
+            if (p[k] >= 0) q[k].template load<(S >= kReadOnce)>(row_at<RT>(m.rows, p[k], m.row_pitch), (int64_t)ch * 8);
         }
         float g[8];
         d.get(g);
         if (m.drows) {
 #pragma unroll
           for (int k = 0; k < KB; ++k) {
-            const int p = lane_i32(r.p, k0 + k);
-            if (p < 0) continue;
-            const float w = lane_f32(r.w, k0 + k);
+            if (p[k] < 0) continue;
             float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = g[e] * w;
-            st8<RT, S == kThrough>((char*)m.drows + (int64_t)p * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, f);
+            for (int e = 0; e < 8; ++e) f[e] = g[e] * w[k];
+            st8<RT, S == kThrough>((char*)m.drows + (int64_t)p[k] * m.drows_pitch * (RT == MOE_F32 ? 4 : 2), (int64_t)ch * 8, f);
           }
         }
         if (m.dw) {
 #pragma unroll
           for (int k = 0; k < KB; ++k) {
-            if (lane_i32(r.p, k0 + k) < 0) continue;
+            if (p[k] < 0) continue;
             float f[8];
             q[k].get(f);
 #pragma unroll
