@@ -337,7 +337,8 @@ _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_devic
 
 
 def _home():
-    """The module _marshal, with the library's entry points."""
+    """The module _marshal, with the library's entry points.  It compares the sizes of the argument
+    structs that it was built with with the library's."""
     global _marshal
     if _marshal is None:
         lib = load()
@@ -346,7 +347,8 @@ def _home():
         except ImportError as e:
             raise MoeError(f"_marshal.so could not be loaded ({e}); build it with "
                            "`python -m asynchronous_moe_expert_amd.build`") from None
-        m.setup(MoeError, *(C.cast(getattr(lib, name), _p).value for name in ("moe_strerror",) + _HOME))
+        m.setup(MoeError, *(C.cast(getattr(lib, name), _p).value
+                            for name in ("moe_strerror", "moe_version", "moe_struct_size") + _HOME))
         _marshal = m
     return _marshal
 

@@ -5,6 +5,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -43,7 +44,8 @@ def _run(cmd: list[str], verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compiles every source (side by side) and links; each file is put in its place whole."""
+    """Compiles every source (side by side) and links.  The library and _marshal.so share argument
+    structs, so both are put in their places, whole, once everything has been built."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     compiled = [f for f in HIPCC_FLAGS if f != "-shared"]
     with tempfile.TemporaryDirectory(prefix="moestep_") as tmp, \
@@ -51,29 +53,29 @@ def build(verbose: bool = False) -> str:
         objects = [os.path.join(tmp, os.path.basename(f) + ".o") for f in sources()]
         jobs = [pool.submit(_run, [hipcc, *compiled, "-I", os.path.join(ROOT, "include"), "-c", f, "-o", o], verbose)
                 for f, o in zip(sources(), objects)]
-        jobs.append(pool.submit(build_marshal, verbose))
+        marshal = os.path.join(tmp, "_marshal.so")
+        jobs.append(pool.submit(build_marshal, marshal, verbose))
         for j in jobs:
             j.result()
         _run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", LIB + ".tmp"], verbose)
+        shutil.copy(marshal, MARSHAL + ".tmp")
     os.replace(LIB + ".tmp", LIB)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     return LIB
 
 
-def build_marshal(verbose: bool = False) -> str:
+def build_marshal(out: str, verbose: bool = False) -> None:
     import torch
 
     at = os.path.dirname(torch.__file__)
-    tmp = MARSHAL + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(at, "include"),
            "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
-           "-I", sysconfig.get_paths()["include"], os.path.join(PKG, "csrc", "marshal.cpp"), "-o", tmp,
+           "-I", sysconfig.get_paths()["include"], os.path.join(PKG, "csrc", "marshal.cpp"), "-o", out,
            "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     _run(cmd, verbose)
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
 
 
 if __name__ == "__main__":

@@ -7,7 +7,8 @@
 // Every function takes its operator's tensors (None where one is left out) and numbers in order, and
 // last the stream's handle; the current device is the tensors' own.  A view that the kernels cannot
 // address, or a size that the struct cannot hold, raises MoeError and enqueues nothing.  The
-// library's entry points are handed over by setup().
+// library's entry points are handed over by setup(), which refuses a library that was built from
+// another moe_step.h (other sizes of the argument structs, or another version).
 #include <Python.h>
 
 #include <cfloat>
@@ -418,25 +419,44 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-// setup(MoeError, address of moe_strerror, addresses of the entry points in Entry's order)
+// sizeof of each entry's argument struct as compiled here; moe_struct_size's ids begin at 5 for kRoute
+constexpr int kFirstStruct = 5;
+constexpr size_t kStructSize[kEntries] = {
+    sizeof(moe_route_args),        sizeof(moe_route_backward_args),      sizeof(moe_sort_rows_args),
+    sizeof(moe_merge_rows_args),   sizeof(moe_merge_rows_backward_args), sizeof(moe_residual_norm_args),
+    sizeof(moe_residual_norm_backward_args)};
+
+// setup(MoeError, addresses of moe_strerror, moe_version and moe_struct_size, addresses of the entry
+// points in Entry's order); what was set up before stays if it raises
 PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 2 + kEntries) {
+  constexpr int kHelpers = 3;
+  if (n != 1 + kHelpers + kEntries) {
     PyErr_SetString(PyExc_TypeError, "setup: wrong number of arguments");
     return nullptr;
   }
-  void* p[1 + kEntries];
-  for (int i = 0; i < 1 + kEntries; ++i) {
+  void* p[kHelpers + kEntries];
+  for (int i = 0; i < kHelpers + kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(args[1 + i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "setup: an address of 0");
       return nullptr;
     }
   }
+  const int version = ((int (*)(void))p[1])();
+  if (version != MOE_STEP_VERSION)
+    return PyErr_Format(args[0], "the library has version %d, _marshal was built for %d: build both again", version,
+                        MOE_STEP_VERSION);
+  for (int i = 0; i < kEntries; ++i) {
+    const size_t size = ((size_t(*)(int))p[2])(kFirstStruct + i);
+    if (size != kStructSize[i])
+      return PyErr_Format(args[0], "struct layout mismatch (id %d): library %zu vs _marshal %zu: build both again",
+                          kFirstStruct + i, size, kStructSize[i]);
+  }
   Py_INCREF(args[0]);
   Py_XDECREF(g_error);
   g_error = args[0];
   g_strerror = (const char* (*)(int))p[0];
-  for (int i = 0; i < kEntries; ++i) g_entry[i] = p[1 + i];
+  for (int i = 0; i < kEntries; ++i) g_entry[i] = p[kHelpers + i];
   Py_RETURN_NONE;
 }
 
