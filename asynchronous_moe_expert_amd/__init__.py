@@ -15,6 +15,7 @@ from ._native import (  # noqa: F401
     EXPORTS,
     LIB_PATH,
     MOE_BF16,
+    MOE_BIAS_ON_SCORE,
     MOE_F32,
     MOE_FP8_E4M3,
     MOE_SIGMOID,

@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(PKG, "libmoestep.so")
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+MOE_BIAS_ON_SCORE = 16  # or-ed to either: the bias is added to the gate's score, not to the logit
 
 ERR_SLOT_RANGE = 1 << 0
 ERR_EXPERT_NONLOCAL = 1 << 1
@@ -378,7 +379,9 @@ def _elsewhere(call, args, tensors, stream) -> None:
 
 def moe_route(logits, expert, w, bias=None, score: int = MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
               stream=None) -> None:
-    """logits [T][E] (f32 or bf16); out: expert [T][K] int32, w [T][K] f32."""
+    """logits [T][E] (f32 or bf16); out: expert [T][K] int32, w [T][K] f32.  bias [E] f32 moves the
+    choice only: it is added to the logits, or with score = MOE_SIGMOID | MOE_BIAS_ON_SCORE (or MOE_SOFTMAX
+    | ...) to the gate's scores, as the balancing bias of a router trained without an auxiliary loss is."""
     call, at = (_marshal or _home()).moe_route, logits.get_device()
     if stream is None and at >= 0 and at == _device():
         call(logits, expert, w, bias, score, renorm, scale, _raw_stream(at))

@@ -180,7 +180,9 @@ size_t room(const at::Tensor* t) {
 void* address(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
 int32_t score_of(int64_t v) {
-  if (v != MOE_SOFTMAX && v != MOE_SIGMOID) refuse("score must be MOE_SOFTMAX or MOE_SIGMOID, got %lld", (long long)v);
+  const int64_t gate = v & ~(int64_t)MOE_BIAS_ON_SCORE;
+  if (gate != MOE_SOFTMAX && gate != MOE_SIGMOID)
+    refuse("score must be MOE_SOFTMAX or MOE_SIGMOID, with MOE_BIAS_ON_SCORE or without, got %lld", (long long)v);
   return (int32_t)v;
 }
 

@@ -192,6 +192,8 @@ class ExpertLayer:
     """A layer whose experts are all on this rank, so that a token's K results come back together
     and nothing waits: moe_route chooses, moe_sort_rows gives the index (no row is copied), the
     grouped FFN gathers its rows from x through row_slot, moe_merge_rows applies the weights.
+    run()'s bias is a router's balancing bias, added to the gate's scores (MOE_BIAS_ON_SCORE), or with
+    bias_on_score False one of the logits; either moves the choice alone.
 
     After run() the buffers hold what a caller may want further on: expert and w ([T][K]), pos,
     counts and offsets as moe_sort_rows gives them, y (the experts' rows, before the weights).  They
@@ -199,10 +201,10 @@ class ExpertLayer:
     by side, take a layer object each (the packed weights may be shared)."""
 
     def __init__(self, E: int, H: int, I: int, K: int, act_dtype: int, w_dtype: int, T_max: int, device="cuda",
-                 score: int = N.MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0):
+                 score: int = N.MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0, bias_on_score: bool = True):
         self.E, self.H, self.I, self.K, self.T_max = E, H, I, K, T_max
         self.act_dtype, self.w_dtype = act_dtype, w_dtype
-        self.how = dict(score=score, renorm=renorm, scale=scale)
+        self.how = dict(score=score | (N.MOE_BIAS_ON_SCORE if bias_on_score else 0), renorm=renorm, scale=scale)
         dev = torch.device(device)
         n = max(T_max * K, 1)
         if T_max < 0 or n > 1 << 24:

@@ -371,19 +371,28 @@ size_t moe_combine_noalloc_max_arrivals(void);
 
 /* ---------------------------------------------------------------------- moe_route --
  * Chooses K of E experts per token and gives their weights.
- *   score_e = logits[t][e] + bias[e]  (one fp32 addition; bias NULL: the logit)
- *   expert[t][0..K-1] = the experts of the K largest scores, descending, equal scores in
+ *   rank_e = logits[t][e]             without a bias
+ *          = logits[t][e] + bias[e]   with one: a bias of the LOGITS
+ *          = s_e + bias[e]            with one and MOE_BIAS_ON_SCORE: the balancing bias that a router
+ *                                     trained without an auxiliary loss brings, added to its gate's
+ *                                     score s_e = sigmoid(logit) or softmax(logits)_e.  The two orders
+ *                                     differ (logits 4 and 1, biases 0 and 0.5: the logits' sums take
+ *                                     the first, the sigmoids' the second).
+ *   expert[t][0..K-1] = the experts of the K largest ranks, descending, equal ranks in
  *                       ascending order of e
  *   MOE_SOFTMAX : w_j = scale * exp(l_j - m) / Z with Z summed over the K chosen experts if renorm,
  *                 else over all E
  *   MOE_SIGMOID : w_j = scale * s(l_j), s(z) = 1 / (1 + exp(-z)); divided by the sum of the chosen
  *                 experts' s if renorm
- * The bias enters the choice only.  An expert whose score is NaN or -inf is never chosen (a logit
- * or bias of -inf takes an expert out); a token with fewer than K others gets expert -1 and weight
- * 0 in the positions left.  A NaN logit counts as probability 0 in Z; logits of +inf share it.
+ * The bias enters the choice only.  rank is one fp32 addition; s_e is rounded to fp32 as the weights
+ * without renorm are (so logits above 17 all have a sigmoid of 1, and the lowest of equal ranks comes
+ * first).  An expert whose logit or rank is NaN or -inf is never chosen (a logit or bias of -inf takes
+ * an expert out); a token with fewer than K others gets expert -1 and weight 0 in the positions left.
+ * A NaN logit counts as probability 0 in Z; logits of +inf share it.  The choice is over all E: there
+ * is no choice of groups of experts before it.
  * Limits: 1 <= E <= 512, 1 <= K <= min(E, 32); logits F32 or BF16 at their own alignment, any
  * pitch >= E. */
-typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1, MOE_BIAS_ON_SCORE = 16 /* or-ed to either */ } moe_score;
 
 typedef struct moe_route_args {
   int32_t T, E, K;
@@ -391,7 +400,7 @@ typedef struct moe_route_args {
   int32_t dtype;           /* MOE_F32 or MOE_BF16 */
   int64_t pitch;
   const float* bias;       /* [E], optional */
-  int32_t score;           /* moe_score */
+  int32_t score;           /* moe_score, MOE_BIAS_ON_SCORE or-ed to it or not */
   int32_t renorm;          /* 0 or 1 */
   float scale;
   int32_t* expert;         /* out [T][K] */
@@ -404,7 +413,8 @@ int moe_route(const moe_route_args* args, hipStream_t stream);
  * (the choice itself has none): dlogits[t][e] = sum_j dw[t][j] * d w_j / d l_e, zero for experts
  * that no weight depends on.  expert as moe_route gave it: -1 positions count for nothing, other
  * values outside [0, E) neither and raise MOE_ERR_EXPERT_NONLOCAL; an expert named twice by one
- * token counts twice.  dlogits has the logits' type; limits as for moe_route. */
+ * token counts twice.  MOE_BIAS_ON_SCORE in score changes nothing here.  dlogits has the logits' type;
+ * limits as for moe_route. */
 typedef struct moe_route_backward_args {
   int32_t T, E, K;
   const void* logits;      /* [T][pitch] */

@@ -7,6 +7,7 @@ from __future__ import annotations
 import numpy as np
 
 SOFTMAX, SIGMOID = 0, 1
+BIAS_ON_SCORE = 16  # or-ed to either
 
 
 def _sigmoid(z):
@@ -22,21 +23,38 @@ def _parts(l, m):
     return np.where(fine, p, 0.0)
 
 
-def choose(logits: np.ndarray, K: int, bias=None) -> np.ndarray:
-    """[T][K] int32: the K largest scores (fp32 logit + fp32 bias), ties to the lowest expert, -1
-    for positions that no expert with a score above -inf is left for."""
+def gate_scores(logits, score: int) -> np.ndarray:
+    """[T][E]: the sigmoid of each logit or the softmax of each token's; 0 for NaN and -inf."""
+    l = np.asarray(logits, np.float64)
+    if score == SIGMOID:
+        return np.where(l > -np.inf, _sigmoid(l), 0.0)
+    m = np.max(np.where(np.isnan(l), -np.inf, l), axis=1, keepdims=True)
+    p = _parts(l, m)
+    z = p.sum(1, keepdims=True)
+    return np.where(z > 0, p / np.where(z > 0, z, 1), 0.0)
+
+
+def choose(logits: np.ndarray, K: int, bias=None, score: int = SOFTMAX, gate=None) -> np.ndarray:
+    """[T][K] int32: the K largest ranks, ties to the lowest expert, -1 for positions that no expert
+    with a logit and a rank above -inf is left for.  A rank is the logit, with a bias fp32 logit +
+    fp32 bias, or with BIAS_ON_SCORE in `score` fp32 gate score + fp32 bias (the scores given as `gate`,
+    or gate_scores)."""
     with np.errstate(invalid="ignore", over="ignore"):
-        score = logits.astype(np.float32)
+        l = logits.astype(np.float32)
+        rank = l
+        if bias is not None and score & BIAS_ON_SCORE:
+            rank = (gate_scores(logits, score & ~BIAS_ON_SCORE) if gate is None else gate).astype(np.float32)
         if bias is not None:
-            score = score + np.asarray(bias, np.float32)
-    ok = score > -np.inf  # false for NaN
-    key = np.where(ok, score.astype(np.float64), -np.inf)
+            rank = rank + np.asarray(bias, np.float32)
+    ok = (l > -np.inf) & (rank > -np.inf)  # false for NaN
+    key = np.where(ok, rank.astype(np.float64), -np.inf)
     order = np.argsort(-key, axis=1, kind="stable")[:, :K]
     return np.where(np.take_along_axis(ok, order, 1), order, -1).astype(np.int32)
 
 
 def shares(logits, expert, score: int, renorm: bool) -> np.ndarray:
     """The chosen positions' weights before the scale factor, [T][K]."""
+    score &= ~BIAS_ON_SCORE
     l = np.asarray(logits, np.float64)
     there = expert >= 0
     lc = np.take_along_axis(l, np.where(there, expert, 0).astype(np.int64), 1)
@@ -52,12 +70,13 @@ def shares(logits, expert, score: int, renorm: bool) -> np.ndarray:
 
 
 def route(logits, K: int, bias=None, score: int = SOFTMAX, renorm: bool = True, scale: float = 1.0):
-    expert = choose(np.asarray(logits), K, bias)
+    expert = choose(np.asarray(logits), K, bias, score)
     return expert, scale * shares(logits, expert, score, renorm)
 
 
 def route_backward(logits, expert, dw, score: int = SOFTMAX, renorm: bool = True, scale: float = 1.0) -> np.ndarray:
     l = np.asarray(logits, np.float64)
+    score &= ~BIAS_ON_SCORE
     T, E = l.shape
     expert = np.where((expert >= 0) & (expert < E), expert, -1)
     there = expert >= 0

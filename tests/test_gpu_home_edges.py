@@ -5,6 +5,10 @@ import pytest
 import torch
 
 import asynchronous_moe_expert_amd as M
+import workloads as W
+from oracle import home as O
+from test_gpu_home import HALF, I32, ROUTES, U, errword, gpu, hard_logits, like, val, within
+from workloads.device import weight_tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +38,97 @@ def test_a_group_with_an_infinite_value_stands_for_nan(group, size):
         hit[:] = True
     assert got[:, hit].isnan().all()
     assert finite.isfinite().all() and torch.equal(got[:, ~hit], finite[:, ~hit])
+
+
+# --------------------------------------------------------------------------- the bias of the scores
+def route(logits, K, **how):
+    expert, w = like((logits.shape[0], K), I32, fill=-7), like((logits.shape[0], K), F32, fill=-7)
+    M.moe_route(logits, expert, w, **how)
+    return expert.cpu().numpy(), w
+
+
+def scores_of(logits, score):
+    """Every expert's gate score as moe_route rounds it: weights without renorm, 32 experts at a time, the others
+    taken out of the choice by a bias of the logits; NaN where an expert cannot be chosen."""
+    T, E = logits.shape
+    s = np.full((T, E), np.nan, np.float32)
+    for a in range(0, E, 32):
+        K = min(32, E - a)
+        bias = torch.full((E,), float("-inf"), device="cuda")
+        bias[a:a + K] = 0
+        expert, w = route(logits, K, bias=bias, score=score, renorm=False)
+        t, k = np.nonzero(expert >= 0)
+        s[t, expert[t, k]] = w.cpu().numpy()[t, k]
+    return s
+
+
+@pytest.mark.parametrize("E,K", ROUTES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", [M.MOE_SOFTMAX, M.MOE_SIGMOID])
+def test_route_with_a_bias_of_the_scores(E, K, dtype, score):
+    """The choice is that of fp32 score + fp32 bias, exactly, for the scores that the call itself gives as
+    weights; those are off by 4 u (sigmoid: exp 2, sum and quotient 1 each) or as the weights' bounds are."""
+    rng = np.random.default_rng(E * 100 + K + 7)
+    for T, pad, renorm in ((1, 0, True), (77, 3, False), (50, 8, True)):
+        logits = gpu(hard_logits(rng, T, E, dtype), dtype, pad)
+        l = val(logits)
+        s = scores_of(logits, score)
+        ok = l > -np.inf
+        assert np.array_equal(ok, ~np.isnan(s))
+        exact = O.gate_scores(l, score)
+        if score == M.MOE_SIGMOID:
+            tol = 4 * U * exact
+        else:
+            with np.errstate(invalid="ignore", over="ignore"):
+                top = np.nanmax(np.where(np.isfinite(l) & (np.abs(l) < 1e30), l, -np.inf), axis=1, keepdims=True)
+                size = np.where(np.isfinite(l) & np.isfinite(top), np.minimum(np.abs(l) + np.abs(top), 1e3), 0)
+            tol = exact * (60 + 4 * size) * U
+        within(np.where(ok, s, 0), np.where(ok, exact, 0), tol + 1e-37)
+        bias = np.round(rng.standard_normal(E) * 0.2, 2).astype(np.float32)  # some of them equal
+        bias[rng.random(E) < 0.1] = -np.inf
+        bias[rng.random(E) < 0.05] = np.nan
+        bias[rng.random(E) < 0.05] = np.inf
+        how = dict(score=score | M.MOE_BIAS_ON_SCORE, renorm=renorm, scale=2.5)
+        expert, w = route(logits, K, bias=gpu(bias), **how)
+        want = O.choose(l, K, bias, score | O.BIAS_ON_SCORE, gate=s)
+        assert np.array_equal(expert, want)
+        # the weights know nothing of the bias
+        share = 2.5 * O.shares(l, want, score, renorm)
+        with np.errstate(invalid="ignore", over="ignore"):
+            lc = np.take_along_axis(l, np.maximum(want, 0).astype(np.int64), 1)
+            top = np.nanmax(np.where(np.isfinite(l) & (np.abs(l) < 1e30), l, -np.inf), axis=1, keepdims=True)
+            size = np.where(np.isfinite(lc) & np.isfinite(top), np.minimum(np.abs(lc) + np.abs(top), 1e3), 0)
+        within(val(w), share, share * (60 + 4 * size) * U + 1e-37)
+        # without a bias the flag changes nothing, nor does it in the gradient
+        assert all(np.array_equal(a, b) for a, b in zip(
+            (np.asarray(v) if isinstance(v, np.ndarray) else val(v) for v in route(logits, K, **how)),
+            (np.asarray(v) if isinstance(v, np.ndarray) else val(v) for v in route(logits, K, score=score, renorm=renorm, scale=2.5))))
+        dw, err = gpu(rng.standard_normal((T, K)).astype(np.float32)), errword()
+        got = [like((T, E), dtype, fill=3) for _ in range(2)]
+        for d, sc in zip(got, (score, how["score"])):
+            M.moe_route_backward(logits, gpu(expert), dw, d, err, score=sc, renorm=renorm, scale=2.5)
+        assert torch.equal(got[0], got[1])
+
+
+def test_the_two_biases_by_hand():
+    logits, bias = torch.tensor([[4.0, 1.0, -30.0]], device="cuda"), torch.tensor([0.0, 0.5, 0.9], device="cuda")
+    for score, want in ((M.MOE_SIGMOID, [[0, 1, 2]]), (M.MOE_SIGMOID | M.MOE_BIAS_ON_SCORE, [[1, 0, 2]]),
+                        (M.MOE_SOFTMAX, [[0, 1, 2]]), (M.MOE_SOFTMAX | M.MOE_BIAS_ON_SCORE, [[0, 2, 1]])):
+        assert route(logits, 3, bias=bias, score=score)[0].tolist() == want
+
+
+@pytest.mark.parametrize("on_score", [True, False])
+def test_expert_layer_with_a_balancing_bias(on_score):
+    rng = np.random.default_rng(5)
+    T, E, K, H, I = 40, 8, 2, 64, 128
+    wts = W.gen.make_layer_weights(rng, E, H, I, 0.05, "f32")
+    w = weight_tensors(wts)
+    layer = M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, T, score=M.MOE_SIGMOID, scale=2.5, bias_on_score=on_score)
+    layer.load_weights(w["wg"], w["wu"], w["wd"])
+    logits, bias = rng.permutation(T * E).reshape(T, E) / 64.0 - 2, rng.permutation(E) / 8.0  # no near ties
+    logits, bias = logits.astype(np.float32), bias.astype(np.float32)
+    x, out = gpu(rng.standard_normal((T, H)).astype(np.float32)), like((T, H), F32)
+    layer.run(x, gpu(logits), out, bias=gpu(bias))
+    want = O.choose(logits, K, bias, O.SIGMOID | (O.BIAS_ON_SCORE if on_score else 0))
+    assert np.array_equal(layer.expert.cpu().numpy(), want)
+    assert not np.array_equal(want, O.choose(logits, K, bias, O.SIGMOID | (0 if on_score else O.BIAS_ON_SCORE)))
