@@ -354,10 +354,23 @@ def _home():
     return _marshal
 
 
+def keep_for(stream, at: int, tensors) -> None:
+    """Records what a call on `stream` works on, unless that is the current stream of the tensors'
+    device `at`, so that the allocator keeps it until the call's work is done."""
+    if stream is None:
+        return
+    handle = _stream(stream)
+    if handle == _raw_stream(at):
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(handle, device=at) if handle else torch.cuda.default_stream(at)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _elsewhere(call, args, tensors, stream) -> None:
-    """A call on a given stream, or with tensors that are not on the current device.  On a stream
-    other than the current one the tensors are recorded, so that the allocator keeps them until
-    the call's work is done."""
+    """A call on a given stream, or with tensors that are not on the current device."""
     at = tensors[0].get_device()
     if at < 0:
         call(*args, 0)  # refuses: not on a GPU
@@ -365,16 +378,9 @@ def _elsewhere(call, args, tensors, stream) -> None:
     where = getattr(stream, "device", None)
     if where is not None and where.index != at:
         raise MoeError(f"a stream of {where} for tensors on {tensors[0].device}")
-    current = _raw_stream(at)
-    handle = current if stream is None else _stream(stream)
     with torch.cuda.device(at):
-        call(*args, handle)
-    if handle != current:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(handle, device=at) if handle else torch.cuda.default_stream(at)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+        call(*args, _raw_stream(at) if stream is None else _stream(stream))
+    keep_for(stream, at, tensors)
 
 
 def moe_route(logits, expert, w, bias=None, score: int = MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0,

@@ -72,6 +72,7 @@ class ExpertStep:
         self.w_gu = torch.empty(self.E_loc * 2 * self.I * self.H, dtype=wg.dtype, device=wg.device)
         self.w_d = torch.empty(self.E_loc * self.H * self.I, dtype=wg.dtype, device=wg.device)
         N.moe_pack_ffn_weights(wg, wu, wd, self.w_gu, self.w_d, self.w_dtype, stream=stream)
+        N.keep_for(stream, wg.get_device(), (wg, wu, wd, self.w_gu, self.w_d))
         self.s_gate, self.s_up, self.s_down = s_gate, s_up, s_down
 
     def assemble(self, slot, expert, expert_base: int, pool, n: int | None = None, stream=None) -> None:
@@ -247,9 +248,9 @@ class ExpertLayer:
         N.moe_sort_rows(self.expert, self.E, None, None, None, self.pos, self.counts, self.offsets, self.err,
                         self.sort_ws, row_slot=self.row_slot, stream=stream)
         if n:
-            if hasattr(stream, "cuda_stream"):
-                x.record_stream(stream)
             N.moe_expert_ffn_grouped(n, self.E, self.H, self.I, self.act_dtype, self.w_dtype, None, self.offsets,
                                      self.w_gu, self.w_d, self.y, self.workspace, self.s_gate, self.s_up, self.s_down,
                                      stream=stream, gather=(None, None, x, self.row_slot))
+            N.keep_for(stream, x.get_device(), (x, self.row_slot, self.offsets, self.w_gu, self.w_d, self.s_gate,
+                                                self.s_up, self.s_down, self.y, self.workspace))
         N.moe_merge_rows(self.y[:n], self.pos[:n], self.w, out, self.err, stream=stream)

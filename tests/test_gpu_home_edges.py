@@ -132,3 +132,37 @@ def test_expert_layer_with_a_balancing_bias(on_score):
     want = O.choose(logits, K, bias, O.SIGMOID | (O.BIAS_ON_SCORE if on_score else 0))
     assert np.array_equal(layer.expert.cpu().numpy(), want)
     assert not np.array_equal(want, O.choose(logits, K, bias, O.SIGMOID | (0 if on_score else O.BIAS_ON_SCORE)))
+
+
+# ----------------------------------------------------------------------------------- other streams
+@pytest.mark.parametrize("raw", [True, False])
+def test_a_layer_and_its_input_may_go_while_another_stream_works(raw):
+    """x, the weights and the layer are dropped as soon as run() returns, behind work that keeps the side
+    stream busy; what the allocator hands out meanwhile is other memory."""
+    rng = np.random.default_rng(6)
+    T, E, K, H, I = 64, 8, 2, 256, 256
+    w = weight_tensors(W.gen.make_layer_weights(rng, E, H, I, 0.05, "f32"))
+    x0, logits = gpu(rng.standard_normal((T, H)).astype(np.float32)), gpu(rng.standard_normal((T, E)).astype(np.float32))
+    outs = []
+    s = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    for other in (False, True):
+        layer = M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, T)
+        wg, wu, wd = (w[k].clone() for k in ("wg", "wu", "wd"))
+        x, out = x0.clone(), torch.zeros(T, H, device="cuda")
+        torch.cuda.synchronize()
+        handle = None
+        if other:
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    busy @ busy
+            handle = s.cuda_stream if raw else s
+        layer.load_weights(wg, wu, wd, stream=handle)
+        layer.run(x, logits, out, stream=handle)
+        sizes = [t.numel() * t.element_size() for t in (x, wg, wu, wd, layer.w_gu, layer.w_d, layer.workspace, layer.y)]
+        del layer, x, wg, wu, wd
+        taken = [torch.full((n,), 0xee, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        del taken
+        outs.append(out)
+    assert outs[0].abs().max() > 0 and torch.equal(outs[0], outs[1])

@@ -1,0 +1,44 @@
+"""ExpertLayer's plumbing on the CPU: what it hands to the allocator and what it refuses, with the calls
+themselves left out."""
+import pytest
+import torch
+
+import asynchronous_moe_expert_amd as M
+from asynchronous_moe_expert_amd import _native as N
+
+T, E, K, H, I = 5, 8, 2, 64, 128
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The names of the calls that run() makes; none of them does anything."""
+    made = []
+    for name in ("moe_route", "moe_sort_rows", "moe_expert_ffn_grouped", "moe_merge_rows", "moe_pack_ffn_weights"):
+        monkeypatch.setattr(N, name, lambda *a, name=name, **k: made.append(name))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)  # that of tensors on the CPU
+    return made
+
+
+def layer(**how):
+    made = M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, T, device="cpu", **how)
+    made.load_weights(torch.zeros(E, I, H), torch.zeros(E, I, H), torch.zeros(E, H, I))
+    return made
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_a_run_on_another_stream_records_what_it_works_on(calls, monkeypatch, raw):
+    class Stream:
+        cuda_stream = 77
+
+    recorded = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: Stream())
+    monkeypatch.setattr(N, "_raw_stream", lambda index: 5)
+    one, x, logits, out = layer(), torch.zeros(T, H), torch.zeros(T, E), torch.zeros(T, H)
+    one.s_gate = torch.zeros(3)
+    for stream in (None, 5):  # the current one
+        one.run(x, logits, out, stream=stream)
+    assert not recorded
+    one.run(x, logits, out, stream=77 if raw else Stream())
+    for t in (x, one.w_gu, one.w_d, one.s_gate, one.workspace, one.y, one.row_slot, one.offsets):
+        assert (t.data_ptr(), 77) in recorded
