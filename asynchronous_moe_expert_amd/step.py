@@ -194,7 +194,8 @@ class ExpertLayer:
     and nothing waits: moe_route chooses, moe_sort_rows gives the index (no row is copied), the
     grouped FFN gathers its rows from x through row_slot, moe_merge_rows applies the weights.
     run()'s bias is a router's balancing bias, added to the gate's scores (MOE_BIAS_ON_SCORE), or with
-    bias_on_score False one of the logits; either moves the choice alone.
+    bias_on_score False one of the logits; either moves the choice alone.  1 <= E <= 256 (what
+    moe_sort_rows and the FFN take on one rank), 1 <= K <= min(E, 32).
 
     After run() the buffers hold what a caller may want further on: expert and w ([T][K]), pos,
     counts and offsets as moe_sort_rows gives them, y (the experts' rows, before the weights).  They
@@ -210,6 +211,9 @@ class ExpertLayer:
         n = max(T_max * K, 1)
         if T_max < 0 or n > 1 << 24:
             raise N.MoeError(f"ExpertLayer: T_max {T_max} with K {K} is over the documented limits")
+        if not 1 <= E <= 256 or not 1 <= K <= min(E, 32):
+            raise N.MoeError(f"ExpertLayer: {K} of {E} experts; 1 to 256 experts fit on one rank, of which 1 to 32 "
+                             "are chosen")
         self._expert = torch.empty(n, dtype=torch.int32, device=dev)
         self._w = torch.empty(n, dtype=torch.float32, device=dev)
         self.pos = torch.empty(n, dtype=torch.int32, device=dev)

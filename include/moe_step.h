@@ -391,7 +391,8 @@ size_t moe_combine_noalloc_max_arrivals(void);
  * A NaN logit counts as probability 0 in Z; logits of +inf share it.  The choice is over all E: there
  * is no choice of groups of experts before it.
  * Limits: 1 <= E <= 512, 1 <= K <= min(E, 32); logits F32 or BF16 at their own alignment, any
- * pitch >= E. */
+ * pitch >= E.  E counts the layer's experts; moe_sort_rows and moe_expert_ffn_grouped take at most
+ * 256 of them per call, those of one rank (expert_base). */
 typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1, MOE_BIAS_ON_SCORE = 16 /* or-ed to either */ } moe_score;
 
 typedef struct moe_route_args {

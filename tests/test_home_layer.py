@@ -42,3 +42,14 @@ def test_a_run_on_another_stream_records_what_it_works_on(calls, monkeypatch, ra
     one.run(x, logits, out, stream=77 if raw else Stream())
     for t in (x, one.w_gu, one.w_d, one.s_gate, one.workspace, one.y, one.row_slot, one.offsets):
         assert (t.data_ptr(), 77) in recorded
+
+
+@pytest.mark.parametrize("E,K", [(257, 4), (512, 8), (0, 1), (8, 0), (8, 9), (64, 33)])
+def test_sizes_that_no_call_takes_are_refused_when_the_layer_is_built(E, K):
+    with pytest.raises(M.MoeError, match="256 experts"):
+        M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, 4, device="cpu")
+
+
+def test_the_largest_sizes_are_taken():
+    for E, K in ((256, 32), (1, 1), (256, 1)):
+        M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, 4, device="cpu")
