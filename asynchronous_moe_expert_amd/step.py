@@ -247,6 +247,14 @@ class ExpertLayer:
             raise N.MoeError(f"ExpertLayer: {T} tokens, built for {self.T_max}")
         if x.shape != (T, self.H) or x.stride(1) != 1 or x.dtype != _TORCH[self.act_dtype] or logits.shape != (T, self.E):
             raise N.MoeError(f"ExpertLayer: x {tuple(x.shape)} {x.dtype} with logits {tuple(logits.shape)}")
+        if out.shape != x.shape:
+            raise N.MoeError(f"ExpertLayer: out {tuple(out.shape)} for x {tuple(x.shape)}")
+        if self.w_gu is None:
+            raise N.MoeError("ExpertLayer: load_weights() comes before run()")
+        if T == 1:  # its pitch, which a view may give any value, says nothing
+            x = x.as_strided((1, self.H), (self.H, 1))
+        elif T and x.stride(0) < self.H:
+            raise N.MoeError(f"ExpertLayer: x's rows overlap (stride {x.stride(0)} for {self.H} elements)")
         self.expert, self.w = self._expert[:n].view(T, self.K), self._w[:n].view(T, self.K)
         N.moe_route(logits, self.expert, self.w, bias=bias, stream=stream, **self.how)
         N.moe_sort_rows(self.expert, self.E, None, None, None, self.pos, self.counts, self.offsets, self.err,

@@ -53,3 +53,25 @@ def test_sizes_that_no_call_takes_are_refused_when_the_layer_is_built(E, K):
 def test_the_largest_sizes_are_taken():
     for E, K in ((256, 32), (1, 1), (256, 1)):
         M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, 4, device="cpu")
+
+
+def test_a_refused_run_makes_no_call(calls):
+    one, x, logits, out = layer(), torch.zeros(T, H), torch.zeros(T, E), torch.zeros(T, H)
+    del calls[:]
+    for bad, text in (((x, logits, out[:3]), "out"), ((x, logits, torch.zeros(T, H + 8)), "out"),
+                      ((x[:1].expand(T, H), logits, out), "overlap"), ((x, logits[:2], out), "logits")):
+        with pytest.raises(M.MoeError, match=text):
+            one.run(*bad)
+    with pytest.raises(M.MoeError, match="load_weights"):
+        M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, T, device="cpu").run(x, logits, out)
+    assert not calls
+
+
+def test_one_token_may_have_any_pitch(calls, monkeypatch):
+    """The row of a [H][1] column's transpose is one run of H elements whatever its stride says."""
+    seen = []
+    monkeypatch.setattr(N, "moe_expert_ffn_grouped", lambda *a, gather, **k: seen.append(gather[2]))
+    x = torch.arange(float(H)).view(H, 1).t()
+    assert x.stride() == (1, 1)
+    layer().run(x, torch.zeros(1, E), torch.zeros(1, H))
+    assert seen[0].stride() == (H, 1) and torch.equal(seen[0], x)
