@@ -160,6 +160,15 @@ void* vec(const char* what, const at::Tensor* t, int64_t n, unsigned types) {
   return t->data_ptr();
 }
 
+// What vec() takes as the first rows of a [][cols] array: flat, or with as many columns.
+void* table(const char* what, const at::Tensor* t, int64_t rows, int64_t cols, unsigned types) {
+  void* p = vec(what, t, rows * cols, types);
+  if (t && rows && t->dim() != 1 && (t->dim() != 2 || t->size(1) != cols))
+    refuse("%s: %lld dimensions, the last of %lld; %lld columns expected", what, (long long)t->dim(),
+           (long long)(t->dim() ? t->size(-1) : 0), (long long)cols);
+  return p;
+}
+
 // A contiguous [T][K] tensor of type `k`; its address.
 void* each(const char* what, const at::Tensor& t, int64_t T, int64_t K, unsigned k) {
   mat(what, t, T, K, k);
@@ -189,6 +198,8 @@ int32_t score_of(int64_t v) {
 // pos: T x K whole numbers in token order ([T][K] or flat), w like it or nothing; K
 int64_t positions(const at::Tensor& pos, const at::Tensor* w, int64_t T) {
   const int64_t n = pos.numel(), K = T ? n / T : pos.dim() > 1 ? pos.size(-1) : 1;
+  if (pos.dim() > 1 && pos.size(0) != T)
+    refuse("pos: %lld rows for %lld tokens", (long long)pos.size(0), (long long)T);
   if (n != T * K) refuse("pos: %lld elements are not a whole number for each of %lld tokens", (long long)n, (long long)T);
   if (w && w->numel() != n) refuse("w: %lld elements, %lld expected", (long long)w->numel(), (long long)n);
   return K;
@@ -261,12 +272,12 @@ PyObject* sort_rows(Call& c) {
     a.xs = xs->data_ptr();
     if (a.x_dtype == MOE_FP8_E4M3) {
       if (!x_scale) refuse("x_scale: required for fp8 rows");
-      a.x_scale = (const float*)vec("x_scale", x_scale, s.rows * groups(H, group), F32);
+      a.x_scale = (const float*)table("x_scale", x_scale, s.rows, groups(H, group), F32);
       a.group = (int32_t)group;
     }
   }
   a.perm = (int32_t*)vec("perm", perm, n, I32);
-  a.pos = (int32_t*)vec("pos", &pos, n, I32);
+  a.pos = (int32_t*)table("pos", &pos, s.rows, s.cols, I32);
   a.counts = (int32_t*)vec("counts", &counts, E_loc, I32);
   a.offsets = (int32_t*)vec("offsets", &offsets, E_loc + 1, I32);
   a.row_slot = (int32_t*)vec("row_slot", row_slot, n, I32);
@@ -288,8 +299,8 @@ PyObject* merge_rows(Call& c) {
   a.row_pitch = mat("rows", rows, a.n_rows, s.cols, F32 | BF16);
   a.rows = rows.data_ptr();
   a.row_dtype = code(rows);
-  a.pos = (const int32_t*)vec("pos", &pos, s.rows * K, I32);
-  a.w = (const float*)vec("w", w, s.rows * K, F32);
+  a.pos = (const int32_t*)table("pos", &pos, s.rows, K, I32);
+  a.w = (const float*)table("w", w, s.rows, K, F32);
   a.out_pitch = mat("out", out, s.rows, s.cols, F32 | BF16);
   a.out = out.data_ptr();
   a.out_dtype = code(out);
@@ -323,9 +334,9 @@ PyObject* merge_rows_backward(Call& c) {
     a.drows = drows->data_ptr();
   }
   a.row_dtype = code(*one);
-  a.pos = (const int32_t*)vec("pos", &pos, s.rows * K, I32);
-  a.w = (const float*)vec("w", w, s.rows * K, F32);
-  a.dw = (float*)vec("dw", dw, s.rows * K, F32);
+  a.pos = (const int32_t*)table("pos", &pos, s.rows, K, I32);
+  a.w = (const float*)table("w", w, s.rows, K, F32);
+  a.dw = (float*)table("dw", dw, s.rows, K, F32);
   a.err = (uint32_t*)vec("err", &err, 1, I32);
   return c.run(kMergeBack, &a);
 }
@@ -364,7 +375,7 @@ PyObject* residual_norm(Call& c) {
   a.out_dtype = code(out);
   if (a.out_dtype == MOE_FP8_E4M3) {
     if (!out_scale) refuse("out_scale: required for fp8 output");
-    a.out_scale = (float*)vec("out_scale", out_scale, s.rows * groups(s.cols, group), F32);
+    a.out_scale = (float*)table("out_scale", out_scale, s.rows, groups(s.cols, group), F32);
     a.group = (int32_t)group;
   }
   a.rstd = (float*)vec("rstd", rstd, s.rows, F32);
