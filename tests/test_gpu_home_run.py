@@ -301,7 +301,7 @@ def test_offsets_past_32_bits():
     assert torch.equal(e1, e2) and torch.equal(w1, w2)
 
 
-# Calls that move 96 MiB of rows or more read them non-temporally, from 192 MiB on they write so too.
+# Calls that move 96 MiB of rows or more read them non-temporally, from 220 MiB on they write so too.
 LARGE = [(5000, 4, 2880), (9600, 4, 2880)]
 
 
