@@ -97,9 +97,8 @@ __device__ __forceinline__ float over(float v, float s, float inv) {
 }
 
 // How a group's values become 8-bit codes.  r scales all of a row, so it cancels in y / scale: the
-// code of z = h gamma is z (448 / max|z|), two roundings where y / scale has six, and fewer codes
-// fall on the wrong side of a border (of 201 million codes 2782 are not those of a 64-bit
-// evaluation, 4455 with y / scale in fp32).  z is used while r and the group's max|z| are of ordinary size
+// code of z = h gamma is z (448 / max|z|), two roundings where y / scale has six, so that fewer codes
+// fall on the wrong side of a border.  z is used while r and the group's max|z| are of ordinary size
 // (`plain` rows: 2^-40 <= r <= 2^40); other rows hold y itself, and groups past the limits go
 // through y / scale, which makes every code of a group with an infinite y NaN.
 constexpr float kOrdinary = -1.f;  // no reciprocal of a scale is negative; that of an infinite one is 0

@@ -53,8 +53,9 @@ extern "C" {
 #define MOE_STEP_VERSION 2  /* 2: moe_ffn_args.index */
 
 /* Element storage types.  MOE_BF16 is bfloat16; MOE_FP8_E4M3 is OCP 8-bit float E4M3
- * (bias 7, max 448, no infinities), used for weights only, with one fp32 scale per
- * weight row (represented value = code value * row scale). */
+ * (bias 7, max 448, no infinities): weights, with one fp32 scale per weight row (represented
+ * value = code value * row scale), and the rows that moe_residual_norm writes and moe_sort_rows
+ * reads, with a scale per row or per group of columns. */
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
 
 /* Host-side return codes. */
@@ -526,8 +527,16 @@ int moe_merge_rows_backward(const moe_merge_rows_backward_args* args, hipStream_
  * out_dtype MOE_FP8_E4M3: out_scale is [T][ceil(H / group)], one scale per `group` columns (32, 64
  * or 128; the last group may be shorter), or [T] for group = 0; over a group
  *   scale = max|y| / 448, at least the smallest normal fp32 (1 where all are 0),
- *   code  = y / scale to nearest even, by the reciprocal of scale.
- * A NaN keeps a NaN code; a group that holds an infinity stands for NaN.
+ *   code  = y / scale to nearest even.
+ * r is the same for a whole row and leaves the quotient: where it and the group's largest z = h * gamma
+ * are of ordinary size (2^-40 <= r <= 2^40, 2^-60 <= max|z| <= 2^80) the call computes
+ *   scale = max|z| * r / 448,  code = z * (448 / max|z|)
+ * and elsewhere the quotient by the reciprocal of scale.  A value within a few 2^-24 of the border of
+ * two codes may take either.
+ * What is not finite: a NaN has a NaN code and no part in the maximum; a group with an infinite y (an
+ * infinite gamma, an h * gamma past fp32) has NaN codes throughout.  The sum of the squares is fp32: a row
+ * with an infinite h, or with finite ones of about 1e19 and more, has r = 0, so that y is 0 where h is
+ * finite and NaN where it is not.
  * row_list, row_count (both or neither): only the rows row_list[0 .. *row_count - 1] are computed, the others
  * left as they were (moe_combine_release's rel_list and rel_count, for the rows that a step
  * released).  row_list has T entries, *row_count is read on the device and cut to [0, T]; an entry

@@ -40,6 +40,28 @@ def test_a_group_with_an_infinite_value_stands_for_nan(group, size):
     assert finite.isfinite().all() and torch.equal(got[:, ~hit], finite[:, ~hit])
 
 
+@pytest.mark.parametrize("out", [F32, FP8])
+def test_rows_whose_squares_leave_fp32(out):
+    """r is 0 for a row with an infinite h, or whose sum of squares passes fp32's range: y is 0 where h is finite
+    and NaN where it is not; a NaN makes the whole row NaN.  The row beside them is as without them."""
+    H = 256
+    x = torch.ones(5, H, device="cuda")
+    x[1, 7] = float("inf")
+    x[2] = 1e25
+    x[3, 9] = float("nan")
+    gamma = torch.ones(H, device="cuda")
+    got, rstd = torch.zeros(5, H, dtype=F32 if out == F32 else torch.uint8, device="cuda"), torch.full((5,), 9.0, device="cuda")
+    scale = torch.zeros(5, H // 32, device="cuda") if out == FP8 else None
+    M.moe_residual_norm(x, None, gamma, 0.0, got, rstd=rstd, out_scale=scale, group=32)
+    y = got if out == F32 else got.view(FP8).float() * scale.repeat_interleave(32, 1)
+    y, finite = y.cpu(), torch.ones(H, dtype=torch.bool)
+    finite[7] = False
+    assert rstd.cpu()[:3].tolist() == [1, 0, 0] and rstd[3].isnan()
+    assert (y[1][finite] == 0).all() and y[1, 7].isnan() and (y[2] == 0).all() and y[3].isnan().all()
+    # 448 codes times 1 / 448: two roundings
+    assert (y[[0, 4]] - 1).abs().max() <= 2 * U
+
+
 # --------------------------------------------------------------------------- the bias of the scores
 def route(logits, K, **how):
     expert, w = like((logits.shape[0], K), I32, fill=-7), like((logits.shape[0], K), F32, fill=-7)
