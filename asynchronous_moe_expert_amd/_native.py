@@ -327,7 +327,9 @@ def combine_call(a: CombineArgs, part: str = "release", stream=None) -> None:
 # The checks of these calls' tensors (device, type, shape, stride) and their argument structs are
 # made by the compiled module _marshal, which costs a call 0.3 us where the same in Python took
 # 2-5 us beside a launch of 3 us.  Tensors on another device than the current one are worked on
-# where they are.
+# where they are.  The calls write into the given buffers and record nothing for torch's autograd,
+# whether a tensor requires a gradient or not: the gradients are calls of their own, which a training
+# step (or a torch.autograd.Function around a pair of them) makes itself.
 
 _marshal = None
 _HOME = ("moe_route", "moe_route_backward", "moe_sort_rows", "moe_merge_rows", "moe_merge_rows_backward",
