@@ -120,7 +120,7 @@ __device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
   return {s, back, 1.f / s};
 }
 
-// Bound by memory: 16384 x 4096 bf16 with the residual, 8 bits out, 470 MB in 80 us (5.9 TB/s); 8192 x
+// Bound by memory: 16384 x 4096 bf16 with the residual, 8 bits out, 470 MB in 80 us a call (5.9 TB/s); 8192 x
 // 2880, bf16 out, 189 MB in 32 us.  The fp8 outputs' arithmetic shows as well (84 us before the
 // ordinary groups had their own branch).  A call of 64 rows is launch and latency, 4.0 us.  Rows of
 // four chunks per thread in bf16 are held to six waves per SIMD, three workgroups per CU (4096 x 16384
@@ -238,7 +238,7 @@ struct NormBackJob {
 //   dh = r g - h r^2 <r g, h> / H + dres,  dgamma = sum_t (dout r) h
 // so that dout r is formed once and serves both.  A workgroup takes the rows blockIdx, blockIdx +
 // gridDim, ... , the next row's loads in flight, and keeps its share of dgamma in registers.
-// 8191 x 2880 bf16, 189 MB: 34 us (5.6 TB/s) and 4.7 us for the sum of the 512 shares; the arithmetic
+// 8191 x 2880 bf16, 189 MB: 34 us (5.5 TB/s) and 4.6 us for the sum of the 512 shares; the arithmetic
 // is half of that time (36 us with h r and gamma formed anew for each row).  256 workgroups 46 us in
 // all, 512 40 before that change, 1024 39 with twice the workspace; a second row in flight changes nothing.
 // MANY (C = 1): several rows at a time in a workgroup, row_threads threads to a row, so that short rows

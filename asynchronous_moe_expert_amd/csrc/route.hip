@@ -213,10 +213,6 @@ __device__ __forceinline__ void order(Candidate& a, Candidate& b) {  // the larg
   a = x;
 }
 
-// Bound by its instructions: 16384 tokens x 256 fp32, top-8, sigmoid with bias move 18 MB (4 us) and
-// take 6.8 us; K rounds of a maximum over the row took 10.3, and with a 32-bit maximum, a search for its
-// lowest expert and lanes that each loaded 64 consecutive bytes 17.0.  A small call (64 tokens) is
-// launch and latency, 2.8 us.
 // The N largest of a row's candidates, descending, in every lane: sorting networks of N = 4 or 8.
 // Two descending lists a, b have their N largest in max(a[i], b[N - 1 - i]), which rises and falls
 // once and is sorted by halving.
@@ -268,6 +264,11 @@ __device__ __forceinline__ void largest_sorted(const Candidate* c, Candidate* a)
   merge_dpp<N, kDppMirror>(a);
 }
 
+// Bound by its instructions: 16384 tokens x 256 fp32, top-8, sigmoid with bias move 18 MB (4 us) and
+// take 8.0 us a call (the kernel 7.6 in the median of 20, 6.6 the fastest); K rounds of a maximum over the
+// row took 10.3, and with a 32-bit maximum, a search for its lowest expert and lanes that each loaded 64
+// consecutive bytes 17.0.  A small call (64 tokens) is launch and latency, the kernel 2.9 us.  K > 8 takes
+// the rounds: 16384 x 512, top-10, 20 us.
 // N = 4, 8: the N >= K largest by sorting networks.  N = 0 (K > 8): K rounds, each taking the row's
 // largest candidate, the maximum of the lane's own and then of the 16 lanes, which its owner strikes
 // out.  ON_SCORE: there is a bias, of the gate's scores and not of the logits.
@@ -394,7 +395,7 @@ __global__ __launch_bounds__(kRouteT) void route_backward_kernel(RouteJob j, con
   for (int q = 0; q < V; ++q) d[q] = all ? l[q] * each : 0.f;
   // the chosen experts' part through the token's row in LDS, which only its own 16 lanes touch: each
   // position marks its expert, and where none finds another's mark no expert is named twice and
-  // each writes its value (forward and gradient of 16384 x 256, top-8: 17.0 us; 18.9 with every position
+  // each writes its value (forward and gradient of 16384 x 256, top-8, softmax over all: 17.1 us; 18.9 with every position
   // held against every expert, as the other branch does)
   constexpr int W = V < 4 ? V : 4;
   __shared__ __attribute__((aligned(16))) float s_row[kRouteTok][16 * V];

@@ -234,8 +234,8 @@ struct Carried {
 };
 
 // A workgroup per token (blockIdx, blockIdx + gridDim, ...), in a block that covers the row in the
-// fewest passes (8192 tokens to 8 rows of 4096 bf16, 604 MB: 100 us, 6.0 TB/s; blocks of 128 threads
-// 103).  Bound by the writes: a standalone probe that writes each 16 bytes to eight places reaches
+// fewest passes (8192 tokens to 8 rows of 4096 bf16, 604 MB: 103 us in the median of 20 launches, 5.9 TB/s,
+// 97 the fastest; blocks of 128 threads 3% more).  Bound by the writes: a standalone probe that writes each 16 bytes to eight places reaches
 // 5.8 TB/s.
 template <int DT, bool NT>
 __global__ __launch_bounds__(512) void sort_copy_kernel(CopyJob c, int T, const int32_t* __restrict__ pos) {
