@@ -104,14 +104,46 @@ class ResidualNormBackwardArgs(C.Structure):
                 ("dresidual_pitch", _i64), ("dgamma", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t)]
 
 
+class ExpertMatmulArgs(C.Structure):
+    _fields_ = [("n", _i32), ("E_loc", _i32), ("N", _i32), ("D", _i32), ("offsets", _p), ("x", _p), ("dtype", _i32),
+                ("x_rows", _i64), ("x_pitch", _i64), ("row_slot", _p), ("x_scale", _p), ("w", _p),
+                ("w_transposed", _i32), ("w_pitch", _i64), ("w_stride", _i64), ("w_scale", _p), ("out", _p),
+                ("out_dtype", _i32), ("out_pitch", _i64), ("err", _p)]
+
+
+class ExpertMatmulBackwardArgs(C.Structure):
+    _fields_ = [("n", _i32), ("E_loc", _i32), ("N", _i32), ("D", _i32), ("offsets", _p), ("dout", _p),
+                ("dout_pitch", _i64), ("x", _p), ("x_pitch", _i64), ("dtype", _i32), ("accumulate", _i32), ("dw", _p),
+                ("dw_dtype", _i32), ("dw_pitch", _i64), ("dw_stride", _i64)]
+
+
+class SwigluArgs(C.Structure):
+    _fields_ = [("n", _i32), ("I", _i32), ("gu", _p), ("dtype", _i32), ("gu_pitch", _i64), ("count", _p), ("h", _p),
+                ("h_dtype", _i32), ("h_pitch", _i64), ("h_scale", _p), ("group", _i32)]
+
+
+class SwigluBackwardArgs(C.Structure):
+    _fields_ = [("n", _i32), ("I", _i32), ("gu", _p), ("dtype", _i32), ("gu_pitch", _i64), ("dh", _p),
+                ("dh_pitch", _i64), ("count", _p), ("dgu", _p), ("dgu_pitch", _i64), ("h", _p), ("h_pitch", _i64)]
+
+
+class QuantizeWeightsArgs(C.Structure):
+    _fields_ = [("E_loc", _i32), ("N", _i32), ("D", _i32), ("w", _p), ("dtype", _i32), ("w_pitch", _i64),
+                ("w_stride", _i64), ("transposed", _i32), ("codes", _p), ("codes_pitch", _i64),
+                ("codes_stride", _i64), ("scale", _p)]
+
+
 _STRUCTS = [AssembleArgs, PackArgs, FfnArgs, StateC, CombineArgs, RouteArgs, RouteBackwardArgs, SortRowsArgs,
-            MergeRowsArgs, MergeRowsBackwardArgs, ResidualNormArgs, ResidualNormBackwardArgs]
+            MergeRowsArgs, MergeRowsBackwardArgs, ResidualNormArgs, ResidualNormBackwardArgs, ExpertMatmulArgs,
+            ExpertMatmulBackwardArgs, SwigluArgs, SwigluBackwardArgs, QuantizeWeightsArgs]
 EXPORTS = ["moe_assemble", "moe_pack_ffn_weights", "moe_ffn_workspace_size", "moe_expert_ffn_grouped",
            "moe_state_reset", "moe_combine_release", "moe_combine_plan", "moe_combine_apply",
            "moe_combine_workspace_size", "moe_strerror", "moe_version", "moe_struct_size",
            "moe_combine_release_noalloc", "moe_combine_noalloc_max_arrivals", "moe_route", "moe_route_backward",
            "moe_sort_rows", "moe_sort_rows_workspace_size", "moe_merge_rows", "moe_merge_rows_backward",
-           "moe_residual_norm", "moe_residual_norm_backward", "moe_residual_norm_backward_workspace_size"]
+           "moe_residual_norm", "moe_residual_norm_backward", "moe_residual_norm_backward_workspace_size",
+           "moe_expert_matmul", "moe_expert_matmul_backward", "moe_swiglu", "moe_swiglu_backward",
+           "moe_quantize_weights"]
 
 
 class MoeError(RuntimeError):
@@ -145,6 +177,11 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                        ("moe_merge_rows_backward", [_p, _p]),
                        ("moe_residual_norm", [_p, _p]),
                        ("moe_residual_norm_backward", [_p, _p]),
+                       ("moe_expert_matmul", [_p, _p]),
+                       ("moe_expert_matmul_backward", [_p, _p]),
+                       ("moe_swiglu", [_p, _p]),
+                       ("moe_swiglu_backward", [_p, _p]),
+                       ("moe_quantize_weights", [_p, _p]),
                        ("moe_version", []), ("moe_strerror", [C.c_int])]:
         f = getattr(lib, name)
         f.argtypes = args
@@ -323,7 +360,7 @@ def combine_call(a: CombineArgs, part: str = "release", stream=None) -> None:
     _check(getattr(load(), fn)(C.byref(a), _stream(stream)), fn)
 
 
-# ------------------------------------------------------------------ the home rank's side
+# ------------------------------------------------- the home rank's side and the experts' products
 # The checks of these calls' tensors (device, type, shape, stride) and their argument structs are
 # made by the compiled module _marshal, which costs a call 0.3 us where the same in Python took
 # 2-5 us beside a launch of 3 us.  Tensors on another device than the current one are worked on
@@ -333,7 +370,8 @@ def combine_call(a: CombineArgs, part: str = "release", stream=None) -> None:
 
 _marshal = None
 _HOME = ("moe_route", "moe_route_backward", "moe_sort_rows", "moe_merge_rows", "moe_merge_rows_backward",
-         "moe_residual_norm", "moe_residual_norm_backward")
+         "moe_residual_norm", "moe_residual_norm_backward", "moe_expert_matmul", "moe_expert_matmul_backward",
+         "moe_swiglu", "moe_swiglu_backward", "moe_quantize_weights")
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -478,3 +516,62 @@ def moe_residual_norm_backward(dout, h, gamma, rstd, dx, dgamma, workspace, dres
     else:
         t = (dout, h, gamma, rstd, dx, dgamma, workspace, dres, dresidual)
         _elsewhere(call, t, t, stream)
+
+
+def moe_expert_matmul(x, w, offsets, out, err=None, row_slot=None, x_scale=None, w_scale=None, transposed: bool = False,
+                      stream=None) -> None:
+    """x [n][D], or with row_slot [n] (and err) [rows][D]; w [E][N][D], transposed [E][D][N]; offsets [E + 1] int32;
+    out [n][N].  f32, bf16 (out bf16 or f32), or fp8 with x_scale [rows][ceil(D / 128)] and w_scale
+    [E][ceil(N / 128)][ceil(D / 128)] f32 (out bf16 or f32).  Any strides of rows and matrices.  With transposed
+    and the gradient of a forward product's out as x, out is the gradient of its rows."""
+    call, at = (_marshal or _home()).moe_expert_matmul, x.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(x, w, offsets, out, err, row_slot, x_scale, w_scale, transposed, _raw_stream(at))
+    else:
+        t = (x, w, offsets, out, err, row_slot, x_scale, w_scale)
+        _elsewhere(call, t + (transposed,), t, stream)
+
+
+def moe_expert_matmul_backward(dout, x, offsets, dw, accumulate: bool = False, stream=None) -> None:
+    """dout [n][N] and x [n][D] of one type (f32 or bf16), offsets [E + 1]; out: dw [E][N][D] (f32, or bf16 from
+    bf16), added to with accumulate."""
+    call, at = (_marshal or _home()).moe_expert_matmul_backward, dout.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(dout, x, offsets, dw, accumulate, _raw_stream(at))
+    else:
+        t = (dout, x, offsets, dw)
+        _elsewhere(call, t + (accumulate,), t, stream)
+
+
+def moe_swiglu(gu, h, h_scale=None, group: int = 0, count=None, stream=None) -> None:
+    """gu [n][2 I] (f32 or bf16): gate columns, then up columns; h [n][I] f32, bf16 or fp8 (then h_scale
+    [n][groups] f32).  count: one int32 on the device, the rows to compute (offsets[E:] for the rows that
+    moe_sort_rows placed)."""
+    call, at = (_marshal or _home()).moe_swiglu, gu.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(gu, h, h_scale, count, group, _raw_stream(at))
+    else:
+        t = (gu, h, h_scale, count)
+        _elsewhere(call, t + (group,), t, stream)
+
+
+def moe_swiglu_backward(gu, dh, dgu, h=None, count=None, stream=None) -> None:
+    """gu and dgu [n][2 I], dh and (optional, the forward's rows again) h [n][I], all f32 or all bf16.  dgu may
+    be gu."""
+    call, at = (_marshal or _home()).moe_swiglu_backward, gu.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(gu, dh, dgu, h, count, _raw_stream(at))
+    else:
+        t = (gu, dh, dgu, h, count)
+        _elsewhere(call, t, t, stream)
+
+
+def moe_quantize_weights(w, codes, scale, transposed: bool = False, stream=None) -> None:
+    """w [E][N][D] f32 or bf16; out: codes [E][N][D] fp8 and scale [E][ceil(N / 128)][ceil(D / 128)] f32, or with
+    transposed those of each w[e]'s transpose."""
+    call, at = (_marshal or _home()).moe_quantize_weights, w.get_device()
+    if stream is None and at >= 0 and at == _device():
+        call(w, codes, scale, transposed, _raw_stream(at))
+    else:
+        t = (w, codes, scale)
+        _elsewhere(call, t + (transposed,), t, stream)

@@ -32,6 +32,11 @@ extern "C" size_t moe_struct_size(int which) {
     case 9: return sizeof(moe_merge_rows_backward_args);
     case 10: return sizeof(moe_residual_norm_args);
     case 11: return sizeof(moe_residual_norm_backward_args);
+    case 12: return sizeof(moe_expert_matmul_args);
+    case 13: return sizeof(moe_expert_matmul_backward_args);
+    case 14: return sizeof(moe_swiglu_args);
+    case 15: return sizeof(moe_swiglu_backward_args);
+    case 16: return sizeof(moe_quantize_weights_args);
     default: return 0;
   }
 }

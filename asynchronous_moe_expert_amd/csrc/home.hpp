@@ -1,6 +1,9 @@
-// Device helpers of the home rank's operators (route.hip, rows.hip, norm.hip): eight elements of
+// Device helpers of the home rank's operators (route.hip, rows.hip, norm.hip) and of the
+// experts' products (products.hip, swiglu.hip): eight elements of
 // a row as fp32 in registers, sums and maxima over lanes, and launches that report their own error.
 #pragma once
+
+#include <float.h>
 
 #include "common.hpp"
 
@@ -148,6 +151,47 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ float wave_max(float v) {
   v = max16(v);
   return fmaxf(fmaxf(lane_f32(v, 0), lane_f32(v, 16)), fmaxf(lane_f32(v, 32), lane_f32(v, 48)));
+}
+
+// the maximum over aligned runs of 4, 8 or 16 lanes
+__device__ __forceinline__ float run_max(float v, int lanes) {
+  v = fmaxf(v, dpp_f32<kDppXor1>(v));
+  v = fmaxf(v, dpp_f32<kDppXor2>(v));
+  if (lanes >= 8) v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+  if (lanes >= 16) v = fmaxf(v, dpp_f32<kDppMirror>(v));
+  return v;
+}
+
+__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax / 448.f, FLT_MIN) : 1.f; }
+
+// v / s through s's reciprocal and one correction (the quotient's own rounding)
+__device__ __forceinline__ float over(float v, float s, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, s, v), inv, q);
+}
+
+// How a group's values become 8-bit codes.  r scales all of a row, so it cancels in y / scale: the
+// code of z = h gamma is z (448 / max|z|), two roundings where y / scale has six, so that fewer codes
+// fall on the wrong side of a border.  z is used while r and the group's max|z| are of ordinary size
+// (`plain` rows: 2^-40 <= r <= 2^40); other rows hold y itself, and groups past the limits go
+// through y / scale, which makes every code of a group with an infinite y NaN.
+constexpr float kOrdinary = -1.f;  // no reciprocal of a scale is negative; that of an infinite one is 0
+struct Coding {
+  float scale, mul, inv;  // inv != kOrdinary: through y = value * mul, over(y, scale, inv)
+  __device__ __forceinline__ void operator()(float* v) const {
+    if (__ballot(inv != kOrdinary) == 0) {  // the wave's groups are all ordinary
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= mul;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = inv == kOrdinary ? v[e] * mul : over(v[e] * mul, scale, inv);
+  }
+};
+__device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
+  if (plain && amax >= 0x1p-60f && amax <= 0x1p80f) return {amax * r / 448.f, 448.f / amax, kOrdinary};
+  const float back = plain ? r : 1.f, s = scale_of(amax * back);
+  return {s, back, 1.f / s};
 }
 
 // A launch whose own return value is the status (an error left by an earlier call of someone

@@ -1,5 +1,5 @@
-// _marshal: the binding's checks of the home rank's operators' tensors, and the filling of their
-// argument structs.  A decode step's calls take the GPU 3-4 us each and the launch itself takes the
+// _marshal: the binding's checks of the tensors of the home rank's operators and of the experts' products,
+// and the filling of their argument structs.  A decode step's calls take the GPU 3-4 us each and the launch itself takes the
 // host 3.0 us, so what stands between a Python call and the launch counts: the checks of
 // moe_residual_norm's nine tensors and its struct took 4.6 us in Python, where each look at a tensor
 // costs 0.05-0.1 us, and take 0.3 us here (a call of 64 rows 8.4 and 4.1 us).
@@ -25,7 +25,10 @@ namespace {
 
 PyObject* g_error = nullptr;  // MoeError
 
-enum Entry { kRoute, kRouteBack, kSort, kMerge, kMergeBack, kNorm, kNormBack, kEntries };
+enum Entry {
+  kRoute, kRouteBack, kSort, kMerge, kMergeBack, kNorm, kNormBack, kMatmul, kMatmulBack, kSwiglu, kSwigluBack, kQuantize,
+  kEntries
+};
 void* g_entry[kEntries] = {};
 const char* (*g_strerror)(int) = nullptr;
 
@@ -148,6 +151,24 @@ int64_t mat(const char* what, const at::Tensor& t, int64_t rows, int64_t cols, u
   if (t.stride(0) < cols)
     refuse("%s: rows overlap (stride %lld for %lld elements)", what, (long long)t.stride(0), (long long)cols);
   return t.stride(0);
+}
+
+// An [E][rows][cols] tensor of one of `types` whose rows are contiguous: the elements between its rows and
+// between its matrices.
+struct Matrices {
+  int64_t pitch, stride;
+};
+Matrices mats(const char* what, const at::Tensor& t, int64_t E, int64_t rows, int64_t cols, unsigned types) {
+  type(what, t, types);
+  if (t.dim() != 3) refuse("%s: %lld dimensions, 3 expected", what, (long long)t.dim());
+  if (t.size(0) != E || t.size(1) != rows || t.size(2) != cols)
+    refuse("%s: shape (%lld, %lld, %lld), expected (%lld, %lld, %lld)", what, (long long)t.size(0), (long long)t.size(1),
+           (long long)t.size(2), (long long)E, (long long)rows, (long long)cols);
+  if (t.stride(2) != 1 && cols > 1) refuse("%s: the elements of a row must be contiguous", what);
+  const int64_t pitch = rows > 1 ? t.stride(1) : cols, stride = E > 1 ? t.stride(0) : rows * pitch;
+  if (pitch < cols) refuse("%s: rows overlap (stride %lld for %lld elements)", what, (long long)pitch, (long long)cols);
+  if (stride < (rows - 1) * pitch + cols) refuse("%s: matrices overlap (stride %lld)", what, (long long)stride);
+  return {pitch, stride};
 }
 
 // A contiguous tensor of one of `types` with at least n elements; its address.
@@ -414,6 +435,135 @@ PyObject* residual_norm_backward(Call& c) {
   return c.run(kNormBack, &a);
 }
 
+int64_t experts(const at::Tensor& offsets) {
+  if (offsets.dim() != 1 || offsets.numel() < 2)
+    refuse("offsets: one element more than there are experts expected, in one dimension");
+  return offsets.numel() - 1;
+}
+
+PyObject* expert_matmul(Call& c) {
+  const at::Tensor &x = c.tensor("x"), &w = c.tensor("w"), &offsets = c.tensor("offsets"), &out = c.tensor("out");
+  const at::Tensor *err = c.opt("err"), *row_slot = c.opt("row_slot"), *x_scale = c.opt("x_scale"),
+                   *w_scale = c.opt("w_scale");
+  const int transposed = c.truth();
+  const int64_t E = experts(offsets);
+  const Shape s = shape("out", out), in = shape("x", x);
+  moe_expert_matmul_args a{};
+  a.n = i32(s.rows); a.E_loc = i32(E); a.N = i32(s.cols); a.D = i32(in.cols);
+  a.offsets = (const int32_t*)vec("offsets", &offsets, E + 1, I32);
+  if (!row_slot && in.rows != s.rows)
+    refuse("x: %lld rows for %lld of out", (long long)in.rows, (long long)s.rows);
+  if (row_slot && !err) refuse("err: required with row_slot");
+  a.x_pitch = mat("x", x, in.rows, in.cols, F32 | BF16 | FP8);
+  a.x = x.data_ptr();
+  a.x_rows = in.rows;
+  a.dtype = code(x);
+  a.row_slot = (const int32_t*)vec("row_slot", row_slot, s.rows, I32);
+  const Matrices m = mats("w", w, E, transposed ? in.cols : s.cols, transposed ? s.cols : in.cols, same(x));
+  a.w = w.data_ptr();
+  a.w_pitch = m.pitch;
+  a.w_stride = m.stride;
+  a.w_transposed = transposed;
+  if (a.dtype == MOE_FP8_E4M3) {
+    if (!x_scale || !w_scale) refuse("x_scale and w_scale: required for fp8");
+    const int64_t kb = groups(in.cols, 128), nb = groups(s.cols, 128);
+    a.x_scale = (const float*)table("x_scale", x_scale, in.rows, kb, F32);
+    if (w_scale->dim() == 3) mats("w_scale", *w_scale, E, nb, kb, F32);
+    a.w_scale = (const float*)vec("w_scale", w_scale, E * nb * kb, F32);
+  }
+  a.out_pitch = mat("out", out, s.rows, s.cols, F32 | BF16);
+  a.out = out.data_ptr();
+  a.out_dtype = code(out);
+  a.err = (uint32_t*)vec("err", err, 1, I32);
+  return c.run(kMatmul, &a);
+}
+
+PyObject* expert_matmul_backward(Call& c) {
+  const at::Tensor &dout = c.tensor("dout"), &x = c.tensor("x"), &offsets = c.tensor("offsets"), &dw = c.tensor("dw");
+  const int accumulate = c.truth();
+  const int64_t E = experts(offsets);
+  const Shape s = shape("dout", dout), in = shape("x", x);
+  moe_expert_matmul_backward_args a{};
+  a.n = i32(s.rows); a.E_loc = i32(E); a.N = i32(s.cols); a.D = i32(in.cols);
+  a.offsets = (const int32_t*)vec("offsets", &offsets, E + 1, I32);
+  a.dout_pitch = mat("dout", dout, s.rows, s.cols, F32 | BF16);
+  a.dout = dout.data_ptr();
+  a.dtype = code(dout);
+  a.x_pitch = mat("x", x, s.rows, in.cols, same(dout));
+  a.x = x.data_ptr();
+  a.accumulate = accumulate;
+  const Matrices m = mats("dw", dw, E, s.cols, in.cols, F32 | BF16);
+  a.dw = dw.data_ptr();
+  a.dw_dtype = code(dw);
+  a.dw_pitch = m.pitch;
+  a.dw_stride = m.stride;
+  return c.run(kMatmulBack, &a);
+}
+
+PyObject* swiglu(Call& c) {
+  const at::Tensor &gu = c.tensor("gu"), &h = c.tensor("h");
+  const at::Tensor *h_scale = c.opt("h_scale"), *count = c.opt("count");
+  const int64_t group = c.whole();
+  const Shape s = shape("h", h);
+  moe_swiglu_args a{};
+  a.n = i32(s.rows); a.I = i32(s.cols);
+  a.gu_pitch = mat("gu", gu, s.rows, 2 * s.cols, F32 | BF16);
+  a.gu = gu.data_ptr();
+  a.dtype = code(gu);
+  a.count = (const int32_t*)vec("count", count, 1, I32);
+  a.h_pitch = mat("h", h, s.rows, s.cols, F32 | BF16 | FP8);
+  a.h = h.data_ptr();
+  a.h_dtype = code(h);
+  if (a.h_dtype == MOE_FP8_E4M3) {
+    if (!h_scale) refuse("h_scale: required for fp8 output");
+    a.h_scale = (float*)table("h_scale", h_scale, s.rows, groups(s.cols, group), F32);
+    a.group = (int32_t)group;
+  }
+  return c.run(kSwiglu, &a);
+}
+
+PyObject* swiglu_backward(Call& c) {
+  const at::Tensor &gu = c.tensor("gu"), &dh = c.tensor("dh"), &dgu = c.tensor("dgu");
+  const at::Tensor *h = c.opt("h"), *count = c.opt("count");
+  const Shape s = shape("dh", dh);
+  moe_swiglu_backward_args a{};
+  a.n = i32(s.rows); a.I = i32(s.cols);
+  a.gu_pitch = mat("gu", gu, s.rows, 2 * s.cols, F32 | BF16);
+  a.gu = gu.data_ptr();
+  a.dtype = code(gu);
+  a.dh_pitch = mat("dh", dh, s.rows, s.cols, same(gu));
+  a.dh = dh.data_ptr();
+  a.count = (const int32_t*)vec("count", count, 1, I32);
+  a.dgu_pitch = mat("dgu", dgu, s.rows, 2 * s.cols, same(gu));
+  a.dgu = dgu.data_ptr();
+  a.h_pitch = s.cols;
+  if (h) a.h_pitch = mat("h", *h, s.rows, s.cols, same(gu));
+  a.h = address(h);
+  return c.run(kSwigluBack, &a);
+}
+
+PyObject* quantize_weights(Call& c) {
+  const at::Tensor &w = c.tensor("w"), &codes = c.tensor("codes"), &scale = c.tensor("scale");
+  const int transposed = c.truth();
+  if (w.dim() != 3) refuse("w: %lld dimensions, 3 expected", (long long)w.dim());
+  const int64_t E = w.size(0), N = w.size(1), D = w.size(2);
+  moe_quantize_weights_args a{};
+  a.E_loc = i32(E); a.N = i32(N); a.D = i32(D);
+  const Matrices from = mats("w", w, E, N, D, F32 | BF16);
+  const Matrices to = mats("codes", codes, E, transposed ? D : N, transposed ? N : D, FP8);
+  mats("scale", scale, E, groups(transposed ? D : N, 128), groups(transposed ? N : D, 128), F32);
+  a.w = w.data_ptr();
+  a.dtype = code(w);
+  a.w_pitch = from.pitch;
+  a.w_stride = from.stride;
+  a.transposed = transposed;
+  a.codes = codes.data_ptr();
+  a.codes_pitch = to.pitch;
+  a.codes_stride = to.stride;
+  a.scale = (float*)vec("scale", &scale, 1, F32);
+  return c.run(kQuantize, &a);
+}
+
 // No C++ exception leaves a function that Python calls.
 template <PyObject* (*F)(Call&), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -437,7 +587,8 @@ constexpr int kFirstStruct = 5;
 constexpr size_t kStructSize[kEntries] = {
     sizeof(moe_route_args),        sizeof(moe_route_backward_args),      sizeof(moe_sort_rows_args),
     sizeof(moe_merge_rows_args),   sizeof(moe_merge_rows_backward_args), sizeof(moe_residual_norm_args),
-    sizeof(moe_residual_norm_backward_args)};
+    sizeof(moe_residual_norm_backward_args), sizeof(moe_expert_matmul_args),   sizeof(moe_expert_matmul_backward_args),
+    sizeof(moe_swiglu_args),       sizeof(moe_swiglu_backward_args),     sizeof(moe_quantize_weights_args)};
 
 // setup(MoeError, addresses of moe_strerror, moe_version and moe_struct_size, addresses of the entry
 // points in Entry's order); what was set up before stays if it raises
@@ -483,6 +634,11 @@ PyMethodDef g_methods[] = {
     {"moe_merge_rows_backward", FAST((entry<merge_rows_backward, 8>)), nullptr},
     {"moe_residual_norm", FAST((entry<residual_norm, 13>)), nullptr},
     {"moe_residual_norm_backward", FAST((entry<residual_norm_backward, 10>)), nullptr},
+    {"moe_expert_matmul", FAST((entry<expert_matmul, 10>)), nullptr},
+    {"moe_expert_matmul_backward", FAST((entry<expert_matmul_backward, 6>)), nullptr},
+    {"moe_swiglu", FAST((entry<swiglu, 6>)), nullptr},
+    {"moe_swiglu_backward", FAST((entry<swiglu_backward, 6>)), nullptr},
+    {"moe_quantize_weights", FAST((entry<quantize_weights, 5>)), nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods};
 

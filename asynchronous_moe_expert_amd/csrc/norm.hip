@@ -1,7 +1,6 @@
 // moe_residual_norm, moe_residual_norm_backward: h = x + residual, y = h * rsqrt(mean h^2 + eps) *
 // gamma in fp32, bf16 or 8 bits with scales; and its gradient.  A row stays in registers between
 // its reduction and its output, so each input is read once and each output written once.
-#include <float.h>
 #include <math.h>
 
 #include "home.hpp"
@@ -77,47 +76,6 @@ __device__ __forceinline__ float rows_sum(float v, float* s, int sub, int tpr) {
     for (int w = 1; w < waves; ++w) all += s[sub * waves + w];
     return all;
   }
-}
-
-// the maximum over aligned runs of 4, 8 or 16 lanes
-__device__ __forceinline__ float run_max(float v, int lanes) {
-  v = fmaxf(v, dpp_f32<kDppXor1>(v));
-  v = fmaxf(v, dpp_f32<kDppXor2>(v));
-  if (lanes >= 8) v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
-  if (lanes >= 16) v = fmaxf(v, dpp_f32<kDppMirror>(v));
-  return v;
-}
-
-__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax / 448.f, FLT_MIN) : 1.f; }
-
-// v / s through s's reciprocal and one correction (the quotient's own rounding)
-__device__ __forceinline__ float over(float v, float s, float inv) {
-  const float q = v * inv;
-  return fmaf(fmaf(-q, s, v), inv, q);
-}
-
-// How a group's values become 8-bit codes.  r scales all of a row, so it cancels in y / scale: the
-// code of z = h gamma is z (448 / max|z|), two roundings where y / scale has six, so that fewer codes
-// fall on the wrong side of a border.  z is used while r and the group's max|z| are of ordinary size
-// (`plain` rows: 2^-40 <= r <= 2^40); other rows hold y itself, and groups past the limits go
-// through y / scale, which makes every code of a group with an infinite y NaN.
-constexpr float kOrdinary = -1.f;  // no reciprocal of a scale is negative; that of an infinite one is 0
-struct Coding {
-  float scale, mul, inv;  // inv != kOrdinary: through y = value * mul, over(y, scale, inv)
-  __device__ __forceinline__ void operator()(float* v) const {
-    if (__ballot(inv != kOrdinary) == 0) {  // the wave's groups are all ordinary
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= mul;
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = inv == kOrdinary ? v[e] * mul : over(v[e] * mul, scale, inv);
-  }
-};
-__device__ __forceinline__ Coding coding_of(float amax, float r, bool plain) {
-  if (plain && amax >= 0x1p-60f && amax <= 0x1p80f) return {amax * r / 448.f, 448.f / amax, kOrdinary};
-  const float back = plain ? r : 1.f, s = scale_of(amax * back);
-  return {s, back, 1.f / s};
 }
 
 // Bound by memory: 16384 x 4096 bf16 with the residual, 8 bits out, 470 MB in 80 us a call (5.9 TB/s); 8192 x

@@ -266,3 +266,120 @@ class ExpertLayer:
             N.keep_for(stream, x.get_device(), (x, self.row_slot, self.offsets, self.w_gu, self.w_d, self.s_gate,
                                                 self.s_up, self.s_down, self.y, self.workspace))
         N.moe_merge_rows(self.y[:n], self.pos[:n], self.w, out, self.err, stream=stream)
+
+
+class ExpertTrainLayer:
+    """A layer whose experts are all on this rank, with its gradients, over plain row-major weights:
+    moe_route, moe_sort_rows, two products per expert with moe_swiglu between them, moe_merge_rows; and
+    backward() through all of them.  dtype MOE_F32 or MOE_BF16; or MOE_FP8_E4M3, forward only: x in 8 bits with a
+    scale per 128 columns (moe_residual_norm's output for group = 128), weights from moe_quantize_weights, the
+    rows between the products in 8 bits again, out in bf16.
+
+    run() without train gathers its rows from x and keeps nothing for backward(); with train it sorts x into
+    xs, which the gradient of the first product's weights reads.  The weights are read, never kept or packed: an
+    optimizer may change them between a backward() and the next run().  After run() the buffers hold expert and
+    w ([T][K]), pos, counts, offsets, gu, h and y (rows sorted by expert).  They belong to one run at a time, as
+    ExpertLayer's do."""
+
+    def __init__(self, E: int, H: int, I: int, K: int, dtype: int, T_max: int, device="cuda",
+                 score: int = N.MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0, bias_on_score: bool = True):
+        self.E, self.H, self.I, self.K, self.dtype, self.T_max = E, H, I, K, dtype, T_max
+        self.gate = dict(score=score, renorm=renorm, scale=scale)
+        self.how = dict(self.gate, score=score | (N.MOE_BIAS_ON_SCORE if bias_on_score else 0))
+        n = max(T_max * K, 1)
+        if T_max < 0 or n > 1 << 24:
+            raise N.MoeError(f"ExpertTrainLayer: T_max {T_max} with K {K} is over the documented limits")
+        if not 1 <= E <= 256 or not 1 <= K <= min(E, 32):
+            raise N.MoeError(f"ExpertTrainLayer: {K} of {E} experts; 1 to 256 experts fit on one rank, of which 1 to "
+                             "32 are chosen")
+        if dtype not in _TORCH or H % 8 or I % 8 or H < 8 or I < 8 or (dtype == N.MOE_FP8_E4M3 and (H % 16 or I % 16)):
+            raise N.MoeError(f"ExpertTrainLayer: dtype {dtype} with rows of {H} and {I}")
+        self._dev = torch.device(device)
+        self._adt = torch.float32 if dtype == N.MOE_F32 else torch.bfloat16
+        i32 = dict(dtype=torch.int32, device=self._dev)
+        self._expert, self.pos, self.row_slot = (torch.empty(n, **i32) for _ in range(3))
+        self._w = torch.empty(n, dtype=torch.float32, device=self._dev)
+        self.counts, self.offsets, self.err = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.zeros(1, **i32)
+        self.sort_ws = torch.empty(max(N.moe_sort_rows_workspace_size(n), 16), dtype=torch.uint8, device=self._dev)
+        self._n = n
+        self.gu, self.y = self._rows(2 * I), self._rows(H)
+        self.h_scale = None
+        if dtype == N.MOE_FP8_E4M3:
+            self.h = torch.empty((n, I), dtype=torch.uint8, device=self._dev)
+            self.h_scale = torch.empty((n, (I + 127) // 128), dtype=torch.float32, device=self._dev)
+        else:
+            self.h = self._rows(I)
+        self.xs = self._kept = self._back = self.expert = self.w = None
+
+    def _rows(self, columns: int) -> torch.Tensor:
+        return torch.empty((self._n, columns), dtype=self._adt, device=self._dev)
+
+    def run(self, x, logits, w_gu, w_d, out, bias=None, x_scale=None, s_gu=None, s_d=None, train: bool = False,
+            stream=None) -> None:
+        """x [T][H], logits [T][E], w_gu [E][2 I][H] (gate rows, then up rows), w_d [E][H][I]; out [T][H]:
+        sum_j w_j E_j(x).  fp8: x_scale, and s_gu and s_d as moe_quantize_weights gave them."""
+        T, n = x.shape[0], x.shape[0] * self.K
+        fp8 = self.dtype == N.MOE_FP8_E4M3
+        if x.device != self.y.device:
+            raise N.MoeError(f"ExpertTrainLayer: x on {x.device}, the layer on {self.y.device}")
+        if T > self.T_max:
+            raise N.MoeError(f"ExpertTrainLayer: {T} tokens, built for {self.T_max}")
+        if x.shape != (T, self.H) or out.shape != (T, self.H) or logits.shape != (T, self.E):
+            raise N.MoeError(f"ExpertTrainLayer: x {tuple(x.shape)} with logits {tuple(logits.shape)} and out "
+                             f"{tuple(out.shape)}")
+        if w_gu.shape != (self.E, 2 * self.I, self.H) or w_d.shape != (self.E, self.H, self.I):
+            raise N.MoeError(f"ExpertTrainLayer: weights {tuple(w_gu.shape)} and {tuple(w_d.shape)}")
+        for t in (x, w_gu, w_d):
+            if N.dtype_code(t) != self.dtype:
+                raise N.MoeError(f"ExpertTrainLayer: {t.dtype} in a layer of type {self.dtype}")
+        if fp8 and (train or x_scale is None or s_gu is None or s_d is None):
+            raise N.MoeError("ExpertTrainLayer: fp8 takes x_scale, s_gu and s_d, and runs forward only")
+        self._kept = None
+        self.expert, self.w = self._expert[:n].view(T, self.K), self._w[:n].view(T, self.K)
+        xs = None
+        if train:
+            if self.xs is None:
+                self.xs = self._rows(self.H)
+            xs = self.xs[:n]
+        N.moe_route(logits, self.expert, self.w, bias=bias, stream=stream, **self.how)
+        N.moe_sort_rows(self.expert, self.E, x if train else None, xs, None, self.pos, self.counts, self.offsets, self.err,
+                        self.sort_ws, row_slot=self.row_slot, stream=stream)
+        gu, h, y = self.gu[:n], self.h[:n], self.y[:n]
+        if train:
+            N.moe_expert_matmul(xs, w_gu, self.offsets, gu, stream=stream)
+        else:
+            N.moe_expert_matmul(x, w_gu, self.offsets, gu, self.err, row_slot=self.row_slot, x_scale=x_scale, w_scale=s_gu,
+                                stream=stream)
+        scale = self.h_scale[:n] if fp8 else None
+        N.moe_swiglu(gu, h, scale, 128 if fp8 else 0, count=self.offsets[self.E:], stream=stream)
+        N.moe_expert_matmul(h, w_d, self.offsets, y, x_scale=scale, w_scale=s_d, stream=stream)
+        N.moe_merge_rows(y, self.pos[:n], self.w, out, self.err, stream=stream)
+        if train:
+            self._kept = (T, logits, w_gu, w_d)
+
+    def backward(self, dout, dx, dlogits, dw_gu, dw_d, accumulate: bool = False, stream=None) -> None:
+        """The gradients of the last run(train=True) for dout [T][H]: dx [T][H], dlogits [T][E] (of the
+        logits' type; the choice itself and a bias have none), dw_gu and dw_d like the weights (f32, or bf16 in a
+        bf16 layer), added to with accumulate.  logits and the weights are read again."""
+        if self._kept is None:
+            raise N.MoeError("ExpertTrainLayer: backward() comes after run(train=True), once")
+        T, logits, w_gu, w_d = self._kept
+        n = T * self.K
+        if dout.shape != (T, self.H) or dx.shape != (T, self.H) or dlogits.shape != (T, self.E):
+            raise N.MoeError(f"ExpertTrainLayer: dout {tuple(dout.shape)}, dx {tuple(dx.shape)} and dlogits "
+                             f"{tuple(dlogits.shape)} for {T} tokens")
+        if dw_gu.shape != w_gu.shape or dw_d.shape != w_d.shape:
+            raise N.MoeError(f"ExpertTrainLayer: gradients {tuple(dw_gu.shape)} and {tuple(dw_d.shape)}")
+        if self._back is None:
+            self._back = (self._rows(self.H), self._rows(self.I), self._rows(self.H), torch.empty_like(self._w))
+        dy, dh, dxs = (t[:n] for t in self._back[:3])
+        dw, pos, gu, count = self._back[3][:n].view(T, self.K), self.pos[:n], self.gu[:n], self.offsets[self.E:]
+        N.moe_merge_rows_backward(dout, self.y[:n], pos, self.w, dy, dw, self.err, stream=stream)
+        N.moe_expert_matmul_backward(dy, self.h[:n], self.offsets, dw_d, accumulate, stream=stream)
+        N.moe_expert_matmul(dy, w_d, self.offsets, dh, transposed=True, stream=stream)
+        N.moe_swiglu_backward(gu, dh, gu, count=count, stream=stream)  # gu holds its own gradient from here on
+        self._kept = None
+        N.moe_expert_matmul_backward(gu, self.xs[:n], self.offsets, dw_gu, accumulate, stream=stream)
+        N.moe_expert_matmul(gu, w_gu, self.offsets, dxs, transposed=True, stream=stream)
+        N.moe_merge_rows(dxs, pos, None, dx, self.err, stream=stream)
+        N.moe_route_backward(logits, self.expert, dw, dlogits, self.err, stream=stream, **self.gate)

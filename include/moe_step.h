@@ -603,12 +603,147 @@ typedef struct moe_residual_norm_backward_args {
 size_t moe_residual_norm_backward_workspace_size(int32_t H);
 int moe_residual_norm_backward(const moe_residual_norm_backward_args* args, hipStream_t stream);
 
+/* ============================================================== the experts' products ==
+ * The matrix products of a layer's experts over rows sorted by expert, with plain row-major weights
+ * (moe_expert_ffn_grouped keeps its own packed ones and is the faster way to the FFN's forward pass
+ * alone), and what stands between them; for training, and for rows and weights in 8 bits.  The
+ * conventions above hold, those of the home rank's side among them.  Moreover:
+ *   - offsets is read on the device (moe_sort_rows or moe_assemble gives it); expert e has the rows
+ *     offsets[e] .. offsets[e + 1] - 1.  n is an upper bound on offsets[E_loc]: rows from offsets[E_loc] on are
+ *     neither read nor written.  offsets that are not ascending within [0, n] are cut to that range, an
+ *     expert whose end lies before its begin having no rows.
+ *   - N and D (columns of the outputs, of the inputs) are multiples of 8 (D of 16 for fp8 rows) and at most
+ *     65536; every row of a matrix begins at a multiple of 16 bytes.  1 <= E_loc <= 256.
+ *   - A value of an output depends on the row and the weights that its formula names and on nothing else:
+ *     infinities and NaN in other rows, or behind a row's or a matrix's end, do not reach it.
+ */
+
+/* -------------------------------------------------------------- moe_expert_matmul --
+ *   out[r][j] = sum_d w[e][j][d] * x[r'][d]     for the rows r of each expert e
+ * with r' = r, or row_slot[r] with row_slot (moe_sort_rows' or moe_assemble's: the rows are gathered as
+ * they are read).  With w_transposed w is [E_loc][D][N] and out[r][j] = sum_d w[e][d][j] * x[r'][d]: called with
+ * the forward product's weights and the gradient of its out as x, that is the gradient of its rows (of
+ * the gathered ones: add them up by token with moe_merge_rows, w = NULL).
+ * Sums are fp32 and rounded once.  A row_slot outside [0, x_rows) counts as a row of zeros and raises
+ * MOE_ERR_SLOT_RANGE.
+ * Types (x and w, out): (F32, F32), (BF16, BF16), (BF16, F32), (FP8, BF16), (FP8, F32).
+ * FP8: what a code stands for is code * scale, with a scale per row and 128 columns for x, x_scale
+ * [x_rows][ceil(D / 128)] (as moe_residual_norm and moe_swiglu write them for group = 128), and one per 128
+ * x 128 for w, w_scale [E_loc][ceil(N / 128)][ceil(D / 128)] (moe_quantize_weights).  The codes' products over
+ * 128 columns are summed first, then multiplied by the two scales' product.  w_transposed is 0.
+ * Weights: w[e] begins w_stride elements after w[e - 1], its rows are w_pitch apart; an expert's matrix and
+ * all of x are at most 64 GiB. */
+typedef struct moe_expert_matmul_args {
+  int32_t n, E_loc, N, D;
+  const int32_t* offsets;  /* [E_loc + 1] device */
+  const void* x;           /* [x_rows][x_pitch] */
+  int32_t dtype;           /* of x and w: MOE_F32, MOE_BF16 or MOE_FP8_E4M3 */
+  int64_t x_rows;          /* with row_slot: rows of x; without: ignored (n) */
+  int64_t x_pitch;
+  const int32_t* row_slot; /* [n], optional */
+  const float* x_scale;    /* fp8 only */
+  const void* w;           /* [E_loc][N][w_pitch], transposed [E_loc][D][w_pitch] */
+  int32_t w_transposed;    /* 0 or 1 */
+  int64_t w_pitch, w_stride;
+  const float* w_scale;    /* fp8 only */
+  void* out;               /* out [n][out_pitch] */
+  int32_t out_dtype;       /* MOE_F32 or MOE_BF16 */
+  int64_t out_pitch;
+  uint32_t* err;           /* device error word (OR-ed), with row_slot */
+} moe_expert_matmul_args;
+
+int moe_expert_matmul(const moe_expert_matmul_args* args, hipStream_t stream);
+
+/* The gradient of moe_expert_matmul's weights:
+ *   dw[e][j][d] = sum over the rows r of e of dout[r][j] * x[r][d]   (+ dw[e][j][d] with accumulate)
+ * fp32 sums over the rows in ascending order of tiles, rounded once (with accumulate: once, after the
+ * addition).  An expert with no rows gets zeros, or with accumulate keeps what it has.  x holds the rows as
+ * they were multiplied (for gathered ones: moe_sort_rows' xs).
+ * Types (dout and x, dw): (F32, F32), (BF16, BF16), (BF16, F32). */
+typedef struct moe_expert_matmul_backward_args {
+  int32_t n, E_loc, N, D;
+  const int32_t* offsets;  /* [E_loc + 1] device */
+  const void* dout;        /* [n][dout_pitch] */
+  int64_t dout_pitch;
+  const void* x;           /* [n][x_pitch] */
+  int64_t x_pitch;
+  int32_t dtype;           /* of dout and x */
+  int32_t accumulate;      /* 0 or 1 */
+  void* dw;                /* out [E_loc][N][dw_pitch] */
+  int32_t dw_dtype;
+  int64_t dw_pitch, dw_stride;
+} moe_expert_matmul_backward_args;
+
+int moe_expert_matmul_backward(const moe_expert_matmul_backward_args* args, hipStream_t stream);
+
+/* --------------------------------------------------------------------- moe_swiglu --
+ *   h[r][i] = silu(gu[r][i]) * gu[r][I + i],  silu(z) = z / (1 + exp(-z))
+ * for the rows r < min(n, *count) (count NULL: all n; offsets + E_loc counts the rows that moe_sort_rows
+ * placed); other rows of h and h_scale are left as they were.  h_dtype MOE_FP8_E4M3: h_scale and the codes
+ * as moe_residual_norm's out_scale and codes for y = h: one scale per `group` columns (32, 64 or 128), or per
+ * row for group = 0; a NaN has a NaN code and no part in the maximum, a group with an infinite h has NaN
+ * codes throughout.  silu(-inf) is NaN.
+ * Types: gu F32 or BF16; h F32, BF16 or FP8.  I is a multiple of 8 and at most 32768. */
+typedef struct moe_swiglu_args {
+  int32_t n, I;
+  const void* gu;          /* [n][gu_pitch]: I gate columns, then I up columns */
+  int32_t dtype;
+  int64_t gu_pitch;
+  const int32_t* count;    /* device, optional */
+  void* h;                 /* out [n][h_pitch] */
+  int32_t h_dtype;
+  int64_t h_pitch;
+  float* h_scale;          /* out, fp8 only: [n][ceil(I / group)], or [n] for group = 0 */
+  int32_t group;           /* fp8 only: 0, 32, 64 or 128 */
+} moe_swiglu_args;
+
+int moe_swiglu(const moe_swiglu_args* args, hipStream_t stream);
+
+/* The gradient of moe_swiglu, with s = 1 / (1 + exp(-g)):
+ *   dgu[r][i] = dh u s (1 + g (1 - s)),  dgu[r][I + i] = dh g s,  h[r][i] = g s u again (optional)
+ * for the same rows.  dgu may be gu itself (same pitch).  All of one type, F32 or BF16. */
+typedef struct moe_swiglu_backward_args {
+  int32_t n, I;
+  const void* gu;          /* [n][gu_pitch] */
+  int32_t dtype;           /* of every array */
+  int64_t gu_pitch;
+  const void* dh;          /* [n][dh_pitch] */
+  int64_t dh_pitch;
+  const int32_t* count;    /* device, optional */
+  void* dgu;               /* out [n][dgu_pitch] */
+  int64_t dgu_pitch;
+  void* h;                 /* out [n][h_pitch], optional */
+  int64_t h_pitch;
+} moe_swiglu_backward_args;
+
+int moe_swiglu_backward(const moe_swiglu_backward_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------------ moe_quantize_weights --
+ * Weights in 8 bits for moe_expert_matmul: over each 128 x 128 block (those at the ends may be smaller)
+ *   scale = max|w| / 448, at least the smallest normal fp32 (1 where all are 0),  code = w / scale
+ * to nearest even; NaN and infinities as in moe_swiglu.  With transposed the codes are those of w[e]'s
+ * transpose, codes [E_loc][D][codes_pitch] and scale [E_loc][ceil(D / 128)][ceil(N / 128)]: the weights of the product
+ * in the other direction.  Types: w F32 or BF16. */
+typedef struct moe_quantize_weights_args {
+  int32_t E_loc, N, D;
+  const void* w;           /* [E_loc][N][w_pitch] */
+  int32_t dtype;
+  int64_t w_pitch, w_stride;
+  int32_t transposed;      /* 0 or 1 */
+  void* codes;             /* out [E_loc][N][codes_pitch], transposed [E_loc][D][codes_pitch] */
+  int64_t codes_pitch, codes_stride;
+  float* scale;            /* out [E_loc][ceil(N / 128)][ceil(D / 128)], transposed the other way round */
+} moe_quantize_weights_args;
+
+int moe_quantize_weights(const moe_quantize_weights_args* args, hipStream_t stream);
+
 /* ---------------------------------------------------------------------- helpers -- */
 const char* moe_strerror(int status);
 int moe_version(void);
 /* sizeof of the argument structs as compiled into the library (which: 0 assemble,
  * 1 pack, 2 ffn, 3 combine state, 4 combine args, 5 route, 6 route backward, 7 sort rows,
- * 8 merge rows, 9 merge rows backward, 10 residual norm, 11 residual norm backward), so that
+ * 8 merge rows, 9 merge rows backward, 10 residual norm, 11 residual norm backward, 12 expert
+ * matmul, 13 expert matmul backward, 14 swiglu, 15 swiglu backward, 16 quantize weights), so that
  * bindings can check their own struct layout; 0 for an unknown id. */
 size_t moe_struct_size(int which);
 
