@@ -1,38 +1,8 @@
 // moe_expert_matmul, moe_expert_matmul_backward: the products of each expert's rows with its row-major
 // weights, in either direction, and the weights' gradient.
-//
-// Every kernel computes tiles of a matrix  C[p][q] = sum_k P[p][k] Q[q][k].  The matrix instruction's
-// second operand is P and its first is Q, so that a lane ends up with four neighbouring q of one p, that
-// is, with neighbouring elements of an output row:
-//   forward        p = batch row,      q = output column, k = d    P rows along k,   Q = w[e]'s rows along k
-//   rows' gradient p = batch row,      q = input column,  k = j    P rows along k,   Q = w[e]'s rows across k
-//   weights'       p = output column,  q = input column,  k = row  both across k; k runs over an expert's rows
-#include "home.hpp"
+#include "products.hpp"
 
 namespace moe {
-
-enum { kForward = 0, kRowsGrad = 1, kWeightsGrad = 2 };
-
-struct ProductJob {
-  int n, E, N, D;            // N: columns of C (forward: w's rows), D: the contraction; weights' gradient: C is N x D
-  const int32_t* offsets;
-  const void *x, *w, *dout;
-  int64_t x_rows, x_pitch, w_pitch, w_stride, dout_pitch, out_pitch, out_stride;
-  const int32_t* row_slot;
-  const float *x_scale, *w_scale;
-  void* out;
-  int out_f32, accumulate;
-  uint32_t* err;
-};
-
-template <int DT>
-constexpr int esize() { return DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1; }
-
-// offsets cut to an ascending range within [0, n]
-__device__ __forceinline__ void expert_rows(const ProductJob& j, int e, int& r0, int& r1) {
-  r0 = min(max(j.offsets[e], 0), j.n);
-  r1 = max(r0, min(j.offsets[e + 1], j.n));
-}
 
 // ------------------------------------------------------------------------------------ any type, any size
 // 64 x 64 tiles in fp32: elements are widened (8-bit ones scaled) into LDS rows of 32 k, 36 apart so that
@@ -165,31 +135,18 @@ __global__ __launch_bounds__(256) void product_kernel(ProductJob j) {
       const int q = q0 + wq + b * 16 + (lane >> 4) * 4;
       if (q >= Q) continue;
       const int64_t at = (MODE == kWeightsGrad ? e * j.out_stride : 0) + p * j.out_pitch + q;
-      f32x4 v = acc[a][b];
-      if (j.out_f32) {
-        f32x4* o = reinterpret_cast<f32x4*>((float*)j.out + at);
-        if (j.accumulate) v += *o;
-        *o = v;
-      } else {
-        u32x2* o = reinterpret_cast<u32x2*>((uint16_t*)j.out + at);
-        if (j.accumulate) {
-          const u32x2 old = *o;
-          v[0] += __uint_as_float(old[0] << 16);
-          v[1] += __uint_as_float(old[0] & 0xffff0000u);
-          v[2] += __uint_as_float(old[1] << 16);
-          v[3] += __uint_as_float(old[1] & 0xffff0000u);
-        }
-        *o = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-      }
+      put4(j, at, acc[a][b]);
     }
   }
 }
 
 // ------------------------------------------------------------------------------------ checks and dispatch
 constexpr int64_t kReach = (int64_t)1 << 36;  // bytes of x, or of an expert's matrix
+constexpr int64_t kPitch = (int64_t)1 << 24;  // bytes between its rows
 
 template <int DT, int MODE>
 static int run_product(const ProductJob& j, hipStream_t stream) {
+  if (DT != MOE_F32) return run_tiles(j, DT, MODE, stream);
   const int64_t ct = ((MODE == kWeightsGrad ? j.D : j.N) + kS - 1) / kS;
   const int64_t rt = MODE == kWeightsGrad ? (int64_t)j.E * ((j.N + kS - 1) / kS) : j.n / kS + (j.n < j.E ? j.n : j.E);
   if (rt * ct > (1 << 24) - 1) return MOE_EINVAL_SIZE;
@@ -198,7 +155,7 @@ static int run_product(const ProductJob& j, hipStream_t stream) {
 
 // a matrix of `rows` rows of `cols` elements, one of several `stride` apart
 static int matrix_status(const void* p, int64_t rows, int64_t cols, int64_t pitch, int64_t stride, int many, int es) {
-  if (pitch < cols || pitch > kReach || rows * pitch * es > kReach) return MOE_EINVAL_SIZE;
+  if (pitch < cols || pitch * es > kPitch || rows * pitch * es > kReach) return MOE_EINVAL_SIZE;
   if (many > 1 && (stride < (rows - 1) * pitch + cols || stride > kReach)) return MOE_EINVAL_SIZE;
   if (!aligned_rows(p, pitch, es, 16) || (many > 1 && (stride * es) % 16)) return MOE_EINVAL_ALIGN;
   return MOE_OK;

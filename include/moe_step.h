@@ -613,7 +613,8 @@ int moe_residual_norm_backward(const moe_residual_norm_backward_args* args, hipS
  *     neither read nor written.  offsets that are not ascending within [0, n] are cut to that range, an
  *     expert whose end lies before its begin having no rows.
  *   - N and D (columns of the outputs, of the inputs) are multiples of 8 (D of 16 for fp8 rows) and at most
- *     65536; every row of a matrix begins at a multiple of 16 bytes.  1 <= E_loc <= 256.
+ *     65536; every row of a matrix begins at a multiple of 16 bytes, at most 16 MiB after the one before.
+ *     1 <= E_loc <= 256.
  *   - A value of an output depends on the row and the weights that its formula names and on nothing else:
  *     infinities and NaN in other rows, or behind a row's or a matrix's end, do not reach it.
  */
