@@ -51,8 +51,8 @@ struct Place {
 // How an operand lies in LDS and how a step of it is copied there.  A stage holds 256 p and 256 q by 64 k (128
 // codes); a wave's copy instruction fills 1 KiB, eight runs of 128 bytes, each from one row of memory.
 //   along k:  row r is 128 bytes, its 16-byte piece c at place c ^ key(r): key = bits 1..3 of r for P and bits 1,
-//             4, 5 for Q.  Lane l reads piece l / 16 (+ 4) of P's row l % 16, of Q's row 16 (l % 16 / 4) + l % 4 (+ 4
-//             for the next 16 of the matrix instruction's rows, so that a lane ends up with 16 neighbouring
+//             3, 4 for Q.  Lane l reads piece l / 16 (+ 4) of P's row l % 16, of Q's row 8 (l % 16 / 4) + l % 4 (+ 4
+//             for the next 16 of the matrix instruction's rows, so that a lane ends up with eight neighbouring
 //             columns of C): sixteen rows' pieces lie in the sixteen places of the 256 bytes that LDS gives a cycle.
 //   across k: blocks of 64 columns; in a block row k is 128 bytes, its 32-byte part c at place c ^ f(k), f(k) =
 //             bits 1 and 3 of k.  ds_read_b64_tr_b16 gives lane l of a group of 16 column l of four rows, 8 g to 8 g
@@ -63,43 +63,43 @@ struct Tile {
   static constexpr int es = esize<DT>();
   static constexpr bool kPAlong = MODE != kWeightsGrad, kQAlong = MODE == kForward;
   static constexpr bool kScaled = DT == MOE_FP8_E4M3;
-  static constexpr int kP = MT / 2, kQ = 4;                    // copies of a wave in a step
-  static constexpr int kPCopies = kP + (kScaled ? 1 : 0);      // a scale for each row besides
   static constexpr int kHalf = MT / 2;
+  // copies that a wave of group 0 makes in a step: of each group's rows of P, of Q, and of the rows' scales
+  static constexpr int kP = MT / 2, kQ = 8, kScales = kScaled ? 1 : 0;
+  static constexpr int kFirst = kQ + kP + kScales, kSecond = kP;
 };
-
 __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   const uint64_t v = (uint64_t)p;
   return (const char*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
                        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32);
 }
 
-// A block of columns of an operand whose rows lie across k: byte offsets of this lane's copies from row k0 of the
-// matrix, and the row that it copies (32 more for odd copies).  Columns past the end are read at the last ones.
+// NB blocks of 64 columns of an operand whose rows lie across k: byte offsets of this lane's copies from row k0 of
+// the matrix, two copies to a block, of row() and of the row 32 further.  Columns past the end are read at others.
+template <int NB>
 struct Across {
-  uint32_t off[2];
+  uint32_t off[NB];
   __device__ __forceinline__ void set(int wq, int lane, int col0, int cols, int64_t pitch, int es) {
     const int k = row(wq, lane), f = ((k >> 1) & 1) | ((k >> 3) & 1) << 1, piece = (lane & 7) ^ (2 * f);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
       const int first = col0 + 64 * b < cols ? col0 + 64 * b : col0 < cols ? col0 : 0;
       off[b] = (uint32_t)(k * (int)pitch * es + (first + min(piece * 8, cols - 8 - first)) * es);
     }
   }
   static __device__ __forceinline__ int row(int wq, int lane) { return 8 * wq + (lane >> 3); }
-  // copies N (4 or 2) KiB of step `step` of the contraction's rows 0 .. end - 1, which begin at base
-  template <int N>
+  // step `step` of the contraction's rows 0 .. end - 1, which begin at base
   __device__ __forceinline__ void copy(const char* base, int64_t pitch_bytes, uint32_t dst, int step, int end, int wq,
                                        int lane) const {
     const char* from = uniform_ptr(base + (int64_t)step * kStep * pitch_bytes);
     const char* odd = uniform_ptr(from + 32 * pitch_bytes);
     if ((step + 1) * kStep <= end) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) copy16(c & 1 ? odd : from, off[c >> 1], dst + c * 4096);
+      for (int c = 0; c < 2 * NB; ++c) copy16(c & 1 ? odd : from, off[c >> 1], dst + c * 4096);
     } else {
       const int k = step * kStep + row(wq, lane);
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
+      for (int c = 0; c < 2 * NB; ++c) {
         const char* src = (c & 1 ? odd : from) + off[c >> 1];
         copy16(k + 32 * (c & 1) < end ? src : (const char*)&g_zeros, dst + c * 4096);
       }
@@ -107,112 +107,158 @@ struct Across {
   }
 };
 
+// Lane groups g hold columns 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3 of a row, two values to a register; after it
+// they hold columns 8 g .. 8 g + 7, 16 bytes that can be stored at once.
+__device__ __forceinline__ void neighbours(u32x4& v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto h = __builtin_amdgcn_permlane32_swap(v[i], v[2 + i], false, false);
+    const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+    v[i] = r[0];
+    v[2 + i] = r[1];
+  }
+}
+
+// What a workgroup has in LDS: two stages of P (16 KiB for each group's rows) and of Q, four of the rows' scales.
+struct Lds {
+  u32x4 *p[2], *q[2];
+  float *scale, *w_scale;
+};
+constexpr int kMaxBlocks = kHMaxRows / 128;  // scales of a row
+
+// The base and pitch of an operand's rows.
+template <int MODE, int DT>
+__device__ __forceinline__ const char* p_base(const ProductJob& j, const Place& at) {
+  return MODE == kWeightsGrad ? (const char*)j.dout + at.k0 * j.dout_pitch * esize<DT>() : (const char*)j.x;
+}
+template <int MODE, int DT>
+__device__ __forceinline__ int64_t q_pitch(const ProductJob& j) {
+  return (MODE == kWeightsGrad ? j.x_pitch : j.w_pitch) * esize<DT>();
+}
+template <int MODE, int DT>
+__device__ __forceinline__ const char* q_base(const ProductJob& j, const Place& at) {
+  if constexpr (MODE == kWeightsGrad) return (const char*)j.x + at.k0 * j.x_pitch * esize<DT>();
+  else return (const char*)j.w + (at.e * j.w_stride + (MODE == kForward ? at.q0 * j.w_pitch : 0)) * esize<DT>();
+}
+
+// The row of the tile's P that lies at place r of group h's 16 MT, and where it comes from (-1: nowhere).
+template <int MT>
+__device__ __forceinline__ int64_t p_source(const ProductJob& j, const Place& at, int h, int r) {
+  const int row = min(at.p0 + h * 16 * MT + min(r, 16 * MT - 1), at.pend - 1);
+  if (!j.row_slot) return row;
+  const int64_t slot = j.row_slot[row];
+  return slot < 0 || slot >= j.x_rows ? -1 : slot;
+}
+
+// The copies of a tile's operands, all made by the four waves wq of group 0.
+template <int MODE, int DT, int MT>
+struct Copies {
+  using T = Tile<MODE, DT, MT>;
+  static constexpr int es = T::es;
+  uint32_t poff[2][T::kPAlong ? T::kP : 1];  // along k: in units of 16 bytes from x
+  uint32_t nosrc = 0;                        // copies of P whose row has no source, bit 31: the scale
+  bool sourced = true;
+  const float* sptr = nullptr;
+  Across<T::kPAlong ? 1 : T::kP / 2> pa[2];
+  uint32_t qoff = 0;
+  Across<4> qa;
+  int pieces;  // of a row along k
+  int steps;
+
+  static __device__ __forceinline__ int ppiece(int wq, int lane) { return (lane & 7) ^ (4 * (wq & 1) + (lane >> 4)); }
+  static __device__ __forceinline__ int qpiece(int wq, int lane) { return (lane & 7) ^ (((lane >> 4) & 1) | 2 * wq); }
+
+  __device__ __forceinline__ void set(const ProductJob& j, const Place& at, int steps_, int wq, int lane) {
+    pieces = j.D * es / 16;
+    steps = steps_;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (T::kPAlong) {
+#pragma unroll
+        for (int c = 0; c < T::kP; ++c) {
+          int64_t slot = p_source<MT>(j, at, h, 8 * (4 * c + wq) + (lane >> 3));
+          if (slot < 0) {
+            atomicOr(j.err, MOE_ERR_SLOT_RANGE);
+            slot = 0;
+            nosrc |= 1u << (h * T::kP + c);
+          }
+          poff[h][c] = (uint32_t)(slot * (j.x_pitch * es / 16) + ppiece(wq, lane));
+        }
+      } else {
+        pa[h].set(wq, lane, at.p0 + h * 16 * MT, j.N, j.dout_pitch, es);
+      }
+    }
+    if constexpr (T::kScaled) {
+      const int64_t slot = p_source<MT>(j, at, wq >> 1, (wq & 1) * 64 + lane);
+      if (slot < 0) nosrc |= 1u << 31;
+      else sptr = j.x_scale + slot * ((j.D + 127) / 128);
+    }
+    sourced = __ballot(nosrc != 0) == 0;
+    if constexpr (T::kQAlong) qoff = (uint32_t)((lane >> 3) * (int)j.w_pitch * es + qpiece(wq, lane) * 16);
+    else qa.set(wq, lane, at.q0, MODE == kWeightsGrad ? j.D : j.N, MODE == kWeightsGrad ? j.x_pitch : j.w_pitch, es);
+  }
+  __device__ __forceinline__ void p_half(const ProductJob& j, const Place& at, int h, const u32x4* stage, int step, int wq,
+                                         int lane) const {
+    const uint32_t dst = lds_at(stage) + h * 16384 + wq * 1024;
+    if constexpr (T::kPAlong) {
+      const char* from = uniform_ptr(p_base<MODE, DT>(j, at) + (int64_t)step * 128);
+      if (sourced && (step + 1) * 8 <= pieces) {
+#pragma unroll
+        for (int c = 0; c < T::kP; ++c) copy16(from + (uint64_t)poff[h][c] * 16, dst + c * 4096);
+      } else {
+#pragma unroll
+        for (int c = 0; c < T::kP; ++c)
+          copy16(step * 8 + ppiece(wq, lane) < pieces && !(nosrc >> (h * T::kP + c) & 1) ? from + (uint64_t)poff[h][c] * 16
+                                                                                        : (const char*)&g_zeros,
+                 dst + c * 4096);
+      }
+    } else {
+      pa[h].copy(p_base<MODE, DT>(j, at), j.dout_pitch * es, dst, step, at.kend - at.k0, wq, lane);
+    }
+  }
+  // Q, group 0's rows of P, and all rows' scales
+  __device__ __forceinline__ void first(const ProductJob& j, const Place& at, const Lds& lds, int step, int wq,
+                                        int lane) const {
+    const int Qn = MODE == kWeightsGrad ? j.D : j.N;
+    const uint32_t dst = lds_at(lds.q[step & 1]) + wq * 1024;
+    const char* q = q_base<MODE, DT>(j, at);
+    if constexpr (T::kQAlong) {  // N is a multiple of 8, so rows are past it by whole copies: read at the first ones
+      const bool whole = (step + 1) * 8 <= pieces;
+#pragma unroll
+      for (int c = 0; c < T::kQ; ++c) {
+        const int r = 8 * (4 * c + wq);
+        const char* from = uniform_ptr(q + (int64_t)step * 128 + (at.q0 + r < Qn ? r : 0) * j.w_pitch * es);
+        if (whole) copy16(from, qoff, dst + c * 4096);
+        else copy16(step * 8 + qpiece(wq, lane) < pieces ? from + qoff : (const char*)&g_zeros, dst + c * 4096);
+      }
+    } else {
+      qa.copy(q, q_pitch<MODE, DT>(j), dst, step, at.kend - at.k0, wq, lane);
+    }
+    p_half(j, at, 0, lds.p[step & 1], step, wq, lane);
+    if constexpr (T::kScaled) {
+      const char* src = !(nosrc >> 31) ? (const char*)(sptr + step) : (const char*)&g_zeros;
+      copy4(src, lds_at(lds.scale) + (step & 3) * 1024 + wq * 256);
+    }
+  }
+  __device__ __forceinline__ void second(const ProductJob& j, const Place& at, const Lds& lds, int step, int wq,
+                                         int lane) const {
+    p_half(j, at, 1, lds.p[step & 1], step, wq, lane);
+  }
+};
+
 template <int MODE, int DT, int MT, int G>
-__device__ __forceinline__ void tile(const ProductJob& j, const Place& at, u32x4* p0s, u32x4* p1s, u32x4* q0s, u32x4* q1s,
-                                     float* s0s, float* s1s, int wq, int lane) {
+__device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const Lds& lds, int wq, int lane) {
   using T = Tile<MODE, DT, MT>;
   constexpr int es = T::es, kHalf = T::kHalf;
   const int g = lane >> 4, l16 = lane & 15;
   const int steps = MODE == kWeightsGrad ? (at.kend - at.k0 + kStep - 1) / kStep : (j.D * es + 127) / 128;
   const int Qn = MODE == kWeightsGrad ? j.D : j.N;
-  const int pieces = j.D * es / 16;  // of a row along k
-
-  // ---- copies of P: this group's 16 MT of the tile's rows, a quarter by each wave
-  uint32_t poff[T::kPAlong ? T::kP : 1];  // along: in units of 16 bytes from x
-  bool sourced = true;                    // along: every row of this wave's copies has a source
-  uint32_t nosrc = 0;                     // the copies whose row has none
-  const float* sptr = nullptr;
-  Across pa;
-  const int ppiece = (lane & 7) ^ (4 * (wq & 1) + (lane >> 4));
-  if constexpr (T::kPAlong) {
-#pragma unroll
-    for (int c = 0; c < T::kP; ++c) {
-      const int row = min(at.p0 + G * 16 * MT + 8 * (4 * c + wq) + (lane >> 3), at.pend - 1);
-      int64_t slot = row;
-      if (j.row_slot) {
-        slot = j.row_slot[row];
-        if (slot < 0 || slot >= j.x_rows) {
-          atomicOr(j.err, MOE_ERR_SLOT_RANGE);
-          slot = 0;
-          nosrc |= 1u << c;
-        }
-      }
-      poff[c] = (uint32_t)(slot * (j.x_pitch * es / 16) + ppiece);
-    }
-    if constexpr (T::kScaled) {
-      const int row = min(at.p0 + G * 16 * MT + min((wq & 1) * 64 + lane, 16 * MT - 1), at.pend - 1);
-      const int64_t slot = j.row_slot ? j.row_slot[row] : row;
-      const int kb = (j.D + 127) / 128;
-      if (slot < 0 || slot >= j.x_rows) nosrc |= 1u << 31;
-      else sptr = j.x_scale + slot * kb;
-    }
-    sourced = __ballot(nosrc != 0) == 0;
-  } else {
-    pa.set(wq, lane, at.p0 + G * 16 * MT, j.N, j.dout_pitch, es);
-  }
-  auto copy_p = [&](u32x4* stage, float* scales, int step) {
-    const uint32_t dst = lds_at(stage) + wq * 1024;
-    if constexpr (T::kPAlong) {
-      const char* from = uniform_ptr((const char*)j.x + (int64_t)step * 128);
-      if (sourced && (step + 1) * 8 <= pieces) {
-#pragma unroll
-        for (int c = 0; c < T::kP; ++c) copy16(from + (uint64_t)poff[c] * 16, dst + c * 4096);
-      } else {
-#pragma unroll
-        for (int c = 0; c < T::kP; ++c)
-          copy16(step * 8 + ppiece < pieces && !(nosrc >> c & 1) ? from + (uint64_t)poff[c] * 16 : (const char*)&g_zeros,
-                 dst + c * 4096);
-      }
-    } else {
-      pa.template copy<T::kP>((const char*)j.dout + at.k0 * j.dout_pitch * es, j.dout_pitch * es, dst, step,
-                              at.kend - at.k0, wq, lane);
-    }
-    if constexpr (T::kScaled) {
-      const char* src = !(nosrc >> 31) && step < steps ? (const char*)(sptr + step) : (const char*)&g_zeros;
-      copy4(src, lds_at(scales) + (wq & 1) * 256);
-    }
-  };
-
-  // ---- copies of Q: an eighth of the tile's columns by each wave.  Columns past the end are read at others:
-  // N is a multiple of 8, so rows along k are past it by whole copies.
-  uint32_t qoff[2];
-  Across qa;
-  if constexpr (T::kQAlong) {
-    const int piece = (lane & 7) ^ (((lane >> 4) & 1) | (wq & 2));  // ^ 4 in odd copies
-    const uint32_t row = (uint32_t)((lane >> 3) * (int)j.w_pitch * es);
-    qoff[0] = row + piece * 16;
-    qoff[1] = row + (piece ^ 4) * 16;
-  } else {
-    qa.set(wq, lane, at.q0 + 128 * G, Qn, MODE == kWeightsGrad ? j.x_pitch : j.w_pitch, es);
-  }
-  auto copy_q = [&](u32x4* stage, int step) {
-    const uint32_t dst = lds_at(stage) + (wq + 16 * G) * 1024;
-    if constexpr (T::kQAlong) {
-      const char* w = (const char*)j.w + (at.e * j.w_stride + (int64_t)at.q0 * j.w_pitch) * es + (int64_t)step * 128;
-      const bool whole = (step + 1) * 8 <= pieces;
-#pragma unroll
-      for (int c = 0; c < T::kQ; ++c) {
-        const int r = 8 * (4 * c + wq + 16 * G);
-        const char* from = uniform_ptr(w + (at.q0 + r < Qn ? r : 0) * j.w_pitch * es);
-        if (whole) {
-          copy16(from, qoff[c & 1], dst + c * 4096);
-        } else {
-          const int piece = (lane & 7) ^ (((lane >> 4) & 1) | (wq & 2)) ^ 4 * (c & 1);
-          copy16(step * 8 + piece < pieces ? from + qoff[c & 1] : (const char*)&g_zeros, dst + c * 4096);
-        }
-      }
-    } else if constexpr (MODE == kWeightsGrad) {
-      qa.template copy<T::kQ>((const char*)j.x + at.k0 * j.x_pitch * es, j.x_pitch * es, dst, step, at.kend - at.k0, wq, lane);
-    } else {
-      qa.template copy<T::kQ>((const char*)j.w + at.e * j.w_stride * es, j.w_pitch * es, dst, step, j.D, wq, lane);
-    }
-  };
 
   // ---- where this lane's fragments lie, in bytes
   int pr, qr, tr;
   if constexpr (T::kPAlong) pr = l16 * 128 + ((g ^ ((l16 >> 1) & 7)) << 4);
   if constexpr (T::kQAlong)
-    qr = wq * 8192 + (16 * (l16 >> 2) + (l16 & 3)) * 128 + ((g ^ (((l16 >> 1) & 1) | ((l16 >> 1) & 6))) << 4);
+    qr = wq * 8192 + (8 * (l16 >> 2) + (l16 & 3)) * 128 + ((g ^ (((l16 >> 1) & 1) | ((l16 >> 1) & 6))) << 4);
   if constexpr (!T::kPAlong || !T::kQAlong)
     tr = (8 * g + (l16 >> 2)) * 128 + ((((l16 >> 3) & 1) | (g & 1) << 1) << 5) + (l16 & 3) * 8;
   // the second slice's piece is 4 further, the next 16 columns' part c further: both by exclusive or, which the
@@ -245,19 +291,16 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, u32x4
       pf[a][0] = along(ps, at0 + (a0 + a) * 2048);
       pf[a][1] = along(ps, at1 + (a0 + a) * 2048);
     }
-    if constexpr (T::kScaled) sc[a] = ss[(a0 + a) * 16 + l16];
+    if constexpr (T::kScaled) sc[a] = ss[G * 128 + (a0 + a) * 16 + l16];
   };
   auto read = [&](const u32x4* ps, const u32x4* qs, const float* ss, int step) {
-    if constexpr (T::kScaled) {
-      const int nb = (j.N + 127) / 128, kb = (j.D + 127) / 128;
-      sw = j.w_scale[((int64_t)at.e * nb + min((at.q0 + 64 * wq) >> 7, nb - 1)) * kb + step];
-    }
+    if constexpr (T::kScaled) sw = lds.w_scale[(wq >> 1) * kMaxBlocks + step];
     if constexpr (T::kQAlong) {
       const int q1 = flip(qr, 64);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        qf[b][0] = along(qs, qr + b * 512);
-        qf[b][1] = along(qs, q1 + b * 512);
+        qf[b][0] = along(qs, qr + (b & 1) * 512 + (b >> 1) * 4096);
+        qf[b][1] = along(qs, q1 + (b & 1) * 512 + (b >> 1) * 4096);
       }
     } else {
       const int tq = wq * 8192 + tr;
@@ -342,58 +385,62 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, u32x4
     __builtin_amdgcn_s_setprio(0);
   };
 
+  if constexpr (T::kScaled) {  // the scales of the tile's two blocks of columns
+    const int nb = (j.N + 127) / 128;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float* from = j.w_scale + ((int64_t)at.e * nb + min((at.q0 >> 7) + b, nb - 1)) * steps;
+      for (int k = G * 256 + wq * 64 + lane; k < steps; k += 512) lds.w_scale[b * kMaxBlocks + k] = from[k];
+    }
+    wait_lds();
+  }
+
   // ---- The waves of a SIMD, one of each group, take turns: while one multiplies a step's fragments, which it
   // holds in registers, the other reads its next ones (Q's and half of P's; the other half takes the place of
   // what has been multiplied).  Group 0 reads step i in phase 2 i and multiplies in phase 2 i + 1, group 1 one
-  // phase later; a barrier ends each phase.  So Q's part of a stage is free after phase 2 i + 1, the groups' parts
-  // of P after 2 i + 1 and 2 i + 2, and the copies of step i + 2 that go out then have two phases to land.  Steps
-  // past the end copy zeros, so that the counts that the waits go by are the same in every step.
-  u32x4* ps[2] = {p0s, p1s};
-  u32x4* qs[2] = {q0s, q1s};
-  float* ss[2] = {s0s, s1s};
+  // phase later; a barrier ends each phase.  So of a stage, Q and group 0's rows of P are free after phase 2 i + 1,
+  // group 1's after 2 i + 2: group 0 copies step i + 2 there in the phase after, two phases before it is read.
   if constexpr (G == 0) {
-    copy_p(ps[0], ss[0], 0);
-    copy_q(qs[0], 0);
-    wait_copies<0>();
+    Copies<MODE, DT, MT> c;
+    c.set(j, at, steps, wq, lane);
+    c.first(j, at, lds, 0, wq, lane);
+    c.second(j, at, lds, 0, wq, lane);
+    wait_copies<T::kSecond>();
     meet();
 #pragma clang loop unroll(disable)
     for (int i = 0; i < steps; i += 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (i + h >= steps) break;
-        copy_q(qs[h ^ 1], i + h + 1);
-        copy_p(ps[h ^ 1], ss[h ^ 1], i + h + 1);
-        read(ps[h], qs[h], ss[h], i + h);
+        const u32x4* ps = lds.p[h];
+        const float* ss = lds.scale + ((i + h) & 3) * 256;
+        if (i + h + 1 < steps) c.first(j, at, lds, i + h + 1, wq, lane);
+        read(ps, lds.q[h], ss, i + h);
         wait_lds();
+        if (i + h + 1 < steps) wait_copies<T::kFirst>();
+        else wait_copies<0>();
         meet();
-        multiply(ps[h], ss[h]);
-        wait_copies<0>();
+        if (i + h + 1 < steps) c.second(j, at, lds, i + h + 1, wq, lane);
+        multiply(ps, ss);
+        wait_copies<T::kSecond>();
         meet();
       }
     }
     meet();
   } else {
-    copy_q(qs[0], 0);
-    copy_p(ps[0], ss[0], 0);
-    wait_copies<T::kPCopies>();
     meet();
-    copy_q(qs[1], 1);
-    wait_copies<T::kQ>();
     meet();
 #pragma clang loop unroll(disable)
     for (int i = 0; i < steps; i += 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (i + h >= steps) break;
-        copy_p(ps[h ^ 1], ss[h ^ 1], i + h + 1);
-        read(ps[h], qs[h], ss[h], i + h);
+        const u32x4* ps = lds.p[h] + 1024;
+        const float* ss = lds.scale + ((i + h) & 3) * 256;
+        read(ps, lds.q[h], ss, i + h);
         wait_lds();
-        wait_copies<T::kPCopies>();
         meet();
-        copy_q(qs[h], i + h + 2);
-        multiply(ps[h], ss[h]);
-        if (i + h + 1 < steps) wait_copies<T::kQ>();
-        else wait_copies<0>();
+        multiply(ps, ss);
         meet();
       }
     }
@@ -404,22 +451,22 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, u32x4
 #pragma unroll
   for (int a = 0; a < MT; ++a) {
     const int p = at.p0 + G * 16 * MT + a * 16 + l16;
-    if (p >= at.pend) continue;
-    if constexpr (T::kQAlong) {  // a lane holds sixteen neighbouring columns
+    const int64_t at0 = out0 + p * j.out_pitch;
+    if (j.out_f32 || j.accumulate) {
+      if (p >= at.pend) continue;
 #pragma unroll
-      for (int b = 0; b < 4; b += 2) {
-        const int q = at.q0 + 64 * wq + 16 * g + 4 * b;
-        if (q >= Qn) continue;
-        const float v[8] = {acc[a][b][0],     acc[a][b][1],     acc[a][b][2],     acc[a][b][3],
-                            acc[a][b + 1][0], acc[a][b + 1][1], acc[a][b + 1][2], acc[a][b + 1][3]};
-        if (j.out_f32) st8<MOE_F32>(j.out, out0 + p * j.out_pitch + q, v);
-        else st8<MOE_BF16>(j.out, out0 + p * j.out_pitch + q, v);
+      for (int b = 0; b < 4; ++b) {
+        const int q = at.q0 + 64 * wq + (T::kQAlong ? 32 * (b >> 1) + 8 * g + 4 * (b & 1) : 16 * b + 4 * g);
+        if (q < Qn) put4(j, at0 + q, acc[a][b]);
       }
     } else {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int q = at.q0 + 64 * wq + 16 * b + 4 * g;
-        if (q < Qn) put4(j, out0 + p * j.out_pitch + q, acc[a][b]);
+      for (int b = 0; b < 4; b += 2) {
+        u32x4 v = {pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]),
+                   pack_bf16x2(acc[a][b + 1][0], acc[a][b + 1][1]), pack_bf16x2(acc[a][b + 1][2], acc[a][b + 1][3])};
+        if constexpr (!T::kQAlong) neighbours(v);
+        const int q = at.q0 + 64 * wq + 16 * b + 8 * g;
+        if (p < at.pend && q < Qn) *reinterpret_cast<u32x4*>((uint16_t*)j.out + at0 + q) = v;
       }
     }
   }
@@ -429,14 +476,16 @@ constexpr int kXcds = 8;
 
 template <int MODE, int DT>
 __global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
-  __shared__ u32x4 p00[1024], p01[1024], p10[1024], p11[1024], q0[2048], q1[2048];
-  __shared__ float s00[128], s01[128], s10[128], s11[128];
+  __shared__ u32x4 p0[2048], p1[2048], q0[2048], q1[2048];
+  constexpr bool kScaled = DT == MOE_FP8_E4M3;
+  __shared__ float scale[kScaled ? 1024 : 1], w_scale[kScaled ? 2 * kMaxBlocks : 1];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int Qn = MODE == kWeightsGrad ? j.D : j.N, ct = (Qn + kTile - 1) / kTile;
+  const Lds lds = {{p0, p1}, {q0, q1}, scale, w_scale};
 
   auto run = [&](const Place& at, auto mt) {
-    if (wv < 4) tile<MODE, DT, mt(), 0>(j, at, p00, p10, q0, q1, s00, s10, wv, lane);
-    else tile<MODE, DT, mt(), 1>(j, at, p01, p11, q0, q1, s01, s11, wv - 4, lane);
+    if (wv < 4) tile<MODE, DT, mt(), 0>(j, at, lds, wv, lane);
+    else tile<MODE, DT, mt(), 1>(j, at, lds, wv - 4, lane);
   };
   const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds, per = (gridDim.x - xcd + kXcds - 1) / kXcds;
 
@@ -526,6 +575,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
       else run(at, std::integral_constant<int, 8>{});
     }
   }
+  wait_copies<0>();  // nothing lands in this LDS once it is another workgroup's
 }
 
 static int compute_units() {
