@@ -2,51 +2,11 @@
 // (v_mfma_f32_16x16x128_f8f6f4 with fp32 scales), operands copied straight into LDS.
 #include <type_traits>
 
-#include "products.hpp"
+#include "product_copy.hpp"
 
 namespace moe {
 
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(8))) int i32x8;
-
-constexpr int kTile = 256, kStep = 64;  // a step's k: 64 bf16 or 128 codes, 128 bytes of a row either way
-static __device__ u32x4 g_zeros;        // what lanes past a contraction's end copy
-
-// A wave's copy of 64 x 16 (or 64 x 4) bytes to LDS, lane after lane from dst on.  In inline assembly, so that
-// the compiler does not put waits of its own before every LDS read that might meet a copy (it tells the copies of
-// a few instructions apart, and a tile has more); the waits are wait_copies and meet below.  The address is
-// read when the copy is issued, and nothing is returned to a register.
-__device__ __forceinline__ uint32_t lds_at(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
-__device__ __forceinline__ void copy16(const char* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
-}
-__device__ __forceinline__ void copy16(const char* base, uint32_t off, uint32_t dst) {  // base in scalar registers
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(const char* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void wait_copies() {  // at most N of this wave's copies are still on their way
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8)); }
-__device__ __forceinline__ void meet() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
-
-// One tile's place: rows of C p0 .. pend - 1 of expert e from column q0, contraction k0 .. kend - 1.
-struct Place {
-  int e, p0, pend, q0, k0, kend;
-};
+constexpr int kTile = 256;
 
 // How an operand lies in LDS and how a step of it is copied there.  A stage holds 256 p and 256 q by 64 k (128
 // codes); a wave's copy instruction fills 1 KiB, eight runs of 128 bytes, each from one row of memory.
@@ -68,12 +28,6 @@ struct Tile {
   static constexpr int kP = MT / 2, kQ = 8, kScales = kScaled ? 1 : 0;
   static constexpr int kFirst = kQ + kP + kScales, kSecond = kP;
 };
-__device__ __forceinline__ const char* uniform_ptr(const char* p) {
-  const uint64_t v = (uint64_t)p;
-  return (const char*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
-                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32);
-}
-
 // NB blocks of 64 columns of an operand whose rows lie across k: byte offsets of this lane's copies from row k0 of
 // the matrix, two copies to a block, of row() and of the row 32 further.  Columns past the end are read at others.
 template <int NB>
@@ -107,24 +61,12 @@ struct Across {
   }
 };
 
-// Lane groups g hold columns 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3 of a row, two values to a register; after it
-// they hold columns 8 g .. 8 g + 7, 16 bytes that can be stored at once.
-__device__ __forceinline__ void neighbours(u32x4& v) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const auto h = __builtin_amdgcn_permlane32_swap(v[i], v[2 + i], false, false);
-    const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
-    v[i] = r[0];
-    v[2 + i] = r[1];
-  }
-}
-
 // What a workgroup has in LDS: two stages of P (16 KiB for each group's rows) and of Q, four of the rows' scales.
 struct Lds {
   u32x4 *p[2], *q[2];
   float *scale, *w_scale;
 };
-constexpr int kMaxBlocks = kHMaxRows / 128;  // scales of a row
+
 
 // The base and pitch of an operand's rows.
 template <int MODE, int DT>
@@ -578,16 +520,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
   wait_copies<0>();  // nothing lands in this LDS once it is another workgroup's
 }
 
-static int compute_units() {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-    return 0;
-  return cus;
-}
-
-int run_tiles(const ProductJob& j, int dtype, int mode, hipStream_t stream) {
-  const unsigned cus = (unsigned)compute_units();
-  if (!cus) return MOE_ELAUNCH;
+int run_tiles(const ProductJob& j, int dtype, int mode, int units, hipStream_t stream) {
+  const unsigned cus = (unsigned)units;
   if (dtype == MOE_FP8_E4M3) return launch(tiles_kernel<kForward, MOE_FP8_E4M3>, cus, 512u, stream, j);
   if (mode == kForward) return launch(tiles_kernel<kForward, MOE_BF16>, cus, 512u, stream, j);
   if (mode == kRowsGrad) return launch(tiles_kernel<kRowsGrad, MOE_BF16>, cus, 512u, stream, j);

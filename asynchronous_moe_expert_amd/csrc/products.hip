@@ -1,5 +1,7 @@
 // moe_expert_matmul, moe_expert_matmul_backward: the products of each expert's rows with its row-major
 // weights, in either direction, and the weights' gradient.
+#include <atomic>
+
 #include "products.hpp"
 
 namespace moe {
@@ -144,9 +146,25 @@ __global__ __launch_bounds__(256) void product_kernel(ProductJob j) {
 constexpr int64_t kReach = (int64_t)1 << 36;  // bytes of x, or of an expert's matrix
 constexpr int64_t kPitch = (int64_t)1 << 24;  // bytes between its rows
 
+// The current device's compute units, looked up once per device (0: none).
+static int compute_units() {
+  static std::atomic<int> known[64];
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
+  if (dev < 64 && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+  if (dev < 64) known[dev].store(cus, std::memory_order_relaxed);
+  return cus;
+}
+
 template <int DT, int MODE>
 static int run_product(const ProductJob& j, hipStream_t stream) {
-  if (DT != MOE_F32) return run_tiles(j, DT, MODE, stream);
+  if (DT != MOE_F32) {
+    const bool few = MODE != kWeightsGrad && j.n <= 64 * (int64_t)j.E;
+    const int cus = compute_units();
+    if (!cus) return MOE_ELAUNCH;
+    return few ? run_narrow(j, DT, MODE, cus, stream) : run_tiles(j, DT, MODE, cus, stream);
+  }
   const int64_t ct = ((MODE == kWeightsGrad ? j.D : j.N) + kS - 1) / kS;
   const int64_t rt = MODE == kWeightsGrad ? (int64_t)j.E * ((j.N + kS - 1) / kS) : j.n / kS + (j.n < j.E ? j.n : j.E);
   if (rt * ct > (1 << 24) - 1) return MOE_EINVAL_SIZE;

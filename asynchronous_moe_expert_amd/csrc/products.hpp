@@ -1,4 +1,4 @@
-// What the kernels of the experts' products share (products.hip, product_tiles.hip).
+// What the kernels of the experts' products share (products.hip, product_tiles.hip, product_narrow.hip).
 #pragma once
 
 #include "home.hpp"
@@ -54,6 +54,8 @@ __device__ __forceinline__ void put4(const ProductJob& j, int64_t at, f32x4 v) {
 }
 
 // product_tiles.hip: 256 x 256 tiles on the bf16 and 8-bit matrix instructions
-int run_tiles(const ProductJob& j, int dtype, int mode, hipStream_t stream);
+int run_tiles(const ProductJob& j, int dtype, int mode, int cus, hipStream_t stream);
+// product_narrow.hip: tiles of few rows, for products that are bound by reading the weights
+int run_narrow(const ProductJob& j, int dtype, int mode, int cus, hipStream_t stream);
 
 }  // namespace moe
