@@ -1,6 +1,9 @@
 // What the kernels that copy their operands straight into LDS share (product_tiles.hip, product_narrow.hip).
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "products.hpp"
 
 namespace moe {
@@ -19,15 +22,30 @@ static __device__ u32x4 g_zeros;  // what lanes past a contraction's end copy
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
+template <int AT = 0>
 __device__ __forceinline__ void copy16(const char* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+  asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst), "n"(AT)
+               : "memory", "scc");
 }
+template <int AT = 0>
 __device__ __forceinline__ void copy16(const char* base, uint32_t off, uint32_t dst) {  // base in scalar registers
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst)
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst), "n"(AT)
+               : "memory", "scc");
+}
+__device__ __forceinline__ void copy16_once(const char* base, uint32_t off, uint32_t dst) {  // non-temporal
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(dst)
                : "memory");
 }
 __device__ __forceinline__ void copy4(const char* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
+}
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {  // f(0) .. f(N - 1), with constants
+  each_of(f, std::make_integer_sequence<int, N>{});
 }
 
 template <int N>
@@ -43,9 +61,10 @@ __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
 }
 
-// One tile's place: rows of C p0 .. pend - 1 of expert e from column q0, contraction k0 .. kend - 1.
+// One tile's place: rows of C p0 .. pend - 1 of expert e (-1: no tile) from column q0, contraction k0 .. kend - 1; mt: the
+// 16 rows of C that each half of the workgroup takes, as many times.
 struct Place {
-  int e, p0, pend, q0, k0, kend;
+  int e, p0, pend, q0, k0, kend, mt;
 };
 
 __device__ __forceinline__ const char* uniform_ptr(const char* p) {

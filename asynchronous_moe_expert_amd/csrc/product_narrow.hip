@@ -10,7 +10,7 @@ namespace moe {
 // what the chip has on its way over the latency (2 to 2.5 us when HBM is busy), so the shapes are chosen to have
 // much on its way on all CUs:
 //   WK = 1, NW = 4, S = 3: two workgroups to a CU, for calls of many of them;
-//   WK = 1, NW = 3, 4, 6 or 8, S = 7, 6, 4 or 3: one to a CU and more steps, for calls whose workgroups all run at
+//   WK = 1, NW = 4, 6 or 8, S = 6, 4 or 3: one to a CU and more steps, for calls whose workgroups all run at
 //           once; run_narrow chooses the NW that leaves the fewest CUs idle;
 //   WK = 4: 32 columns, a step is four times as long, each wave takes its quarter and the waves' sums are added at
 //           the end: for calls that would leave most CUs idle.
@@ -30,7 +30,7 @@ struct Narrow {
 
 template <typename T, int MODE, int DT, int WK, int MT>
 __device__ __forceinline__ void narrow_tile(const ProductJob& j, const Place& at, char* ring, float* scales, const float* wsc,
-                                            int wv, int lane) {
+                                            int wv, int lane, bool once) {
   constexpr int es = T::es, NW = T::kWaves, kStages = T::kStages;
   constexpr int kP = WK == 1 ? (2 * MT + NW - 1) / NW : 2 * MT, kCopies = 4 + kP + (T::kScaled ? 1 : 0);
   static_assert((kStages - 2) * kCopies < 64, "a wave's copies are counted in six bits");
@@ -90,7 +90,8 @@ __device__ __forceinline__ void narrow_tile(const ProductJob& j, const Place& at
         const int piece = (lane & 7) ^ (((lane >> 4) & 1) | 2 * (i & 3));
         const char* from = uniform_ptr(q + (int64_t)first * 16 + (at.q0 + r < j.N ? r : 0) * j.w_pitch * es);
         const uint32_t to = dst + (WK == 1 ? i : 4 * wv + c) * 1024;
-        if (whole) copy16(from, qoff[0] + piece * 16, to);
+        if (whole && once) copy16_once(from, qoff[0] + piece * 16, to);
+        else if (whole) copy16(from, qoff[0] + piece * 16, to);
         else copy16(first + piece < pieces ? from + (qoff[0] + piece * 16) : (const char*)&g_zeros, to);
       }
     } else {
@@ -289,9 +290,13 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(ProductJob j) {
     }
     __syncthreads();
   }
+  // Weights that no other workgroup reads pass through the caches without staying (256 rows of 8 experts, 5760 x 2880
+  // bf16 from HBM: 50 us with cached copies, 44 so), unless a step's 128 bytes of a row are parts of two lines, which
+  // the next step wants again (the same in 8 bits, rows of 2880 bytes: 31 us cached, 33 so).
+  const bool once = n == 1 && (j.w_pitch * T::es) % 128 == 0 && (j.w_stride * T::es) % 128 == 0 && ((uint64_t)j.w & 127) == 0;
   const int rows = at.pend - at.p0;
-  if (rows <= kRows / 2) narrow_tile<T, MODE, DT, WK, T::kMT / 2>(j, at, ring, scales, wsc, wv, lane);
-  else narrow_tile<T, MODE, DT, WK, T::kMT>(j, at, ring, scales, wsc, wv, lane);
+  if (rows <= kRows / 2) narrow_tile<T, MODE, DT, WK, T::kMT / 2>(j, at, ring, scales, wsc, wv, lane, once);
+  else narrow_tile<T, MODE, DT, WK, T::kMT>(j, at, ring, scales, wsc, wv, lane, once);
 }
 
 template <int MODE, int DT, int WK, int NW, int S>
@@ -311,7 +316,7 @@ static int choose_narrow(const ProductJob& j, int64_t cus, hipStream_t stream) {
     // one workgroup to a CU: the least work on the busiest one, the widest of equals
     int best = 8;
     int64_t cost = (units(8) + cus - 1) / cus * 8;
-    for (int nw : {6, 4, 3}) {
+    for (int nw : {6, 4}) {
       const int64_t c = (units(nw) + cus - 1) / cus * nw;
       if (c < cost) {
         best = nw;
@@ -321,8 +326,7 @@ static int choose_narrow(const ProductJob& j, int64_t cus, hipStream_t stream) {
     if (units(best) <= cus) {
       if (best == 8) return launch_narrow<MODE, DT, 1, 8, 3>(j, stream);
       if (best == 6) return launch_narrow<MODE, DT, 1, 6, 4>(j, stream);
-      if (best == 4) return launch_narrow<MODE, DT, 1, 4, 6>(j, stream);
-      return launch_narrow<MODE, DT, 1, 3, 7>(j, stream);
+      return launch_narrow<MODE, DT, 1, 4, 6>(j, stream);
     }
   }
   return launch_narrow<MODE, DT, 1, 4, 3>(j, stream);

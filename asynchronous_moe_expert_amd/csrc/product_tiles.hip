@@ -6,7 +6,8 @@
 
 namespace moe {
 
-constexpr int kTile = 256;
+constexpr int kTile = 256, kStageQ = kTile * 128;
+constexpr int kPool = 3 * (kStageQ + 128 * 128);  // bytes of LDS for the stages: three of MT = 4, two of MT = 8
 
 // How an operand lies in LDS and how a step of it is copied there.  A stage holds 256 p and 256 q by 64 k (128
 // codes); a wave's copy instruction fills 1 KiB, eight runs of 128 bytes, each from one row of memory.
@@ -24,6 +25,9 @@ struct Tile {
   static constexpr bool kPAlong = MODE != kWeightsGrad, kQAlong = MODE == kForward;
   static constexpr bool kScaled = DT == MOE_FP8_E4M3;
   static constexpr int kHalf = MT / 2;
+  static constexpr int kStages = MT <= 4 ? 3 : 2;  // steps in LDS
+  static constexpr int kStageP = 32 * MT * 128;    // bytes of P in one, half for each group; Q has kStageQ
+  static constexpr bool kTurn = kQAlong && MT <= 4;  // column tiles begin at different k
   // copies that a wave of group 0 makes in a step: of each group's rows of P, of Q, and of the rows' scales
   static constexpr int kP = MT / 2, kQ = 8, kScales = kScaled ? 1 : 0;
   static constexpr int kFirst = kQ + kP + kScales, kSecond = kP;
@@ -48,25 +52,34 @@ struct Across {
     const char* from = uniform_ptr(base + (int64_t)step * kStep * pitch_bytes);
     const char* odd = uniform_ptr(from + 32 * pitch_bytes);
     if ((step + 1) * kStep <= end) {
-#pragma unroll
-      for (int c = 0; c < 2 * NB; ++c) copy16(c & 1 ? odd : from, off[c >> 1], dst + c * 4096);
+      each<2 * NB>([&](auto c) { copy16<c() * 4096>(c() & 1 ? odd : from, off[c() >> 1], dst); });
     } else {
       const int k = step * kStep + row(wq, lane);
-#pragma unroll
-      for (int c = 0; c < 2 * NB; ++c) {
-        const char* src = (c & 1 ? odd : from) + off[c >> 1];
-        copy16(k + 32 * (c & 1) < end ? src : (const char*)&g_zeros, dst + c * 4096);
-      }
+      each<2 * NB>([&](auto c) {
+        const char* src = (c() & 1 ? odd : from) + off[c() >> 1];
+        copy16<c() * 4096>(k + 32 * (c() & 1) < end ? src : (const char*)&g_zeros, dst);
+      });
     }
   }
 };
 
-// What a workgroup has in LDS: two stages of P (16 KiB for each group's rows) and of Q, four of the rows' scales.
+// What a workgroup has in LDS: the stages (all of Q's, then P's), four steps of the rows' scales, the weights' scales
+// of the tile's two blocks of columns, and where the rows of this tile and the next come from.
 struct Lds {
-  u32x4 *p[2], *q[2];
+  char* pool;
   float *scale, *w_scale;
+  int* slots;    // [2][256]
+  Place* place;  // [2]
 };
 
+__device__ __forceinline__ Place load_place(const Place* from) {
+  Place at;
+  int* to = reinterpret_cast<int*>(&at);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Place) / 4); ++i)
+    to[i] = __builtin_amdgcn_readfirstlane(reinterpret_cast<const int*>(from)[i]);
+  return at;
+}
 
 // The base and pitch of an operand's rows.
 template <int MODE, int DT>
@@ -83,13 +96,9 @@ __device__ __forceinline__ const char* q_base(const ProductJob& j, const Place& 
   else return (const char*)j.w + (at.e * j.w_stride + (MODE == kForward ? at.q0 * j.w_pitch : 0)) * esize<DT>();
 }
 
-// The row of the tile's P that lies at place r of group h's 16 MT, and where it comes from (-1: nowhere).
-template <int MT>
-__device__ __forceinline__ int64_t p_source(const ProductJob& j, const Place& at, int h, int r) {
-  const int row = min(at.p0 + h * 16 * MT + min(r, 16 * MT - 1), at.pend - 1);
-  if (!j.row_slot) return row;
-  const int64_t slot = j.row_slot[row];
-  return slot < 0 || slot >= j.x_rows ? -1 : slot;
+template <int MODE, int DT>
+__device__ __forceinline__ int contraction_steps(const ProductJob& j, const Place& at) {
+  return MODE == kWeightsGrad ? (at.kend - at.k0 + kStep - 1) / kStep : (j.D * esize<DT>() + 127) / 128;
 }
 
 // The copies of a tile's operands, all made by the four waves wq of group 0.
@@ -105,95 +114,155 @@ struct Copies {
   uint32_t qoff = 0;
   Across<4> qa;
   int pieces;  // of a row along k
-  int steps;
+  int steps, turn;
 
+  // the step of the contraction that is taken as the s-th
+  __device__ __forceinline__ int step_of(int s) const {
+    if constexpr (!T::kTurn) return s;
+    return s + turn < steps ? s + turn : s + turn - steps;
+  }
   static __device__ __forceinline__ int ppiece(int wq, int lane) { return (lane & 7) ^ (4 * (wq & 1) + (lane >> 4)); }
   static __device__ __forceinline__ int qpiece(int wq, int lane) { return (lane & 7) ^ (((lane >> 4) & 1) | 2 * wq); }
 
-  __device__ __forceinline__ void set(const ProductJob& j, const Place& at, int steps_, int wq, int lane) {
+  __device__ __forceinline__ void set(const ProductJob& j, const Place& at, const int* slots, int wq, int lane) {
     pieces = j.D * es / 16;
-    steps = steps_;
+    steps = contraction_steps<MODE, DT>(j, at);
+    turn = turn_of(at, steps);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (T::kPAlong) {
 #pragma unroll
         for (int c = 0; c < T::kP; ++c) {
-          int64_t slot = p_source<MT>(j, at, h, 8 * (4 * c + wq) + (lane >> 3));
-          if (slot < 0) {
-            atomicOr(j.err, MOE_ERR_SLOT_RANGE);
-            slot = 0;
-            nosrc |= 1u << (h * T::kP + c);
-          }
-          poff[h][c] = (uint32_t)(slot * (j.x_pitch * es / 16) + ppiece(wq, lane));
+          const int slot = slots[h * 16 * MT + 8 * (4 * c + wq) + (lane >> 3)];
+          if (slot < 0) nosrc |= 1u << (h * T::kP + c);
+          poff[h][c] = (uint32_t)((slot < 0 ? 0 : slot) * (j.x_pitch * es / 16) + ppiece(wq, lane));
         }
       } else {
         pa[h].set(wq, lane, at.p0 + h * 16 * MT, j.N, j.dout_pitch, es);
       }
     }
     if constexpr (T::kScaled) {
-      const int64_t slot = p_source<MT>(j, at, wq >> 1, (wq & 1) * 64 + lane);
+      const int slot = slots[(wq >> 1) * 16 * MT + min((wq & 1) * 64 + lane, 16 * MT - 1)];
       if (slot < 0) nosrc |= 1u << 31;
-      else sptr = j.x_scale + slot * ((j.D + 127) / 128);
+      else sptr = j.x_scale + (int64_t)slot * ((j.D + 127) / 128);
     }
     sourced = __ballot(nosrc != 0) == 0;
     if constexpr (T::kQAlong) qoff = (uint32_t)((lane >> 3) * (int)j.w_pitch * es + qpiece(wq, lane) * 16);
     else qa.set(wq, lane, at.q0, MODE == kWeightsGrad ? j.D : j.N, MODE == kWeightsGrad ? j.x_pitch : j.w_pitch, es);
   }
-  __device__ __forceinline__ void p_half(const ProductJob& j, const Place& at, int h, const u32x4* stage, int step, int wq,
+  // where the s-th step lies in LDS
+  static __device__ __forceinline__ int p_at(int s) { return T::kStages * kStageQ + s % T::kStages * T::kStageP; }
+  static __device__ __forceinline__ int q_at(int s) { return s % T::kStages * kStageQ; }
+  // Weights whose rows are a power of two apart put the same step of all of them on a few memory channels: the
+  // column tiles of an expert begin at different steps, which costs nothing where its rows fit the L2
+  static __device__ __forceinline__ int turn_of(const Place& at, int steps) {
+    return T::kTurn ? ((at.q0 / kTile) * 11 + at.e * 3) % steps : 0;
+  }
+  __device__ __forceinline__ void p_half(const ProductJob& j, const Place& at, const Lds& lds, int h, int s, int wq,
                                          int lane) const {
-    const uint32_t dst = lds_at(stage) + h * 16384 + wq * 1024;
+    const int step = step_of(s);
+    const uint32_t dst = lds_at(lds.pool) + p_at(s) + h * (T::kStageP / 2) + wq * 1024;
     if constexpr (T::kPAlong) {
       const char* from = uniform_ptr(p_base<MODE, DT>(j, at) + (int64_t)step * 128);
       if (sourced && (step + 1) * 8 <= pieces) {
-#pragma unroll
-        for (int c = 0; c < T::kP; ++c) copy16(from + (uint64_t)poff[h][c] * 16, dst + c * 4096);
+        each<T::kP>([&](auto c) { copy16<c() * 4096>(from + (uint64_t)poff[h][c()] * 16, dst); });
       } else {
-#pragma unroll
-        for (int c = 0; c < T::kP; ++c)
-          copy16(step * 8 + ppiece(wq, lane) < pieces && !(nosrc >> (h * T::kP + c) & 1) ? from + (uint64_t)poff[h][c] * 16
-                                                                                        : (const char*)&g_zeros,
-                 dst + c * 4096);
+        each<T::kP>([&](auto c) {
+          const bool there = step * 8 + ppiece(wq, lane) < pieces && !(nosrc >> (h * T::kP + c()) & 1);
+          copy16<c() * 4096>(there ? from + (uint64_t)poff[h][c()] * 16 : (const char*)&g_zeros, dst);
+        });
       }
     } else {
       pa[h].copy(p_base<MODE, DT>(j, at), j.dout_pitch * es, dst, step, at.kend - at.k0, wq, lane);
     }
   }
   // Q, group 0's rows of P, and all rows' scales
-  __device__ __forceinline__ void first(const ProductJob& j, const Place& at, const Lds& lds, int step, int wq,
-                                        int lane) const {
-    const int Qn = MODE == kWeightsGrad ? j.D : j.N;
-    const uint32_t dst = lds_at(lds.q[step & 1]) + wq * 1024;
+  __device__ __forceinline__ void first(const ProductJob& j, const Place& at, const Lds& lds, int s, int wq, int lane) const {
+    const int Qn = MODE == kWeightsGrad ? j.D : j.N, step = step_of(s);
+    const uint32_t dst = lds_at(lds.pool) + q_at(s) + wq * 1024;
     const char* q = q_base<MODE, DT>(j, at);
     if constexpr (T::kQAlong) {  // N is a multiple of 8, so rows are past it by whole copies: read at the first ones
-      const bool whole = (step + 1) * 8 <= pieces;
-#pragma unroll
-      for (int c = 0; c < T::kQ; ++c) {
-        const int r = 8 * (4 * c + wq);
-        const char* from = uniform_ptr(q + (int64_t)step * 128 + (at.q0 + r < Qn ? r : 0) * j.w_pitch * es);
-        if (whole) copy16(from, qoff, dst + c * 4096);
-        else copy16(step * 8 + qpiece(wq, lane) < pieces ? from + qoff : (const char*)&g_zeros, dst + c * 4096);
+      const char* from = uniform_ptr(q + (int64_t)step * 128 + 8 * wq * j.w_pitch * es);
+      if (at.q0 + kTile <= Qn && (step + 1) * 8 <= pieces) {
+        const int64_t rows = 32 * j.w_pitch * es;
+        each<T::kQ>([&](auto c) {
+          copy16<c() * 4096>(from, qoff, dst);
+          from += rows;
+        });
+      } else {
+        const bool there = step * 8 + qpiece(wq, lane) < pieces;
+        each<T::kQ>([&](auto c) {
+          const int r = 32 * c();
+          const char* row = uniform_ptr(at.q0 + 8 * wq + r < Qn ? from + r * j.w_pitch * es : q + (int64_t)step * 128);
+          copy16<c() * 4096>(there ? row + qoff : (const char*)&g_zeros, dst);
+        });
       }
     } else {
       qa.copy(q, q_pitch<MODE, DT>(j), dst, step, at.kend - at.k0, wq, lane);
     }
-    p_half(j, at, 0, lds.p[step & 1], step, wq, lane);
+    p_half(j, at, lds, 0, s, wq, lane);
     if constexpr (T::kScaled) {
       const char* src = !(nosrc >> 31) ? (const char*)(sptr + step) : (const char*)&g_zeros;
-      copy4(src, lds_at(lds.scale) + (step & 3) * 1024 + wq * 256);
+      copy4(src, lds_at(lds.scale) + (s & 3) * 1024 + wq * 256);
     }
   }
-  __device__ __forceinline__ void second(const ProductJob& j, const Place& at, const Lds& lds, int step, int wq,
-                                         int lane) const {
-    p_half(j, at, 1, lds.p[step & 1], step, wq, lane);
+  __device__ __forceinline__ void second(const ProductJob& j, const Place& at, const Lds& lds, int s, int wq, int lane) const {
+    p_half(j, at, lds, 1, s, wq, lane);
   }
 };
 
-template <int MODE, int DT, int MT, int G>
-__device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const Lds& lds, int wq, int lane) {
+// Copies the first steps of a tile, as many as LDS holds.
+template <int MODE, int DT, int MT>
+__device__ __forceinline__ void begin(const ProductJob& j, const Place& at, const Lds& lds, const int* slots, int wq, int lane) {
+  Copies<MODE, DT, MT> c;
+  c.set(j, at, slots, wq, lane);
+#pragma unroll
+  for (int s = 0; s < Tile<MODE, DT, MT>::kStages; ++s) {
+    if (s < c.steps) {
+      c.first(j, at, lds, s, wq, lane);
+      c.second(j, at, lds, s, wq, lane);
+    }
+  }
+}
+template <int MODE, int DT>
+__device__ __forceinline__ void begin_any(const ProductJob& j, const Place& at, const Lds& lds, const int* slots, int wq,
+                                          int lane) {
+  switch (at.mt) {
+    case 2:
+      if constexpr (MODE != kWeightsGrad) begin<MODE, DT, 2>(j, at, lds, slots, wq, lane);
+      break;
+    case 4: begin<MODE, DT, 4>(j, at, lds, slots, wq, lane); break;
+    case 6:
+      if constexpr (MODE != kWeightsGrad) begin<MODE, DT, 6>(j, at, lds, slots, wq, lane);
+      break;
+    default: begin<MODE, DT, 8>(j, at, lds, slots, wq, lane);
+  }
+}
+
+// Where the next tile's rows come from, and a scale for each block of 128 columns and 128 k of this one: group 1's
+// part, which waits for nothing else in memory.
+template <int MODE>
+__device__ __forceinline__ void find_rows(const ProductJob& j, const Place& at, int* slots, int i) {
+  if constexpr (MODE != kWeightsGrad) {
+    const int row = min(at.p0 + i, at.pend - 1);
+    int slot = row;
+    if (j.row_slot) {
+      slot = j.row_slot[row];
+      if (slot < 0 || slot >= j.x_rows) {
+        atomicOr(j.err, MOE_ERR_SLOT_RANGE);
+        slot = -1;
+      }
+    }
+    slots[i] = slot;
+  }
+}
+
+template <int MODE, int DT, int MT, int G, typename W>
+__device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& walk, const Lds& lds, int par, int wq, int lane) {
   using T = Tile<MODE, DT, MT>;
   constexpr int es = T::es, kHalf = T::kHalf;
   const int g = lane >> 4, l16 = lane & 15;
-  const int steps = MODE == kWeightsGrad ? (at.kend - at.k0 + kStep - 1) / kStep : (j.D * es + 127) / 128;
+  const int steps = contraction_steps<MODE, DT>(j, at);
   const int Qn = MODE == kWeightsGrad ? j.D : j.N;
 
   // ---- where this lane's fragments lie, in bytes
@@ -210,9 +279,9 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const
     asm volatile("v_xor_b32 %0, %1, %2" : "=v"(r) : "n"(bits), "v"(a));
     return r;
   };
-  auto along = [&](const u32x4* stage, int at_) { return *reinterpret_cast<const u32x4*>((const char*)stage + at_); };
-  auto across = [&](const u32x4* stage, int at_) -> u32x4 {
-    const char* b = (const char*)stage + at_;
+  auto along = [&](const char* stage, int at_) { return *reinterpret_cast<const u32x4*>(stage + at_); };
+  auto across = [&](const char* stage, int at_) -> u32x4 {
+    const char* b = stage + at_;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(b));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(b + 512));
     u32x4 r;
@@ -228,14 +297,14 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const
     for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 pf[kHalf][2], qf[4][2];
   float sc[kHalf], sw = 0.f;
-  auto read_p = [&](const u32x4* ps, const float* ss, int a0, int a, int at0, int at1) {  // tile a0 + a of the group's rows
+  auto read_p = [&](const char* ps, const float* ss, int a0, int a, int at0, int at1) {  // tile a0 + a of the group's rows
     if constexpr (T::kPAlong) {
       pf[a][0] = along(ps, at0 + (a0 + a) * 2048);
       pf[a][1] = along(ps, at1 + (a0 + a) * 2048);
     }
     if constexpr (T::kScaled) sc[a] = ss[G * 128 + (a0 + a) * 16 + l16];
   };
-  auto read = [&](const u32x4* ps, const u32x4* qs, const float* ss, int step) {
+  auto read = [&](const char* ps, const char* qs, const float* ss, int step) {
     if constexpr (T::kScaled) sw = lds.w_scale[(wq >> 1) * kMaxBlocks + step];
     if constexpr (T::kQAlong) {
       const int q1 = flip(qr, 64);
@@ -301,7 +370,7 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const
         }
     }
   };
-  auto multiply = [&](const u32x4* ps, const float* ss) {
+  auto multiply = [&](const char* ps, const float* ss) {
     __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
     int p1 = 0;
@@ -327,65 +396,85 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const
     __builtin_amdgcn_s_setprio(0);
   };
 
-  if constexpr (T::kScaled) {  // the scales of the tile's two blocks of columns
-    const int nb = (j.N + 127) / 128;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const float* from = j.w_scale + ((int64_t)at.e * nb + min((at.q0 >> 7) + b, nb - 1)) * steps;
-      for (int k = G * 256 + wq * 64 + lane; k < steps; k += 512) lds.w_scale[b * kMaxBlocks + k] = from[k];
-    }
-    wait_lds();
-  }
-
   // ---- The waves of a SIMD, one of each group, take turns: while one multiplies a step's fragments, which it
   // holds in registers, the other reads its next ones (Q's and half of P's; the other half takes the place of
   // what has been multiplied).  Group 0 reads step i in phase 2 i and multiplies in phase 2 i + 1, group 1 one
   // phase later; a barrier ends each phase.  So of a stage, Q and group 0's rows of P are free after phase 2 i + 1,
   // group 1's after 2 i + 2: group 0 copies step i + 2 there in the phase after, two phases before it is read.
+  // The steps that LDS holds have been copied when the tile begins; from then on step s + S - 1 goes where step s - 1
+  // was (S = 2, or 3 where the rows are few and the weights come from HBM).
+  using C = Copies<MODE, DT, MT>;
+  constexpr int S = T::kStages, kBoth = T::kFirst + T::kSecond;
+  static_assert((S - 1) * kBoth < 64, "a wave's copies are counted in six bits");
   if constexpr (G == 0) {
-    Copies<MODE, DT, MT> c;
-    c.set(j, at, steps, wq, lane);
-    c.first(j, at, lds, 0, wq, lane);
-    c.second(j, at, lds, 0, wq, lane);
-    wait_copies<T::kSecond>();
+    C c;
+    c.set(j, at, lds.slots + par * 256, wq, lane);
+    wait_lds();
     meet();
 #pragma clang loop unroll(disable)
-    for (int i = 0; i < steps; i += 2) {
+    for (int i = 0; i < steps; i += S) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (i + h >= steps) break;
-        const u32x4* ps = lds.p[h];
-        const float* ss = lds.scale + ((i + h) & 3) * 256;
-        if (i + h + 1 < steps) c.first(j, at, lds, i + h + 1, wq, lane);
-        read(ps, lds.q[h], ss, i + h);
+      for (int h = 0; h < S; ++h) {
+        const int s = i + h;
+        if (s >= steps) break;
+        const char *ps = lds.pool + C::p_at(h), *qs = lds.pool + C::q_at(h);
+        const float* ss = lds.scale + (s & 3) * 256;
+        const bool more = s > 0 && s + S - 1 < steps;
+        if (more) c.first(j, at, lds, s + S - 1, wq, lane);
+        read(ps, qs, ss, c.step_of(s));
         wait_lds();
-        if (i + h + 1 < steps) wait_copies<T::kFirst>();
-        else wait_copies<0>();
+        if (s >= S) {  // group 1's rows of step s
+          if (more) wait_copies<(S - 2) * kBoth + T::kFirst>();
+          else wait_copies<0>();
+        }
         meet();
-        if (i + h + 1 < steps) c.second(j, at, lds, i + h + 1, wq, lane);
+        if (more) c.second(j, at, lds, s + S - 1, wq, lane);
         multiply(ps, ss);
-        wait_copies<T::kSecond>();
+        if (s + 1 >= S) {  // the rest of step s + 1
+          if (more) wait_copies<(S - 2) * kBoth + T::kSecond>();
+          else wait_copies<0>();
+        }
         meet();
       }
     }
     meet();
   } else {
+    if constexpr (T::kScaled) {
+      const int nb = (j.N + 127) / 128;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float* from = j.w_scale + ((int64_t)at.e * nb + min((at.q0 >> 7) + b, nb - 1)) * steps;
+        for (int k = wq * 64 + lane; k < steps; k += 256) lds.w_scale[b * kMaxBlocks + k] = from[k];
+      }
+    }
+    {
+      const Place next = walk.next(j);
+      if (next.e >= 0) find_rows<MODE>(j, next, lds.slots + (par ^ 1) * 256, wq * 64 + lane);
+      if (wq == 0 && lane == 0) lds.place[par ^ 1] = next;
+    }
+    const int turn = C::turn_of(at, steps);
+    wait_lds();
     meet();
     meet();
 #pragma clang loop unroll(disable)
-    for (int i = 0; i < steps; i += 2) {
+    for (int i = 0; i < steps; i += S) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < S; ++h) {
         if (i + h >= steps) break;
-        const u32x4* ps = lds.p[h] + 1024;
+        const char *ps = lds.pool + C::p_at(h) + T::kStageP / 2, *qs = lds.pool + C::q_at(h);
         const float* ss = lds.scale + ((i + h) & 3) * 256;
-        read(ps, lds.q[h], ss, i + h);
+        read(ps, qs, ss, i + h + turn < steps ? i + h + turn : i + h + turn - steps);
         wait_lds();
         meet();
         multiply(ps, ss);
         meet();
       }
     }
+  }
+  const Place next = load_place(lds.place + (par ^ 1));
+  // the next tile's first copies go out before this one's stores, which the waits would count otherwise
+  if constexpr (G == 0) {
+    if (next.e >= 0) begin_any<MODE, DT>(j, next, lds, lds.slots + (par ^ 1) * 256, wq, lane);
   }
 
   // ---- outputs
@@ -412,120 +501,211 @@ __device__ __forceinline__ void tile(const ProductJob& j, const Place& at, const
       }
     }
   }
+  // the copies have landed when no more is on its way than this wave's stores, which a whole tile has a known number of
+  if constexpr (G == 0) {
+    if (next.e >= 0) {
+      const bool whole = at.pend - at.p0 == 32 * MT && at.q0 + kTile <= Qn && !j.accumulate;
+      asm volatile("" ::: "memory");
+      if (whole && j.out_f32) wait_copies<4 * MT>();
+      else if (whole) wait_copies<2 * MT>();
+      else wait_copies<0>();
+    }
+  }
+  return next;
 }
 
 constexpr int kXcds = 8;
 
-template <int MODE, int DT>
-__global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
-  __shared__ u32x4 p0[2048], p1[2048], q0[2048], q1[2048];
-  constexpr bool kScaled = DT == MOE_FP8_E4M3;
-  __shared__ float scale[kScaled ? 1024 : 1], w_scale[kScaled ? 2 * kMaxBlocks : 1];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int Qn = MODE == kWeightsGrad ? j.D : j.N, ct = (Qn + kTile - 1) / kTile;
-  const Lds lds = {{p0, p1}, {q0, q1}, scale, w_scale};
+// Which tiles a workgroup computes, one after the other.  One workgroup runs on a CU; those of an XCD (blockIdx % 8)
+// share an L2.
+template <int MODE>
+struct Walk;
 
-  auto run = [&](const Place& at, auto mt) {
-    if (wv < 4) tile<MODE, DT, mt(), 0>(j, at, lds, wv, lane);
-    else tile<MODE, DT, mt(), 1>(j, at, lds, wv - 4, lane);
+// Forward and rows' gradient: an expert's rows make tiles of 256 and one of the rest, of 64, 128, 192 or 256.  The tiles
+// of each height are dealt out to the XCDs evenly, a contiguous part to each (an expert's row tiles of one column
+// block after the other, in bands of at most eight, so that what an XCD computes at a time shares weights and rows),
+// the highest first.  An XCD's workgroups take its tiles in turns, back and forth, so that one that drew a higher
+// tile draws a lower one next; half of them go through theirs from the last to the first, so that low tiles, which
+// are bound by reading their weights, run beside high ones, which are bound by the matrix cores.
+template <>
+struct Walk<kForward> {
+  static constexpr int kHeights = 4;  // MT = 8, 6, 4, 2
+  struct Table {
+    int upto[kHeights][257];  // tiles of the experts before, by height, for one column of tiles
   };
-  const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds, per = (gridDim.x - xcd + kXcds - 1) / kXcds;
+  Table& t;
+  int round = 0;
 
-  if constexpr (MODE == kWeightsGrad) {
-    const int rt = (j.N + kTile - 1) / kTile, V = rt * ct;
-    // each XCD takes an eighth of every expert's tiles, so that all of them have the same share of every
-    // expert's rows
-    int pos = idx;
-    for (int e = 0; e < j.E; ++e) {
-      const int x = (xcd + e) % kXcds, v0 = (int)((int64_t)V * x / kXcds), cnt = (int)((int64_t)V * (x + 1) / kXcds) - v0;
+  __device__ __forceinline__ Walk(const ProductJob& j, Table& table) : t(table) {
+    const int lane = threadIdx.x & 63, k = threadIdx.x >> 6;  // four experts to a lane, a height to a wave
+    if (k < kHeights) {
+      int n[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int r0 = 0, r1 = 0;
+        if (4 * lane + i < j.E) expert_rows(j, 4 * lane + i, r0, r1);
+        const int full = (r1 - r0) / kTile, rest = (r1 - r0) % kTile, height = rest ? kHeights - 1 - (rest - 1) / 64 : -1;
+        n[i] = (k == 0 ? full : 0) + (height == k);
+        sum += n[i];
+      }
+      int upto = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+      }
+      if (lane == 63) t.upto[k][256] = upto;
+      upto -= sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        t.upto[k][4 * lane + i] = upto;
+        upto += n[i];
+      }
+    }
+    __syncthreads();
+  }
+  // this XCD's tiles of a height
+  __device__ __forceinline__ void share(int ct, int xcd, int k, int& u0, int& n) const {
+    const int64_t all = (int64_t)t.upto[k][256] * ct;
+    u0 = (int)(all * xcd / kXcds);
+    n = (int)(all * (xcd + 1) / kXcds) - u0;
+  }
+  __device__ __forceinline__ Place next(const ProductJob& j) {
+    Place at = {-1, 0, 0, 0, 0, 0, 0};
+    const int ct = (j.N + kTile - 1) / kTile, xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+    const int per = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
+    int all = 0, u = 0, u0, n, k = kHeights;
+    for (int i = 0; i < kHeights; ++i) {
+      share(ct, xcd, i, u0, n);
+      all += n;
+    }
+    const int rounds = (all + per - 1) / per;
+    while (k == kHeights && round < rounds) {
+      const int r = 2 * idx < per ? round : rounds - 1 - round;
+      u = r * per + (r & 1 ? per - 1 - idx : idx);
+      ++round;
+      for (k = 0; k < kHeights; ++k) {
+        share(ct, xcd, k, u0, n);
+        if (u < n) {
+          u += u0;
+          break;
+        }
+        u -= n;
+      }
+    }
+    k = __builtin_amdgcn_readfirstlane(k);
+    u = __builtin_amdgcn_readfirstlane(u);
+    if (k == kHeights) return at;
+    const int* upto = t.upto[k];
+    int lo = 0, hi = 256;  // the last expert whose tiles begin at or before u and that has any
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (upto[mid] * ct <= u) lo = mid;
+      else hi = mid;
+    }
+    int r0, r1;
+    expert_rows(j, lo, r0, r1);
+    const int base = upto[lo], tiles = upto[lo + 1] - base;
+    const int v = u - base * ct, bands = (tiles + 7) / 8, bh = (tiles + bands - 1) / bands;
+    const int band = v / (bh * ct), h = min(bh, tiles - band * bh), w = v - band * bh * ct;
+    const int first = k == 0 ? 0 : (r1 - r0) / kTile;  // the rest's tile is the last one
+    at.e = __builtin_amdgcn_readfirstlane(lo);
+    at.p0 = __builtin_amdgcn_readfirstlane(r0 + (first + band * bh + w % h) * kTile);
+    at.q0 = __builtin_amdgcn_readfirstlane(w / h * kTile);
+    at.pend = __builtin_amdgcn_readfirstlane(min(r1, at.p0 + kTile));
+    at.k0 = 0;
+    at.kend = j.D;
+    at.mt = 8 - 2 * k;
+    return at;
+  }
+};
+
+// Weights' gradient: each XCD takes an eighth of every expert's tiles, so that what it computes at a time reads the
+// same rows; the XCDs begin at different experts, so that not all of them store at the same time.
+template <>
+struct Walk<kWeightsGrad> {
+  struct Table {};
+  int pos, step = 0;
+  __device__ __forceinline__ Walk(const ProductJob&, Table&) { pos = blockIdx.x / kXcds; }
+  __device__ __forceinline__ Place next(const ProductJob& j) {
+    Place at = {-1, 0, 0, 0, 0, 0, 0};
+    const int ct = (j.D + kTile - 1) / kTile, V = (j.N + kTile - 1) / kTile * ct, xcd = blockIdx.x % kXcds;
+    const int per = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
+    for (; step < j.E; ++step) {
+      const int e = (step + xcd * j.E / kXcds) % j.E, x = (xcd + e) % kXcds;
+      const int v0 = (int)((int64_t)V * x / kXcds), cnt = (int)((int64_t)V * (x + 1) / kXcds) - v0;
       if (pos >= cnt) {
         pos -= cnt;
         continue;
       }
-      Place at;
-      at.e = e;
+      const int v = v0 + pos;
+      pos += per;
       expert_rows(j, e, at.k0, at.kend);
       at.k0 = __builtin_amdgcn_readfirstlane(at.k0);
       at.kend = __builtin_amdgcn_readfirstlane(at.kend);
-      for (; pos < cnt; pos += per) {
-        const int v = v0 + pos;
-        at.p0 = v / ct * kTile;
-        at.q0 = v % ct * kTile;
-        at.pend = min(j.N, at.p0 + kTile);
-        if (at.kend == at.k0) {  // no rows: zeros, or what was there
-          if (!j.accumulate)
-            for (int i = threadIdx.x; i < kTile * kTile / 4; i += 512) {
-              const int p = at.p0 + i / 64, q = at.q0 + i % 64 * 4;
-              if (p < j.N && q < Qn) put4(j, e * j.out_stride + p * j.out_pitch + q, f32x4{0.f, 0.f, 0.f, 0.f});
-            }
-          continue;
+      at.p0 = v / ct * kTile;
+      at.q0 = v % ct * kTile;
+      at.pend = min(j.N, at.p0 + kTile);
+      if (at.kend > at.k0) {
+        at.e = e;
+        at.mt = at.pend - at.p0 <= 128 ? 4 : 8;
+        return at;
+      }
+      if (!j.accumulate)  // no rows: zeros, or what was there
+        for (int i = threadIdx.x & 255; i < kTile * kTile / 4; i += 256) {  // (group 1 walks)
+          const int p = at.p0 + i / 64, q = at.q0 + i % 64 * 4;
+          if (p < j.N && q < j.D) put4(j, e * j.out_stride + p * j.out_pitch + q, f32x4{0.f, 0.f, 0.f, 0.f});
         }
-        if (at.pend - at.p0 <= 128) run(at, std::integral_constant<int, 4>{});
-        else run(at, std::integral_constant<int, 8>{});
-      }
-      pos -= cnt;
+      --step;  // this expert's next tile of this workgroup
     }
-  } else {
-    // four experts to a lane: how many row tiles each has, the sum over those before
-    __shared__ int s_tiles[256], s_upto[64];
-    int upto = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      int r0 = 0, r1 = 0;
-      if (4 * lane + k < j.E) expert_rows(j, 4 * lane + k, r0, r1);
-      const int tiles = (r1 - r0 + kTile - 1) / kTile;
-      if (wv == 0) s_tiles[4 * lane + k] = tiles;
-      upto += tiles;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(upto, d);
-      if (lane >= d) upto += v;
-    }
-    if (wv == 0) s_upto[lane] = upto;
-    const int total = __builtin_amdgcn_readlane(upto, 63) * ct;
-    __syncthreads();
-    const int u0 = (int)((int64_t)total * xcd / kXcds), u1 = (int)((int64_t)total * (xcd + 1) / kXcds);
-    for (int u = u0 + idx; u < u1; u += per) {
-      // the expert whose tiles u lies among
-      const int owner = __popcll(__ballot(s_upto[lane] * ct <= u));
-      int e = 4 * owner, base = owner ? s_upto[owner - 1] : 0, tiles = s_tiles[e];
-      while (u >= (base + tiles) * ct) {
-        base += tiles;
-        tiles = s_tiles[++e];
-      }
-      e = __builtin_amdgcn_readfirstlane(e);
-      base = __builtin_amdgcn_readfirstlane(base);
-      tiles = __builtin_amdgcn_readfirstlane(tiles);
-      int r0, r1;
-      expert_rows(j, e, r0, r1);
-      // tiles of one expert: bands of at most eight row tiles, in a band the row tiles of one column block
-      // after the other, so that workgroups of an XCD share rows and weights in its L2
-      const int v = u - base * ct, bands = (tiles + 7) / 8, bh = (tiles + bands - 1) / bands;
-      const int band = v / (bh * ct), h = min(bh, tiles - band * bh), w = v - band * bh * ct;
-      Place at;
-      at.e = e;
-      at.p0 = __builtin_amdgcn_readfirstlane(r0 + (band * bh + w % h) * kTile);
-      at.q0 = __builtin_amdgcn_readfirstlane(w / h * kTile);
-      at.pend = __builtin_amdgcn_readfirstlane(min(r1, at.p0 + kTile));
-      at.k0 = 0;
-      at.kend = j.D;
-      const int rows = at.pend - at.p0;
-      if (rows <= 64) run(at, std::integral_constant<int, 2>{});
-      else if (rows <= 128) run(at, std::integral_constant<int, 4>{});
-      else if (rows <= 192) run(at, std::integral_constant<int, 6>{});
-      else run(at, std::integral_constant<int, 8>{});
-    }
+    return at;
   }
-  wait_copies<0>();  // nothing lands in this LDS once it is another workgroup's
+};
+
+template <int MODE, int DT>
+__global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
+  constexpr bool kScaled = DT == MOE_FP8_E4M3;
+  using W = Walk<MODE == kWeightsGrad ? kWeightsGrad : kForward>;
+  __shared__ __attribute__((aligned(1024))) char pool[kPool];
+  __shared__ float scale[kScaled ? 1024 : 1], w_scale[kScaled ? 2 * kMaxBlocks : 1];
+  __shared__ int slots[MODE == kWeightsGrad ? 1 : 2 * 256];
+  __shared__ typename W::Table table;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ Place place[2];
+  const Lds lds = {pool, scale, w_scale, slots, place};
+
+  W walk(j, table);
+  if (wv >= 4) {
+    const Place first = walk.next(j);
+    if (first.e >= 0) find_rows<MODE>(j, first, slots, threadIdx.x - 256);
+    if (threadIdx.x == 256) place[0] = first;
+  }
+  __syncthreads();
+  Place at = load_place(place);
+  if (at.e < 0) return;
+  if (wv < 4) {
+    begin_any<MODE, DT>(j, at, lds, slots, wv, lane);
+    wait_copies<0>();
+  }
+  for (int par = 0; at.e >= 0; par ^= 1) {
+    auto run = [&](auto mt) {
+      if (wv < 4) at = tile<MODE, DT, mt(), 0>(j, at, walk, lds, par, wv, lane);
+      else at = tile<MODE, DT, mt(), 1>(j, at, walk, lds, par, wv - 4, lane);
+    };
+    const int mt = at.mt;
+    if (mt == 4) run(std::integral_constant<int, 4>{});
+    else if (MODE == kWeightsGrad || mt == 8) run(std::integral_constant<int, 8>{});
+    else if (mt == 2) run(std::integral_constant<int, MODE == kWeightsGrad ? 8 : 2>{});
+    else run(std::integral_constant<int, MODE == kWeightsGrad ? 8 : 6>{});
+  }
 }
 
-int run_tiles(const ProductJob& j, int dtype, int mode, int units, hipStream_t stream) {
-  const unsigned cus = (unsigned)units;
-  if (dtype == MOE_FP8_E4M3) return launch(tiles_kernel<kForward, MOE_FP8_E4M3>, cus, 512u, stream, j);
-  if (mode == kForward) return launch(tiles_kernel<kForward, MOE_BF16>, cus, 512u, stream, j);
-  if (mode == kRowsGrad) return launch(tiles_kernel<kRowsGrad, MOE_BF16>, cus, 512u, stream, j);
-  return launch(tiles_kernel<kWeightsGrad, MOE_BF16>, cus, 512u, stream, j);
+int run_tiles(const ProductJob& j, int dtype, int mode, int cus, hipStream_t stream) {
+  const unsigned grid = (unsigned)cus;
+  if (dtype == MOE_FP8_E4M3) return launch(tiles_kernel<kForward, MOE_FP8_E4M3>, grid, 512u, stream, j);
+  if (mode == kForward) return launch(tiles_kernel<kForward, MOE_BF16>, grid, 512u, stream, j);
+  if (mode == kRowsGrad) return launch(tiles_kernel<kRowsGrad, MOE_BF16>, grid, 512u, stream, j);
+  return launch(tiles_kernel<kWeightsGrad, MOE_BF16>, grid, 512u, stream, j);
 }
 
 }  // namespace moe
