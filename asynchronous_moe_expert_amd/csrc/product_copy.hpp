@@ -85,4 +85,53 @@ __device__ __forceinline__ void neighbours(u32x4& v) {
   }
 }
 
+// NB blocks of 64 columns of an operand whose rows lie across k: byte offsets of this lane's copies from row k0 of
+// the matrix, two copies to a block, of row() and of the row 32 further.  Columns past the end are read at others.
+template <int NB>
+struct Across {
+  uint32_t off[NB];
+  __device__ __forceinline__ void set(int wq, int lane, int col0, int cols, int64_t pitch, int es) {
+    const int k = row(wq, lane), f = ((k >> 1) & 1) | ((k >> 3) & 1) << 1, piece = (lane & 7) ^ (2 * f);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int first = col0 + 64 * b < cols ? col0 + 64 * b : col0 < cols ? col0 : 0;
+      off[b] = (uint32_t)(k * (int)pitch * es + (first + min(piece * 8, cols - 8 - first)) * es);
+    }
+  }
+  static __device__ __forceinline__ int row(int wq, int lane) { return 8 * wq + (lane >> 3); }
+  // step `step` of the contraction's rows 0 .. end - 1, which begin at base
+  __device__ __forceinline__ void copy(const char* base, int64_t pitch_bytes, uint32_t dst, int step, int end, int wq,
+                                       int lane) const {
+    const char* from = uniform_ptr(base + (int64_t)step * kStep * pitch_bytes);
+    const char* odd = uniform_ptr(from + 32 * pitch_bytes);
+    if ((step + 1) * kStep <= end) {
+      each<2 * NB>([&](auto c) { copy16<c() * 4096>(c() & 1 ? odd : from, off[c() >> 1], dst); });
+    } else {
+      const int k = step * kStep + row(wq, lane);
+      each<2 * NB>([&](auto c) {
+        const char* src = (c() & 1 ? odd : from) + off[c() >> 1];
+        copy16<c() * 4096>(k + 32 * (c() & 1) < end ? src : (const char*)&g_zeros, dst);
+      });
+    }
+  }
+};
+
+// Lanes 2 r and 2 r + 1 hold a 16-byte piece of the first 64 bytes (a) and of the second (b) of rows 2 r and 2 r + 1;
+// after it a is a piece of row 2 r and b of row 2 r + 1, of the first 64 bytes in even lanes and of the second in odd
+// ones, so that eight lanes store a line of 128 bytes at once.
+template <typename V>
+__device__ __forceinline__ void pair_rows(V& a, V& b, bool odd) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x, y;
+    __builtin_memcpy(&x, (const char*)&a + 4 * i, 4);
+    __builtin_memcpy(&y, (const char*)&b + 4 * i, 4);
+    const uint32_t got = dpp_u32<kDppXor1>(odd ? x : y);
+    x = odd ? got : x;
+    y = odd ? y : got;
+    __builtin_memcpy((char*)&a + 4 * i, &x, 4);
+    __builtin_memcpy((char*)&b + 4 * i, &y, 4);
+  }
+}
+
 }  // namespace moe

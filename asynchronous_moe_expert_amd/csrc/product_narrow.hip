@@ -240,36 +240,15 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(ProductJob j) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kRows = 16 * T::kMT;
   const int ct = (j.N + T::kQ - 1) / T::kQ;
-  // four experts to a lane: how many row tiles each has, the sum over those before
-  int tiles[4], upto = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int r0 = 0, r1 = 0;
-    if (4 * lane + k < j.E) expert_rows(j, 4 * lane + k, r0, r1);
-    tiles[k] = (r1 - r0 + kRows - 1) / kRows;
-    upto += tiles[k];
-  }
-  const int mine = upto;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int v = __shfl_up(upto, d);
-    if (lane >= d) upto += v;
-  }
-  const int total = __builtin_amdgcn_readlane(upto, 63) * ct;
+  const RowTiles<kRows> all(j, lane);
+  const int total = all.total() * ct;
   // an XCD's workgroups take a contiguous part of the tiles: an expert's row tiles of one column block after the
   // other, so that the weights of the second one are found in its L2
   const int xcd = blockIdx.x % 8, u0 = (int)((int64_t)total * xcd / 8), u1 = (int)((int64_t)total * (xcd + 1) / 8);
   const int u = u0 + (int)(blockIdx.x / 8);
   if (u >= u1) return;
-  const int owner = __popcll(__ballot(upto * ct <= u));
-  int base = __builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner), e = 4 * owner, n = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    n = __builtin_amdgcn_readlane(tiles[k], owner);
-    if (u < (base + n) * ct) break;
-    base += n;
-    ++e;
-  }
+  int e, base, n;
+  all.find(u, ct, e, base, n);
   int r0, r1;
   expert_rows(j, e, r0, r1);
   const int v = u - base * ct;

@@ -32,37 +32,6 @@ struct Tile {
   static constexpr int kP = MT / 2, kQ = 8, kScales = kScaled ? 1 : 0;
   static constexpr int kFirst = kQ + kP + kScales, kSecond = kP;
 };
-// NB blocks of 64 columns of an operand whose rows lie across k: byte offsets of this lane's copies from row k0 of
-// the matrix, two copies to a block, of row() and of the row 32 further.  Columns past the end are read at others.
-template <int NB>
-struct Across {
-  uint32_t off[NB];
-  __device__ __forceinline__ void set(int wq, int lane, int col0, int cols, int64_t pitch, int es) {
-    const int k = row(wq, lane), f = ((k >> 1) & 1) | ((k >> 3) & 1) << 1, piece = (lane & 7) ^ (2 * f);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int first = col0 + 64 * b < cols ? col0 + 64 * b : col0 < cols ? col0 : 0;
-      off[b] = (uint32_t)(k * (int)pitch * es + (first + min(piece * 8, cols - 8 - first)) * es);
-    }
-  }
-  static __device__ __forceinline__ int row(int wq, int lane) { return 8 * wq + (lane >> 3); }
-  // step `step` of the contraction's rows 0 .. end - 1, which begin at base
-  __device__ __forceinline__ void copy(const char* base, int64_t pitch_bytes, uint32_t dst, int step, int end, int wq,
-                                       int lane) const {
-    const char* from = uniform_ptr(base + (int64_t)step * kStep * pitch_bytes);
-    const char* odd = uniform_ptr(from + 32 * pitch_bytes);
-    if ((step + 1) * kStep <= end) {
-      each<2 * NB>([&](auto c) { copy16<c() * 4096>(c() & 1 ? odd : from, off[c() >> 1], dst); });
-    } else {
-      const int k = step * kStep + row(wq, lane);
-      each<2 * NB>([&](auto c) {
-        const char* src = (c() & 1 ? odd : from) + off[c() >> 1];
-        copy16<c() * 4096>(k + 32 * (c() & 1) < end ? src : (const char*)&g_zeros, dst);
-      });
-    }
-  }
-};
-
 // What a workgroup has in LDS: the stages (all of Q's, then P's), four steps of the rows' scales, the weights' scales
 // of the tile's two blocks of columns, and where the rows of this tile and the next come from.
 struct Lds {
@@ -370,7 +339,7 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
         }
     }
   };
-  auto multiply = [&](const char* ps, const float* ss) {
+  auto multiply = [&](const char* ps, const float* ss, auto&& meanwhile) {
     __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
     int p1 = 0;
@@ -378,6 +347,10 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
 #pragma unroll
     for (int a = 0; a < kHalf; ++a) {
       row(0, a);
+      if (a == 0) {  // issued while the matrix core works
+        __builtin_amdgcn_sched_barrier(0);
+        meanwhile();
+      }
       if constexpr (T::kPAlong) {
         read_p(ps, ss, kHalf, a, pr, p1);
       } else {
@@ -420,16 +393,19 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
         const char *ps = lds.pool + C::p_at(h), *qs = lds.pool + C::q_at(h);
         const float* ss = lds.scale + (s & 3) * 256;
         const bool more = s > 0 && s + S - 1 < steps;
-        if (more) c.first(j, at, lds, s + S - 1, wq, lane);
         read(ps, qs, ss, c.step_of(s));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) c.first(j, at, lds, s + S - 1, wq, lane);
         wait_lds();
         if (s >= S) {  // group 1's rows of step s
           if (more) wait_copies<(S - 2) * kBoth + T::kFirst>();
           else wait_copies<0>();
         }
         meet();
-        if (more) c.second(j, at, lds, s + S - 1, wq, lane);
-        multiply(ps, ss);
+        multiply(ps, ss, [&]() {
+          if (more) c.second(j, at, lds, s + S - 1, wq, lane);
+        });
         if (s + 1 >= S) {  // the rest of step s + 1
           if (more) wait_copies<(S - 2) * kBoth + T::kSecond>();
           else wait_copies<0>();
@@ -466,7 +442,7 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
         read(ps, qs, ss, i + h + turn < steps ? i + h + turn : i + h + turn - steps);
         wait_lds();
         meet();
-        multiply(ps, ss);
+        multiply(ps, ss, []() {});
         meet();
       }
     }
@@ -477,28 +453,54 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
     if (next.e >= 0) begin_any<MODE, DT>(j, next, lds, lds.slots + (par ^ 1) * 256, wq, lane);
   }
 
-  // ---- outputs
+  // ---- outputs, in whole lines of 128 bytes (but for forward fp32 ones and sums added to bf16).  A large gradient goes
+  // through the caches without staying: it would push out the rows that the next tiles read.  32 experts of 512 rows,
+  // 4096 x 4096, fp32 / bf16 out: 840 / 620 us with parts of lines, 794 / 690 with whole ones, 662 / 589 so.
   const int64_t out0 = MODE == kWeightsGrad ? at.e * j.out_stride : 0;
+  const bool odd = l16 & 1;
 #pragma unroll
   for (int a = 0; a < MT; ++a) {
-    const int p = at.p0 + G * 16 * MT + a * 16 + l16;
-    const int64_t at0 = out0 + p * j.out_pitch;
-    if (j.out_f32 || j.accumulate) {
+    const int row = at.p0 + G * 16 * MT + a * 16, p = row + l16, pe = row + (l16 & 14);
+    const int q0 = at.q0 + 64 * wq;
+    if (j.out_f32 && !T::kQAlong) {
+#pragma unroll
+      for (int b = 0; b < 4; b += 2) {
+        f32x4 u = acc[a][b], v = acc[a][b + 1];
+        pair_rows(u, v, odd);
+        const int q = q0 + 16 * b + (odd ? 16 : 0) + 4 * g;
+        if (MODE == kWeightsGrad && j.through) {
+          if (pe < at.pend && q < Qn) put4<true>(j, out0 + pe * j.out_pitch + q, u);
+          if (pe + 1 < at.pend && q < Qn) put4<true>(j, out0 + (pe + 1) * j.out_pitch + q, v);
+        } else {
+          if (pe < at.pend && q < Qn) put4(j, out0 + pe * j.out_pitch + q, u);
+          if (pe + 1 < at.pend && q < Qn) put4(j, out0 + (pe + 1) * j.out_pitch + q, v);
+        }
+      }
+    } else if (j.out_f32 || j.accumulate) {
       if (p >= at.pend) continue;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int q = at.q0 + 64 * wq + (T::kQAlong ? 32 * (b >> 1) + 8 * g + 4 * (b & 1) : 16 * b + 4 * g);
-        if (q < Qn) put4(j, at0 + q, acc[a][b]);
+        const int q = q0 + (T::kQAlong ? 32 * (b >> 1) + 8 * g + 4 * (b & 1) : 16 * b + 4 * g);
+        if (q < Qn) put4(j, out0 + p * j.out_pitch + q, acc[a][b]);
       }
     } else {
+      u32x4 v[2];
 #pragma unroll
-      for (int b = 0; b < 4; b += 2) {
-        u32x4 v = {pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]),
-                   pack_bf16x2(acc[a][b + 1][0], acc[a][b + 1][1]), pack_bf16x2(acc[a][b + 1][2], acc[a][b + 1][3])};
-        if constexpr (!T::kQAlong) neighbours(v);
-        const int q = at.q0 + 64 * wq + 16 * b + 8 * g;
-        if (p < at.pend && q < Qn) *reinterpret_cast<u32x4*>((uint16_t*)j.out + at0 + q) = v;
+      for (int b = 0; b < 2; ++b) {
+        v[b] = u32x4{pack_bf16x2(acc[a][2 * b][0], acc[a][2 * b][1]), pack_bf16x2(acc[a][2 * b][2], acc[a][2 * b][3]),
+                     pack_bf16x2(acc[a][2 * b + 1][0], acc[a][2 * b + 1][1]),
+                     pack_bf16x2(acc[a][2 * b + 1][2], acc[a][2 * b + 1][3])};
+        if constexpr (!T::kQAlong) neighbours(v[b]);
       }
+      pair_rows(v[0], v[1], odd);
+      const int q = q0 + (odd ? 32 : 0) + 8 * g;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (pe + b < at.pend && q < Qn) {
+          u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)j.out + out0 + (pe + b) * j.out_pitch + q);
+          if (MODE == kWeightsGrad && j.through) st<true>(o, v[b]);
+          else *o = v[b];
+        }
     }
   }
   // the copies have landed when no more is on its way than this wave's stores, which a whole tile has a known number of
@@ -620,26 +622,45 @@ struct Walk<kForward> {
   }
 };
 
-// Weights' gradient: each XCD takes an eighth of every expert's tiles, so that what it computes at a time reads the
-// same rows; the XCDs begin at different experts, so that not all of them store at the same time.
+// Weights' gradient: the tiles of the experts with most rows first, which take longest; each XCD takes an eighth of every
+// expert's, so that what it computes at a time reads the same rows; its workgroups take them in turns, back and forth.
 template <>
 struct Walk<kWeightsGrad> {
-  struct Table {};
-  int pos, step = 0;
-  __device__ __forceinline__ Walk(const ProductJob&, Table&) { pos = blockIdx.x / kXcds; }
+  struct Table {
+    int rows[256], order[256];
+  };
+  Table& t;
+  int rank = 0, before = 0, round = 0;  // before: this XCD's tiles of the experts before `rank`
+  __device__ __forceinline__ Walk(const ProductJob& j, Table& table) : t(table) {
+    const int i = threadIdx.x;
+    if (i < 256) {
+      int r0 = 0, r1 = 0;
+      if (i < j.E) expert_rows(j, i, r0, r1);
+      t.rows[i] = r1 - r0;
+    }
+    __syncthreads();
+    if (i < j.E) {
+      int at = 0;
+      for (int k = 0; k < j.E; ++k) at += t.rows[k] > t.rows[i] || (t.rows[k] == t.rows[i] && k < i);
+      t.order[at] = i;
+    }
+    __syncthreads();
+  }
   __device__ __forceinline__ Place next(const ProductJob& j) {
     Place at = {-1, 0, 0, 0, 0, 0, 0};
     const int ct = (j.D + kTile - 1) / kTile, V = (j.N + kTile - 1) / kTile * ct, xcd = blockIdx.x % kXcds;
-    const int per = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
-    for (; step < j.E; ++step) {
-      const int e = (step + xcd * j.E / kXcds) % j.E, x = (xcd + e) % kXcds;
+    const int idx = blockIdx.x / kXcds, per = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
+    int m = round * per + (round & 1 ? per - 1 - idx : idx);
+    ++round;
+    while (rank < j.E) {
+      const int e = __builtin_amdgcn_readfirstlane(t.order[rank]), x = (xcd + rank) % kXcds;
       const int v0 = (int)((int64_t)V * x / kXcds), cnt = (int)((int64_t)V * (x + 1) / kXcds) - v0;
-      if (pos >= cnt) {
-        pos -= cnt;
+      if (m >= before + cnt) {
+        before += cnt;
+        ++rank;
         continue;
       }
-      const int v = v0 + pos;
-      pos += per;
+      const int v = v0 + m - before;
       expert_rows(j, e, at.k0, at.kend);
       at.k0 = __builtin_amdgcn_readfirstlane(at.k0);
       at.kend = __builtin_amdgcn_readfirstlane(at.kend);
@@ -656,7 +677,8 @@ struct Walk<kWeightsGrad> {
           const int p = at.p0 + i / 64, q = at.q0 + i % 64 * 4;
           if (p < j.N && q < j.D) put4(j, e * j.out_stride + p * j.out_pitch + q, f32x4{0.f, 0.f, 0.f, 0.f});
         }
-      --step;  // this expert's next tile of this workgroup
+      m = round * per + (round & 1 ? per - 1 - idx : idx);
+      ++round;
     }
     return at;
   }

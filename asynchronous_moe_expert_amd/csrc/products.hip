@@ -6,138 +6,151 @@
 
 namespace moe {
 
-// ------------------------------------------------------------------------------------ any type, any size
-// 64 x 64 tiles in fp32: elements are widened (8-bit ones scaled) into LDS rows of 32 k, 36 apart so that
-// rows four apart begin in the same bank only every eighth, and multiplied by v_mfma_f32_16x16x4_f32.  Lane l
-// of a wave holds k = 4 (l / 16) + i in its i-th step: which k a step takes does not matter as long as both
-// operands agree.
-constexpr int kS = 64, kSK = 32, kSLd = 36;
+// ------------------------------------------------------------------------------------------------ fp32
+// S x S tiles by v_mfma_f32_16x16x4_f32, a quarter to each of four waves; the next 32 k are on their way to registers
+// while those in LDS are multiplied.  LDS rows are 32 k, 36 apart, so that four neighbouring ones begin in different
+// banks.  Lane l of a wave holds k = 4 (l / 16) + i in its i-th step of 16 k: which k a step takes does not matter as
+// long as both operands agree.  S = 128 where that makes two tiles for every CU, 64 otherwise.  Forward, us as 64 / 128:
+// 8 experts of 64 rows, 1024 x 1024: 33 / 84; 16 of 256: 88 / 89; 32 of 512: 332 / 314 (109 TFLOP/s); 1 of 4096 rows,
+// 4096 x 4096: 1226 / 1119 (123 of the 154 TFLOP/s that a library product reaches).  The matrix unit bounds the large
+// ones, the latency of one tile's k steps the small ones.
+constexpr int kSK = 32, kSLd = 36;
 
-template <int DT, int MODE>
-__global__ __launch_bounds__(256) void product_kernel(ProductJob j) {
-  __shared__ __attribute__((aligned(16))) float sp[kS * kSLd], sq[kS * kSLd];
-  constexpr int es = esize<DT>();
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, wp = (wv >> 1) * 32, wq = (wv & 1) * 32;
-  const int Q = MODE == kWeightsGrad ? j.D : j.N;
-  const int ct = (Q + kS - 1) / kS;
-  int e, p0, pend, k0 = 0, kend;
-  const int q0 = (int)(blockIdx.x % ct) * kS;
-  if constexpr (MODE == kWeightsGrad) {
-    const int rt = (j.N + kS - 1) / kS, b = blockIdx.x / ct;
-    e = b / rt;
-    p0 = (b - e * rt) * kS;
-    pend = j.N;
-    expert_rows(j, e, k0, kend);
-  } else {
-    int b = blockIdx.x / ct;
-    kend = j.D;
-    for (e = 0; e < j.E; ++e) {
-      expert_rows(j, e, p0, pend);
-      const int t = (pend - p0 + kS - 1) / kS;
-      if (b < t) break;
-      b -= t;
-    }
-    if (e == j.E) return;
-    p0 += b * kS;
-  }
-  // the thread's row (along k) or k and columns (across k) of each operand
-  const int ar = tid >> 2, ak = (tid & 3) * 8, bk = tid >> 3, bc = (tid & 7) * 8;
-  const char* prow = nullptr;
-  int64_t pslot = p0 + ar;
-  if constexpr (MODE != kWeightsGrad) {
-    if (p0 + ar < pend) {
-      if (j.row_slot) {
-        pslot = j.row_slot[p0 + ar];
-        if (pslot < 0 || pslot >= j.x_rows) {
-          atomicOr(j.err, MOE_ERR_SLOT_RANGE);
-          pslot = -1;
-        }
-      }
-      if (pslot >= 0) prow = (const char*)j.x + pslot * j.x_pitch * es;
-    }
-  }
-  const int kb = (j.D + 127) / 128;
-  f32x4 acc[2][2];
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int k = k0; k < kend; k += kSK) {
-    float f[8], g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = g[i] = 0.f;
-    Chunk<DT> c;
+template <int MODE, int S>
+__global__ __launch_bounds__(256) void product_f32_kernel(ProductJob j) {
+  __shared__ __attribute__((aligned(16))) float sp[S * kSLd], sq[S * kSLd];
+  constexpr int T = S / 32, C = S / 64;  // 16 x 16 tiles of a wave's edge; chunks of an operand to a thread
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, wp = (wv >> 1) * (S / 2), wq = (wv & 1) * (S / 2);
+  const int Q = MODE == kWeightsGrad ? j.D : j.N, ct = (Q + S - 1) / S;
+  const int rt = (j.N + S - 1) / S;  // weights' gradient
+  const RowTiles<S> all(j, lane);
+  const uint32_t total = (uint32_t)(MODE == kWeightsGrad ? j.E * rt : all.total()) * ct;
+  for (uint32_t u = blockIdx.x; u < total; u += gridDim.x) {
+    int e, p0, pend, k0 = 0, kend = j.D, q0;
     if constexpr (MODE == kWeightsGrad) {
-      if (k + bk < kend && p0 + bc < pend) {
-        c.load((const char*)j.dout + (int64_t)(k + bk) * j.dout_pitch * es, p0 + bc);
-        c.get(f);
-      }
-      if (k + bk < kend && q0 + bc < Q) {
-        c.load((const char*)j.x + (int64_t)(k + bk) * j.x_pitch * es, q0 + bc);
-        c.get(g);
-      }
+      const int b = u / ct;
+      e = b / rt;
+      p0 = (b - e * rt) * S;
+      pend = j.N;
+      q0 = (u - b * ct) * S;
+      expert_rows(j, e, k0, kend);
     } else {
-      if (prow && k + ak < kend) {
-        c.load(prow, k + ak);
-        c.get(f);
-        if constexpr (DT == MOE_FP8_E4M3) {
-          const float s = j.x_scale[pslot * kb + (k + ak) / 128];
+      int base, n;
+      all.find(u, ct, e, base, n);
+      expert_rows(j, e, p0, pend);
+      const int b = u / ct;
+      p0 += (b - base) * S;
+      q0 = (u - b * ct) * S;
+    }
+    // operands along k: a thread's rows are tid / 4 + 64 c, 8 k each; across k: its k is tid / 8, 8 columns + 64 c
+    const int ar = tid >> 2, ak = (tid & 3) * 8, bk = tid >> 3, bc = (tid & 7) * 8;
+    const float *prow[C] = {}, *w = nullptr;
+    if constexpr (MODE != kWeightsGrad) {
+      w = (const float*)j.w + e * j.w_stride;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= s;
-        }
-      }
-      const char* w = (const char*)j.w + e * j.w_stride * es;
-      if constexpr (MODE == kForward) {
-        if (q0 + ar < Q && k + ak < kend) {
-          c.load(w + (int64_t)(q0 + ar) * j.w_pitch * es, k + ak);
-          c.get(g);
-          if constexpr (DT == MOE_FP8_E4M3) {
-            const float s = j.w_scale[((int64_t)e * ((j.N + 127) / 128) + (q0 + ar) / 128) * kb + (k + ak) / 128];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] *= s;
+      for (int c = 0; c < C; ++c) {
+        const int row = p0 + ar + 64 * c;
+        if (row >= pend) continue;
+        int64_t slot = row;
+        if (j.row_slot) {
+          slot = j.row_slot[row];
+          if (slot < 0 || slot >= j.x_rows) {
+            atomicOr(j.err, MOE_ERR_SLOT_RANGE);
+            continue;
           }
         }
-      } else if (k + bk < kend && q0 + bc < Q) {
-        c.load(w + (int64_t)(k + bk) * j.w_pitch * es, q0 + bc);
-        c.get(g);
+        prow[c] = (const float*)j.x + slot * j.x_pitch;
       }
     }
-    __syncthreads();
+    float f[C][8], g[C][8];
+    auto fetch = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (MODE == kWeightsGrad) sp[(bc + i) * kSLd + bk] = f[i];
-      else sp[ar * kSLd + ak + i] = f[i];
-      if constexpr (MODE == kForward) sq[ar * kSLd + ak + i] = g[i];
-      else sq[(bc + i) * kSLd + bk] = g[i];
-    }
-    __syncthreads();
+      for (int c = 0; c < C; ++c) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      f32x4 p[2], q[2];
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        p[a] = *reinterpret_cast<const f32x4*>(sp + (wp + a * 16 + (lane & 15)) * kSLd + s * 16 + (lane >> 4) * 4);
-        q[a] = *reinterpret_cast<const f32x4*>(sq + (wq + a * 16 + (lane & 15)) * kSLd + s * 16 + (lane >> 4) * 4);
+        for (int i = 0; i < 8; ++i) f[c][i] = g[c][i] = 0.f;
+        Chunk<MOE_F32> x;
+        if constexpr (MODE == kWeightsGrad) {
+          if (k + bk < kend && p0 + bc + 64 * c < pend) {
+            x.load((const float*)j.dout + (k + bk) * j.dout_pitch, p0 + bc + 64 * c);
+            x.get(f[c]);
+          }
+          if (k + bk < kend && q0 + bc + 64 * c < Q) {
+            x.load((const float*)j.x + (k + bk) * j.x_pitch, q0 + bc + 64 * c);
+            x.get(g[c]);
+          }
+        } else {
+          if (prow[c] && k + ak < kend) {
+            x.load(prow[c], k + ak);
+            x.get(f[c]);
+          }
+          if constexpr (MODE == kForward) {
+            if (q0 + ar + 64 * c < Q && k + ak < kend) {
+              x.load(w + (q0 + ar + 64 * c) * j.w_pitch, k + ak);
+              x.get(g[c]);
+            }
+          } else if (k + bk < kend && q0 + bc + 64 * c < Q) {
+            x.load(w + (k + bk) * j.w_pitch, q0 + bc + 64 * c);
+            x.get(g[c]);
+          }
+        }
       }
+    };
+    f32x4 acc[T][T];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int a = 0; a < T; ++a)
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+      for (int c = 0; c < T; ++c) acc[a][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    fetch(k0);
+    for (int k = k0; k < kend; k += kSK) {
+      __syncthreads();
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(q[b][i], p[a][i], acc[a][b], 0, 0, 0);
+      for (int c = 0; c < C; ++c) {
+        if constexpr (MODE == kWeightsGrad) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sp[(bc + 64 * c + i) * kSLd + bk] = f[c][i];
+        } else {
+          float* o = sp + (ar + 64 * c) * kSLd + ak;
+          *reinterpret_cast<f32x4*>(o) = f32x4{f[c][0], f[c][1], f[c][2], f[c][3]};
+          *reinterpret_cast<f32x4*>(o + 4) = f32x4{f[c][4], f[c][5], f[c][6], f[c][7]};
+        }
+        if constexpr (MODE == kForward) {
+          float* o = sq + (ar + 64 * c) * kSLd + ak;
+          *reinterpret_cast<f32x4*>(o) = f32x4{g[c][0], g[c][1], g[c][2], g[c][3]};
+          *reinterpret_cast<f32x4*>(o + 4) = f32x4{g[c][4], g[c][5], g[c][6], g[c][7]};
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sq[(bc + 64 * c + i) * kSLd + bk] = g[c][i];
+        }
+      }
+      __syncthreads();
+      fetch(k + kSK);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        f32x4 p[T], q[T];
+#pragma unroll
+        for (int a = 0; a < T; ++a) {
+          p[a] = *reinterpret_cast<const f32x4*>(sp + (wp + a * 16 + (lane & 15)) * kSLd + s * 16 + (lane >> 4) * 4);
+          q[a] = *reinterpret_cast<const f32x4*>(sq + (wq + a * 16 + (lane & 15)) * kSLd + s * 16 + (lane >> 4) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int a = 0; a < T; ++a)
+#pragma unroll
+            for (int c = 0; c < T; ++c)
+              acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(q[c][i], p[a][i], acc[a][c], 0, 0, 0);
+      }
     }
-  }
+    if (MODE == kWeightsGrad && k0 == kend && j.accumulate) continue;  // no rows: what was there stays
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    const int p = p0 + wp + a * 16 + (lane & 15);
-    if (p >= pend) continue;
+    for (int a = 0; a < T; ++a) {
+      const int p = p0 + wp + a * 16 + (lane & 15);
+      if (p >= pend) continue;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int q = q0 + wq + b * 16 + (lane >> 4) * 4;
-      if (q >= Q) continue;
-      const int64_t at = (MODE == kWeightsGrad ? e * j.out_stride : 0) + p * j.out_pitch + q;
-      put4(j, at, acc[a][b]);
+      for (int c = 0; c < T; ++c) {
+        const int q = q0 + wq + c * 16 + (lane >> 4) * 4;
+        if (q < Q) put4(j, (MODE == kWeightsGrad ? e * j.out_stride : 0) + p * j.out_pitch + q, acc[a][c]);
+      }
     }
   }
 }
@@ -157,18 +170,31 @@ static int compute_units() {
   return cus;
 }
 
-template <int DT, int MODE>
-static int run_product(const ProductJob& j, hipStream_t stream) {
-  if (DT != MOE_F32) {
-    const bool few = MODE != kWeightsGrad && j.n <= 64 * (int64_t)j.E;
-    const int cus = compute_units();
-    if (!cus) return MOE_ELAUNCH;
-    return few ? run_narrow(j, DT, MODE, cus, stream) : run_tiles(j, DT, MODE, cus, stream);
-  }
-  const int64_t ct = ((MODE == kWeightsGrad ? j.D : j.N) + kS - 1) / kS;
-  const int64_t rt = MODE == kWeightsGrad ? (int64_t)j.E * ((j.N + kS - 1) / kS) : j.n / kS + (j.n < j.E ? j.n : j.E);
-  if (rt * ct > (1 << 24) - 1) return MOE_EINVAL_SIZE;
-  return launch(product_kernel<DT, MODE>, (unsigned)(rt * ct), 256u, stream, j);
+template <int MODE, int S>
+static int launch_f32(const ProductJob& j, int64_t tiles, hipStream_t stream) {
+  if (tiles > INT32_MAX) return MOE_EINVAL_SIZE;
+  return launch(product_f32_kernel<MODE, S>, grid_of(tiles), 256u, stream, j);
+}
+
+template <int MODE>
+static int run_f32(const ProductJob& j, int cus, hipStream_t stream) {
+  const auto tiles = [&](int s) {  // as many as there can be
+    const int64_t ct = ((MODE == kWeightsGrad ? j.D : j.N) + s - 1) / s;
+    return ct * (MODE == kWeightsGrad ? (int64_t)j.E * ((j.N + s - 1) / s) : j.n / s + (j.n < j.E ? j.n : j.E));
+  };
+  return tiles(128) >= 2 * cus ? launch_f32<MODE, 128>(j, tiles(128), stream) : launch_f32<MODE, 64>(j, tiles(64), stream);
+}
+
+// Up to 64 rows of an expert on average a product is a pass over its weights.  32 experts, 4096 x 4096 bf16, us as
+// tiles / narrow, forward: 4 rows each 187 / 159, 32 187 / 164, 64 193 / 177, 96 211 / 246, 128 216 / 259.  The rows'
+// gradient: 186 / 188, 188 / 194, 190 / 203, 198 / 261, 207 / 277; it goes by the same rule.
+template <int MODE>
+static int run_product(const ProductJob& j, int dtype, hipStream_t stream) {
+  const int cus = compute_units();
+  if (!cus) return MOE_ELAUNCH;
+  if (dtype == MOE_F32) return run_f32<MODE>(j, cus, stream);
+  if (MODE != kWeightsGrad && j.n <= 64 * (int64_t)j.E) return run_narrow(j, dtype, MODE, cus, stream);
+  return run_tiles(j, dtype, MODE, cus, stream);
 }
 
 // a matrix of `rows` rows of `cols` elements, one of several `stride` apart
@@ -210,10 +236,7 @@ extern "C" int moe_expert_matmul(const moe_expert_matmul_args* a, hipStream_t st
   j.x = a->x; j.x_rows = x_rows; j.x_pitch = a->x_pitch; j.row_slot = a->row_slot; j.x_scale = a->x_scale;
   j.w = a->w; j.w_pitch = a->w_pitch; j.w_stride = a->E_loc > 1 ? a->w_stride : 0; j.w_scale = a->w_scale;
   j.out = a->out; j.out_pitch = a->out_pitch; j.out_f32 = a->out_dtype == MOE_F32; j.err = a->err;
-  if (fp8) return run_product<MOE_FP8_E4M3, kForward>(j, stream);
-  if (a->dtype == MOE_F32)
-    return a->w_transposed ? run_product<MOE_F32, kRowsGrad>(j, stream) : run_product<MOE_F32, kForward>(j, stream);
-  return a->w_transposed ? run_product<MOE_BF16, kRowsGrad>(j, stream) : run_product<MOE_BF16, kForward>(j, stream);
+  return a->w_transposed ? run_product<kRowsGrad>(j, a->dtype, stream) : run_product<kForward>(j, a->dtype, stream);
 }
 
 extern "C" int moe_expert_matmul_backward(const moe_expert_matmul_backward_args* a, hipStream_t stream) {
@@ -237,5 +260,6 @@ extern "C" int moe_expert_matmul_backward(const moe_expert_matmul_backward_args*
   j.x = a->x; j.x_rows = a->n; j.x_pitch = a->x_pitch; j.dout = a->dout; j.dout_pitch = a->dout_pitch;
   j.out = a->dw; j.out_pitch = a->dw_pitch; j.out_stride = a->E_loc > 1 ? a->dw_stride : 0;
   j.out_f32 = a->dw_dtype == MOE_F32; j.accumulate = a->accumulate;
-  return a->dtype == MOE_F32 ? run_product<MOE_F32, kWeightsGrad>(j, stream) : run_product<MOE_BF16, kWeightsGrad>(j, stream);
+  j.through = (int64_t)a->E_loc * a->N * a->D * dtype_size(a->dw_dtype) >= (96ll << 20);  // (home.hpp: what stays near)
+  return run_product<kWeightsGrad>(j, a->dtype, stream);
 }

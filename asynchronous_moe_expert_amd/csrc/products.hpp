@@ -21,7 +21,7 @@ struct ProductJob {
   const int32_t* row_slot;
   const float *x_scale, *w_scale;
   void* out;
-  int out_f32, accumulate;
+  int out_f32, accumulate, through;  // through: outputs past the caches
   uint32_t* err;
 };
 
@@ -34,12 +34,51 @@ __device__ __forceinline__ void expert_rows(const ProductJob& j, int e, int& r0,
   r1 = max(r0, min(j.offsets[e + 1], j.n));
 }
 
+// How many tiles of S rows each expert has, four experts to a lane of a whole wave, and the sums up to them: one round
+// trip to memory for all offsets.
+template <int S>
+struct RowTiles {
+  int tiles[4], mine = 0, upto;
+
+  __device__ __forceinline__ RowTiles(const ProductJob& j, int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      int r0 = 0, r1 = 0;
+      if (4 * lane + k < j.E) expert_rows(j, 4 * lane + k, r0, r1);
+      tiles[k] = (r1 - r0 + S - 1) / S;
+      mine += tiles[k];
+    }
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+  }
+  __device__ __forceinline__ int total() const { return __builtin_amdgcn_readlane(upto, 63); }
+  // The expert of tile u < total() * ct, where a tile of rows makes ct tiles: the row tiles before it, and its own.
+  __device__ __forceinline__ void find(int u, int ct, int& e, int& base, int& n) const {
+    const int owner = __popcll(__ballot(upto * ct <= u));
+    base = __builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner);
+    e = 4 * owner;
+    n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      n = __builtin_amdgcn_readlane(tiles[k], owner);
+      if (u < (base + n) * ct) break;
+      base += n;
+      ++e;
+    }
+  }
+};
+
 // Four neighbouring elements of an output row.
+template <bool NT = false>
 __device__ __forceinline__ void put4(const ProductJob& j, int64_t at, f32x4 v) {
   if (j.out_f32) {
     f32x4* o = reinterpret_cast<f32x4*>((float*)j.out + at);
     if (j.accumulate) v += *o;
-    *o = v;
+    st<NT>(o, v);
   } else {
     u32x2* o = reinterpret_cast<u32x2*>((uint16_t*)j.out + at);
     if (j.accumulate) {
@@ -49,7 +88,7 @@ __device__ __forceinline__ void put4(const ProductJob& j, int64_t at, f32x4 v) {
       v[2] += __uint_as_float(old[1] << 16);
       v[3] += __uint_as_float(old[1] & 0xffff0000u);
     }
-    *o = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    st<NT>(o, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
   }
 }
 

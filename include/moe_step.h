@@ -611,7 +611,8 @@ int moe_residual_norm_backward(const moe_residual_norm_backward_args* args, hipS
  *   - offsets is read on the device (moe_sort_rows or moe_assemble gives it); expert e has the rows
  *     offsets[e] .. offsets[e + 1] - 1.  n is an upper bound on offsets[E_loc]: rows from offsets[E_loc] on are
  *     neither read nor written.  offsets that are not ascending within [0, n] are cut to that range, an
- *     expert whose end lies before its begin having no rows.
+ *     expert whose end lies before its begin having no rows; where two experts then share rows, each element of
+ *     their outputs is that of one of them.
  *   - N and D (columns of the outputs, of the inputs) are multiples of 8 (D of 16 for fp8 rows) and at most
  *     65536; every row of a matrix begins at a multiple of 16 bytes, at most 16 MiB after the one before.
  *     1 <= E_loc <= 256.
