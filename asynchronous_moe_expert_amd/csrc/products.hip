@@ -170,19 +170,14 @@ static int compute_units() {
   return cus;
 }
 
-template <int MODE, int S>
-static int launch_f32(const ProductJob& j, int64_t tiles, hipStream_t stream) {
-  if (tiles > INT32_MAX) return MOE_EINVAL_SIZE;
-  return launch(product_f32_kernel<MODE, S>, grid_of(tiles), 256u, stream, j);
-}
-
 template <int MODE>
 static int run_f32(const ProductJob& j, int cus, hipStream_t stream) {
-  const auto tiles = [&](int s) {  // as many as there can be
+  const auto tiles = [&](int s) {  // as many as there can be: under 2^29 with n <= 2^24 and sides <= 2^16
     const int64_t ct = ((MODE == kWeightsGrad ? j.D : j.N) + s - 1) / s;
     return ct * (MODE == kWeightsGrad ? (int64_t)j.E * ((j.N + s - 1) / s) : j.n / s + (j.n < j.E ? j.n : j.E));
   };
-  return tiles(128) >= 2 * cus ? launch_f32<MODE, 128>(j, tiles(128), stream) : launch_f32<MODE, 64>(j, tiles(64), stream);
+  if (tiles(128) >= 2 * cus) return launch(product_f32_kernel<MODE, 128>, grid_of(tiles(128)), 256u, stream, j);
+  return launch(product_f32_kernel<MODE, 64>, grid_of(tiles(64)), 256u, stream, j);
 }
 
 // Up to 64 rows of an expert on average a product is a pass over its weights.  32 experts, 4096 x 4096 bf16, us as
