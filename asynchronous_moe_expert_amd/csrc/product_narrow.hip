@@ -21,7 +21,7 @@ struct Narrow {
   static constexpr int kWaves = NW, kStages = S;
   static constexpr int kQ = 32 * NW / WK;         // columns
   static constexpr int kMT = WK == 1 ? 4 : 2;     // 16 rows each, at most
-  static constexpr bool kAlong = MODE == kForward, kScaled = DT == MOE_FP8_E4M3;
+  static constexpr bool kAlong = MODE == kForward, kScaled = esize<DT>() == 1;
   static constexpr int kQBytes = 4096 * NW;
   static constexpr int kStage = kQBytes + WK * kMT * 2048;  // bytes: Q, then P
   static_assert(kAlong || NW == 4, "blocks of 64 columns are shared out among four waves");
@@ -158,7 +158,7 @@ __device__ __forceinline__ void narrow_tile(const ProductJob& j, const Place& at
         for (int b = 0; b < 2; ++b) {
           i32x8 w;
           __builtin_memcpy(&w, &qf[b][0], 32);
-          const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, p, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+          const f32x4 v = dot128<DT>(w, p);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(v[i], s, acc[a][b][i]);
         }
@@ -312,7 +312,8 @@ static int choose_narrow(const ProductJob& j, int64_t cus, hipStream_t stream) {
 }
 
 int run_narrow(const ProductJob& j, int dtype, int mode, int cus, hipStream_t stream) {
-  if (dtype == MOE_FP8_E4M3) return choose_narrow<kForward, MOE_FP8_E4M3>(j, cus, stream);
+  if (dtype == MOE_FP8_E4M3)
+    return j.out_f32 ? choose_narrow<kForward, kFp8Wide>(j, cus, stream) : choose_narrow<kForward, MOE_FP8_E4M3>(j, cus, stream);
   if (mode == kRowsGrad) return choose_narrow<kRowsGrad, MOE_BF16>(j, cus, stream);
   return choose_narrow<kForward, MOE_BF16>(j, cus, stream);
 }

@@ -1,5 +1,5 @@
 // The experts' products on large tiles: 256 x 256 of C, bf16 (v_mfma_f32_16x16x32_bf16) or 8 bits
-// (v_mfma_f32_16x16x128_f8f6f4 with fp32 scales), operands copied straight into LDS.
+// (v_mfma_f32_16x16x128_f8f6f4 with fp32 scales; for fp32 outputs of 8-bit operands bf16 again: dot128), operands copied straight into LDS.
 #include <type_traits>
 
 #include "product_copy.hpp"
@@ -23,7 +23,7 @@ template <int MODE, int DT, int MT>
 struct Tile {
   static constexpr int es = esize<DT>();
   static constexpr bool kPAlong = MODE != kWeightsGrad, kQAlong = MODE == kForward;
-  static constexpr bool kScaled = DT == MOE_FP8_E4M3;
+  static constexpr bool kScaled = esize<DT>() == 1;
   static constexpr int kHalf = MT / 2;
   static constexpr int kStages = MT <= 4 ? 3 : 2;  // steps in LDS
   static constexpr int kStageP = 32 * MT * 128;    // bytes of P in one, half for each group; Q has kStageQ
@@ -315,7 +315,7 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
       if (b < 4) {
         i32x8 q;
         __builtin_memcpy(&q, &qf[b][0], 32);
-        v[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, p, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+        v[b] = dot128<DT>(q, p);
       }
       if (b >= 2) {
 #pragma unroll
@@ -686,7 +686,7 @@ struct Walk<kWeightsGrad> {
 
 template <int MODE, int DT>
 __global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
-  constexpr bool kScaled = DT == MOE_FP8_E4M3;
+  constexpr bool kScaled = esize<DT>() == 1;
   using W = Walk<MODE == kWeightsGrad ? kWeightsGrad : kForward>;
   __shared__ __attribute__((aligned(1024))) char pool[kPool];
   __shared__ float scale[kScaled ? 1024 : 1], w_scale[kScaled ? 2 * kMaxBlocks : 1];
@@ -724,7 +724,9 @@ __global__ __launch_bounds__(512) void tiles_kernel(ProductJob j) {
 
 int run_tiles(const ProductJob& j, int dtype, int mode, int cus, hipStream_t stream) {
   const unsigned grid = (unsigned)cus;
-  if (dtype == MOE_FP8_E4M3) return launch(tiles_kernel<kForward, MOE_FP8_E4M3>, grid, 512u, stream, j);
+  if (dtype == MOE_FP8_E4M3)
+    return j.out_f32 ? launch(tiles_kernel<kForward, kFp8Wide>, grid, 512u, stream, j)
+                     : launch(tiles_kernel<kForward, MOE_FP8_E4M3>, grid, 512u, stream, j);
   if (mode == kForward) return launch(tiles_kernel<kForward, MOE_BF16>, grid, 512u, stream, j);
   if (mode == kRowsGrad) return launch(tiles_kernel<kRowsGrad, MOE_BF16>, grid, 512u, stream, j);
   return launch(tiles_kernel<kWeightsGrad, MOE_BF16>, grid, 512u, stream, j);

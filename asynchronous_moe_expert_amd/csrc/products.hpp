@@ -25,6 +25,8 @@ struct ProductJob {
   uint32_t* err;
 };
 
+constexpr int kFp8Wide = 16;  // 8-bit codes, widened to bf16 where they are multiplied (dot128)
+
 template <int DT>
 constexpr int esize() { return DT == MOE_F32 ? 4 : DT == MOE_BF16 ? 2 : 1; }
 

@@ -370,3 +370,24 @@ def test_no_tokens_and_rows_behind_the_last():
             h = torch.full((n, 32), -7.0, dtype=dtype, device="cuda")
             M.moe_swiglu(x, h, count=offsets_of(sizes)[2:])
             assert bool((h[sum(sizes):] == -7).all())
+
+
+@pytest.mark.parametrize("rows", [3, 40, 200, 700])
+@pytest.mark.parametrize("D", [16, 80, 128])
+def test_sums_of_8_bit_products_are_fp32(rows, D):
+    """Codes +-(8 .. 15) 2^(e - 3), e from -3 to 1, are multiples of 2^-6 below 4: products are multiples of 2^-12 and
+    128 of them stay below 2^11, so that fp32 sums in any order are exact, however far the products lie apart."""
+    print("8-bit sums", rows, D, flush=True)
+    g, E, N = seeded(rows + D), 3, 264
+
+    def codes(*shape):
+        m = torch.randint(8, 16, shape, generator=g, device="cuda") * (torch.randint(0, 2, shape, generator=g, device="cuda") * 2 - 1)
+        return m * 2.0 ** (torch.randint(-3, 2, shape, generator=g, device="cuda") - 3)
+
+    sizes = [rows, 0, rows // 2 + 1]
+    x, w = codes(sum(sizes), D), codes(E, N, D)
+    assert torch.equal(x.to(FP8).float(), x) and torch.equal(w.to(FP8).float(), w)
+    out = torch.full((sum(sizes), N), float("nan"), device="cuda")
+    M.moe_expert_matmul(x.to(FP8), w.to(FP8), offsets_of(sizes), out, x_scale=torch.ones(sum(sizes), 1, device="cuda"),
+                        w_scale=torch.ones(E, 3, 1, device="cuda"))
+    same(out, torch.cat([x[a:b].double() @ w[e].double().t() for e, a, b in each(sizes)]), "sums")
