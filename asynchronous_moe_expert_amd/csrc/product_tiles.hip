@@ -1,5 +1,13 @@
 // The experts' products on large tiles: 256 x 256 of C, bf16 (v_mfma_f32_16x16x32_bf16) or 8 bits
-// (v_mfma_f32_16x16x128_f8f6f4 with fp32 scales; for fp32 outputs of 8-bit operands bf16 again: dot128), operands copied straight into LDS.
+// (v_mfma_f32_16x16x128_f8f6f4 with fp32 scales; for fp32 outputs of 8-bit operands bf16 again: dot128), operands
+// copied straight into LDS.
+//
+// Two groups of four waves take half of a tile's rows each and change places: while one multiplies, the other reads
+// its next fragments; group 0 makes all copies, group 1 finds tiles and rows, so that only one waits for memory.
+// 256 x 256 is the most that two stages in LDS and the accumulators in registers allow; smaller tiles read more from
+// L2 for each product.  Reached, 32 experts of 512 rows, 4096 x 4096: forward 484 to 488 us (1.13 PFLOP/s), rows' gradient 488,
+// 8 bits 350 (1.57); 8192 rows of one expert, 4096 x 8192: 390 (1.41, what a library product reaches) and 8 bits 262
+// (2.1).  With few rows an expert the weights' bytes bound it, with uneven ones the last tiles.
 #include <type_traits>
 
 #include "product_copy.hpp"
@@ -208,8 +216,7 @@ __device__ __forceinline__ void begin_any(const ProductJob& j, const Place& at, 
   }
 }
 
-// Where the next tile's rows come from, and a scale for each block of 128 columns and 128 k of this one: group 1's
-// part, which waits for nothing else in memory.
+// Where the next tile's rows come from: group 1's part, which waits for nothing else in memory.
 template <int MODE>
 __device__ __forceinline__ void find_rows(const ProductJob& j, const Place& at, int* slots, int i) {
   if constexpr (MODE != kWeightsGrad) {
@@ -453,9 +460,9 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
     if (next.e >= 0) begin_any<MODE, DT>(j, next, lds, lds.slots + (par ^ 1) * 256, wq, lane);
   }
 
-  // ---- outputs, in whole lines of 128 bytes (but for forward fp32 ones and sums added to bf16).  A large gradient goes
-  // through the caches without staying: it would push out the rows that the next tiles read.  32 experts of 512 rows,
-  // 4096 x 4096, fp32 / bf16 out: 840 / 620 us with parts of lines, 794 / 690 with whole ones, 662 / 589 so.
+  // ---- outputs, in whole lines of 128 bytes (but for forward fp32 ones and sums added to bf16).  A large fp32
+  // gradient goes through the caches without staying: it would push out the rows that the next tiles read.  32 experts
+  // of 512 rows, 4096 x 4096: 806 us through the caches, 673 so (bf16: 691 either way).
   const int64_t out0 = MODE == kWeightsGrad ? at.e * j.out_stride : 0;
   const bool odd = l16 & 1;
 #pragma unroll
@@ -498,8 +505,7 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
       for (int b = 0; b < 2; ++b)
         if (pe + b < at.pend && q < Qn) {
           u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)j.out + out0 + (pe + b) * j.out_pitch + q);
-          if (MODE == kWeightsGrad && j.through) st<true>(o, v[b]);
-          else *o = v[b];
+          *o = v[b];
         }
     }
   }

