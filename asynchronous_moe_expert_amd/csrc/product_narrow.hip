@@ -14,8 +14,8 @@ namespace moe {
 //           once; run_narrow chooses the NW that leaves the fewest CUs idle;
 //   WK = 4: 32 columns, a step is four times as long, each wave takes its quarter and the waves' sums are added at
 //           the end: for calls that would leave most CUs idle.
-// Fragments lie in LDS as the tiles' do (product_tiles.hip).  256 rows of 8 experts, 5760 x 2880: 44 us in bf16 (the
-// weights at 6.1 TB/s), 33 in 8 bits (4.1: rows of 2880 bytes, whose steps are parts of two lines each); 128 experts
+// Fragments lie in LDS as the tiles' do (product_tiles.hip).  256 rows of 8 experts, 5760 x 2880: 45 us in bf16 (the
+// weights at 6.0 TB/s), 34 in 8 bits (4.0: rows of 2880 bytes, whose steps are parts of two lines each); 128 experts
 // of two rows, 2880 x 2880 bf16: 352 (6.0).
 template <int MODE, int DT, int WK, int NW, int S>
 struct Narrow {
@@ -247,37 +247,40 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(ProductJob j) {
   // an XCD's workgroups take a contiguous part of the tiles: an expert's row tiles of one column block after the
   // other, so that the weights of the second one are found in its L2
   const int xcd = blockIdx.x % 8, u0 = (int)((int64_t)total * xcd / 8), u1 = (int)((int64_t)total * (xcd + 1) / 8);
-  const int u = u0 + (int)(blockIdx.x / 8);
-  if (u >= u1) return;
-  int e, base, n;
-  all.find(u, ct, e, base, n);
-  int r0, r1;
-  expert_rows(j, e, r0, r1);
-  const int v = u - base * ct;
-  Place at;
-  at.e = e;
-  at.p0 = __builtin_amdgcn_readfirstlane(r0 + v % n * kRows);
-  at.q0 = v / n * T::kQ;
-  at.pend = __builtin_amdgcn_readfirstlane(min(r1, at.p0 + kRows));
-  at.k0 = 0;
-  at.kend = j.D;
-  if constexpr (T::kScaled) {  // the scales of the one block of columns, or of the two that the columns lie in
-    const int kb = (j.D + 127) / 128, nb = (j.N + 127) / 128;
+  // the grid has a workgroup for every tile but where offsets give rows to several experts (without the loop such tiles
+  // would be left out; 256 rows of 8 experts, 5760 x 2880: 44 us without, 45 with it)
+  for (int u = u0 + (int)(blockIdx.x / 8); u < u1; u += (int)(gridDim.x / 8)) {
+    if (u >= u0 + (int)(gridDim.x / 8)) __syncthreads();  // the tile before is out of LDS
+    int e, base, n;
+    all.find(u, ct, e, base, n);
+    int r0, r1;
+    expert_rows(j, e, r0, r1);
+    const int v = u - base * ct;
+    Place at;
+    at.e = e;
+    at.p0 = __builtin_amdgcn_readfirstlane(r0 + v % n * kRows);
+    at.q0 = v / n * T::kQ;
+    at.pend = __builtin_amdgcn_readfirstlane(min(r1, at.p0 + kRows));
+    at.k0 = 0;
+    at.kend = j.D;
+    if constexpr (T::kScaled) {  // the scales of the one block of columns, or of the two that the columns lie in
+      const int kb = (j.D + 127) / 128, nb = (j.N + 127) / 128;
 #pragma unroll
-    for (int b = 0; b < (128 % T::kQ ? 2 : 1); ++b) {
-      const float* from = j.w_scale + ((int64_t)e * nb + min((at.q0 >> 7) + b, nb - 1)) * kb;
-      for (int k = threadIdx.x; k < (kb + WK - 1) / WK * WK; k += 64 * NW)  // (quarters past the end: times 0)
-        wsc[b * kMaxBlocks + k] = k < kb ? from[k] : 0.f;
+      for (int b = 0; b < (128 % T::kQ ? 2 : 1); ++b) {
+        const float* from = j.w_scale + ((int64_t)e * nb + min((at.q0 >> 7) + b, nb - 1)) * kb;
+        for (int k = threadIdx.x; k < (kb + WK - 1) / WK * WK; k += 64 * NW)  // (quarters past the end: times 0)
+          wsc[b * kMaxBlocks + k] = k < kb ? from[k] : 0.f;
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    // Weights that no other workgroup reads pass through the caches without staying (256 rows of 8 experts, 5760 x 2880
+    // bf16 from HBM: 50 us with cached copies, 44 so), unless a step's 128 bytes of a row are parts of two lines, which
+    // the next step wants again (the same in 8 bits, rows of 2880 bytes: 31 us cached, 33 so).
+    const bool once = n == 1 && (j.w_pitch * T::es) % 128 == 0 && (j.w_stride * T::es) % 128 == 0 && ((uint64_t)j.w & 127) == 0;
+    const int rows = at.pend - at.p0;
+    if (rows <= kRows / 2) narrow_tile<T, MODE, DT, WK, T::kMT / 2>(j, at, ring, scales, wsc, wv, lane, once);
+    else narrow_tile<T, MODE, DT, WK, T::kMT>(j, at, ring, scales, wsc, wv, lane, once);
   }
-  // Weights that no other workgroup reads pass through the caches without staying (256 rows of 8 experts, 5760 x 2880
-  // bf16 from HBM: 50 us with cached copies, 44 so), unless a step's 128 bytes of a row are parts of two lines, which
-  // the next step wants again (the same in 8 bits, rows of 2880 bytes: 31 us cached, 33 so).
-  const bool once = n == 1 && (j.w_pitch * T::es) % 128 == 0 && (j.w_stride * T::es) % 128 == 0 && ((uint64_t)j.w & 127) == 0;
-  const int rows = at.pend - at.p0;
-  if (rows <= kRows / 2) narrow_tile<T, MODE, DT, WK, T::kMT / 2>(j, at, ring, scales, wsc, wv, lane, once);
-  else narrow_tile<T, MODE, DT, WK, T::kMT>(j, at, ring, scales, wsc, wv, lane, once);
 }
 
 template <int MODE, int DT, int WK, int NW, int S>

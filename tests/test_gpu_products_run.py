@@ -391,3 +391,25 @@ def test_sums_of_8_bit_products_are_fp32(rows, D):
     M.moe_expert_matmul(x.to(FP8), w.to(FP8), offsets_of(sizes), out, x_scale=torch.ones(sum(sizes), 1, device="cuda"),
                         w_scale=torch.ones(E, 3, 1, device="cuda"))
     same(out, torch.cat([x[a:b].double() @ w[e].double().t() for e, a, b in each(sizes)]), "sums")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("E,n", [(64, 4000), (2, 3), (8, 900)])
+def test_rows_of_many_experts_at_once(kind, E, n):
+    """offsets 0, n, 0, n, ..: every other expert has all rows, more tiles than any disjoint spans make.  The experts'
+    weights are the same, so that it does not matter whose product a row gets."""
+    dtype = {"f32": F32, "bf16": BF16, "fp8": FP8}[kind]
+    print("shared rows", kind, E, n, flush=True)
+    g, N, D = seeded(E), 264, 144
+    offsets = torch.tensor([0, n] * (E // 2) + [0], dtype=I32, device="cuda")
+    x, one = whole(g, n, D), whole(g, 1, N, D)
+    w = one.expand(E, N, D).contiguous().to(dtype)
+    out = torch.full((n, N), float("nan"), device="cuda")
+    scales = dict(x_scale=torch.ones(n, 2, device="cuda"), w_scale=torch.ones(E, 3, 2, device="cuda")) if kind == "fp8" else {}
+    M.moe_expert_matmul(x.to(dtype), w, offsets, out, **scales)
+    same(out, x.double() @ one[0].double().t(), "forward")
+    if kind == "fp8":
+        return
+    dx, d = torch.full((n, D), float("nan"), device="cuda"), whole(g, n, N)
+    M.moe_expert_matmul(d.to(dtype), w, offsets, dx, transposed=True)
+    same(dx, d.double() @ one[0].double(), "rows' gradient")
