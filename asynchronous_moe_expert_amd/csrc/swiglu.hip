@@ -33,13 +33,14 @@ struct SwigluJob {
 constexpr int kSwigluT = 512;  // threads at most
 
 // A row's chunks of eight columns lie on tpr threads (a multiple of 16, so that a scale's columns are a run
-// of lanes), `many` short rows at a time in a workgroup.  Bound by memory: 16384 rows of 2 x 2048 bf16 to 8 bits with a
+// of lanes), `many` short rows at a time in a workgroup.  A chunk has one owner: the gradient may lie where its inputs
+// do, so no other thread may read them.  Bound by memory: 16384 rows of 2 x 2048 bf16 to 8 bits with a
 // scale per 128 take 34 us (5.0 TB/s), as many with the gradients and h 61 (6.6); 256 rows of 2 x 2880 are a launch, 3.9.
 template <int XT, int OT, int S>
 __global__ __launch_bounds__(kSwigluT) void swiglu_kernel(SwigluJob j) {
   const int rows = j.count ? min(j.n, max(*j.count, 0)) : j.n;
   const int sub = j.many > 1 ? (int)threadIdx.x / j.tpr : 0, lt = (int)threadIdx.x - sub * j.tpr;
-  if (sub >= j.many) return;
+  if (sub >= j.many || lt >= j.tpr) return;  // (workgroups are whole waves, tpr is whole runs of 16)
   constexpr int xs = XT == MOE_F32 ? 4 : 2, os = OT == MOE_F32 ? 4 : OT == MOE_BF16 ? 2 : 1;
   for (int64_t t = (int64_t)blockIdx.x * j.many + sub; t < rows; t += (int64_t)gridDim.x * j.many) {
     const char* gu = (const char*)j.gu + t * j.gu_pitch * xs;
@@ -119,7 +120,7 @@ template <int DT, int S>
 __global__ __launch_bounds__(kSwigluT) void swiglu_backward_kernel(SwigluJob j) {
   const int rows = j.count ? min(j.n, max(*j.count, 0)) : j.n;
   const int sub = j.many > 1 ? (int)threadIdx.x / j.tpr : 0, lt = (int)threadIdx.x - sub * j.tpr;
-  if (sub >= j.many) return;
+  if (sub >= j.many || lt >= j.tpr) return;  // (workgroups are whole waves, tpr is whole runs of 16)
   constexpr int xs = DT == MOE_F32 ? 4 : 2;
   for (int64_t t = (int64_t)blockIdx.x * j.many + sub; t < rows; t += (int64_t)gridDim.x * j.many) {
     const char* gu = (const char*)j.gu + t * j.gu_pitch * xs;

@@ -1,0 +1,48 @@
+"""The experts' products where calls have gone wrong or could: rows of several passes in place, first runs on other
+streams.  References are fp64."""
+import numpy as np
+import pytest
+import torch
+
+import asynchronous_moe_expert_amd as M
+from oracle import products as O
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F32, BF16, FP8, I32 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int32
+HALF = {F32: U, BF16: 2.0 ** -8}
+
+
+def bits(t):
+    return t.view(I32 if t.element_size() == 4 else torch.int16)
+
+
+@pytest.mark.parametrize("I", [4104, 5632, 5760, 11008, 20488])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_swiglu_gradient_of_long_rows_in_place(I, dtype):
+    """Rows of several passes whose threads are no whole number of waves.  In place and not, the bits are the same;
+    against fp64, dg = dh u s (1 + g (1 - s)) is off by 16 u of |dh u s| (1 + |g|) (s 4 u, 1 - s 4 u of s and its own
+    rounding, g (1 - s) and the sum two more, three products), du and h by 8 u of themselves, and a stored value by
+    half a step."""
+    print("swiglu gradient", I, dtype, flush=True)
+    g, n, there = torch.Generator(device="cuda").manual_seed(I), 600, 597
+    gu = (torch.randn(n, 2 * I + 8, generator=g, device="cuda") * 2).to(dtype)[:, :2 * I]
+    dh = torch.randn(n, I, generator=g, device="cuda").to(dtype)
+    count = torch.tensor([there], dtype=I32, device="cuda")
+    dgu = torch.full((n, 2 * I), 3, dtype=dtype, device="cuda")
+    h, again, ahead = (torch.full((n, I), 3, dtype=dtype, device="cuda") for _ in range(3))
+    M.moe_swiglu(gu, ahead, count=count)
+    M.moe_swiglu_backward(gu, dh, dgu, h=h, count=count)
+    rows = [0, 1, 255, 256, 511, there - 1]
+    val, dv = gu[rows].double().cpu().numpy(), dh[rows].double().cpu().numpy()
+    behind = gu[there:].clone()
+    M.moe_swiglu_backward(gu, dh, gu, h=again, count=count)
+    assert torch.equal(bits(gu[:there]), bits(dgu[:there])) and torch.equal(bits(gu[there:]), bits(behind))
+    assert torch.equal(bits(h), bits(again)) and torch.equal(bits(h), bits(ahead))
+    assert bool((dgu[there:] == 3).all()) and bool((h[there:] == 3).all())
+    a, u = val[:, :I], val[:, I:]
+    ref, rh, v = O.swiglu_backward(val, dv), O.swiglu(val), HALF[dtype]
+    room = np.concatenate([16 * U * np.abs(dv * u * O.sigmoid(a)) * (1 + np.abs(a)), 8 * U * np.abs(ref[:, I:])], 1)
+    assert (np.abs(dgu[rows].double().cpu().numpy() - ref) - room - v * np.abs(ref) - 2.0 ** -120).max() <= 0
+    assert (np.abs(h[rows].double().cpu().numpy() - rh) - 8 * U * np.abs(rh) - v * np.abs(rh) - 2.0 ** -120).max() <= 0
