@@ -394,19 +394,41 @@ def _home():
     return _marshal
 
 
+def _stream_object(stream, at: int):
+    """`stream` (an object or a handle) of device `at` as torch knows it."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    handle = _stream(stream)
+    return torch.cuda.ExternalStream(handle, device=at) if handle else torch.cuda.default_stream(at)
+
+
 def keep_for(stream, at: int, tensors) -> None:
     """Records what a call on `stream` works on, unless that is the current stream of the tensors'
     device `at`, so that the allocator keeps it until the call's work is done."""
-    if stream is None:
+    if stream is None or _stream(stream) == _raw_stream(at):
         return
-    handle = _stream(stream)
-    if handle == _raw_stream(at):
-        return
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(handle, device=at) if handle else torch.cuda.default_stream(at)
+    stream = _stream_object(stream, at)
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+
+
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def after_current(stream, at: int) -> None:
+    """`stream` goes on after what device `at`'s current stream has been given so far.  For a buffer made within a
+    call on `stream`: the allocator hands out memory that work of the current stream, and of no other, may still
+    be using."""
+    if stream is None or _stream(stream) == _raw_stream(at):
+        return
+    stream, current = _stream_object(stream, at), torch.cuda.current_stream(at)
+    if _capturing(stream) != _capturing(current):
+        raise MoeError("a call that makes its buffers was given another stream than the current one while one of the two "
+                       "is captured; make the call once before")
+    stream.wait_stream(current)
 
 
 def _elsewhere(call, args, tensors, stream) -> None:

@@ -279,7 +279,8 @@ class ExpertTrainLayer:
     xs, which the gradient of the first product's weights reads.  The weights are read, never kept or packed: an
     optimizer may change them between a backward() and the next run().  After run() the buffers hold expert and
     w ([T][K]), pos, counts, offsets, gu, h and y (rows sorted by expert).  They belong to one run at a time, as
-    ExpertLayer's do."""
+    ExpertLayer's do.  What only training needs is made by the first run(train=True) and the first backward(), which on
+    another stream than the current one wait for the current one's work."""
 
     def __init__(self, E: int, H: int, I: int, K: int, dtype: int, T_max: int, device="cuda",
                  score: int = N.MOE_SOFTMAX, renorm: bool = True, scale: float = 1.0, bias_on_score: bool = True):
@@ -314,6 +315,12 @@ class ExpertTrainLayer:
     def _rows(self, columns: int) -> torch.Tensor:
         return torch.empty((self._n, columns), dtype=self._adt, device=self._dev)
 
+    def _made_now(self, stream, make):
+        """Buffers that only training needs, when a call first needs them."""
+        made = make()
+        N.after_current(stream, self.y.get_device())
+        return made
+
     def run(self, x, logits, w_gu, w_d, out, bias=None, x_scale=None, s_gu=None, s_d=None, train: bool = False,
             stream=None) -> None:
         """x [T][H], logits [T][E], w_gu [E][2 I][H] (gate rows, then up rows), w_d [E][H][I]; out [T][H]:
@@ -339,7 +346,7 @@ class ExpertTrainLayer:
         xs = None
         if train:
             if self.xs is None:
-                self.xs = self._rows(self.H)
+                self.xs = self._made_now(stream, lambda: self._rows(self.H))
             xs = self.xs[:n]
         N.moe_route(logits, self.expert, self.w, bias=bias, stream=stream, **self.how)
         N.moe_sort_rows(self.expert, self.E, x if train else None, xs, None, self.pos, self.counts, self.offsets, self.err,
@@ -371,7 +378,8 @@ class ExpertTrainLayer:
         if dw_gu.shape != w_gu.shape or dw_d.shape != w_d.shape:
             raise N.MoeError(f"ExpertTrainLayer: gradients {tuple(dw_gu.shape)} and {tuple(dw_d.shape)}")
         if self._back is None:
-            self._back = (self._rows(self.H), self._rows(self.I), self._rows(self.H), torch.empty_like(self._w))
+            self._back = self._made_now(stream, lambda: (self._rows(self.H), self._rows(self.I), self._rows(self.H),
+                                                         torch.empty_like(self._w)))
         dy, dh, dxs = (t[:n] for t in self._back[:3])
         dw, pos, gu, count = self._back[3][:n].view(T, self.K), self.pos[:n], self.gu[:n], self.offsets[self.E:]
         N.moe_merge_rows_backward(dout, self.y[:n], pos, self.w, dy, dw, self.err, stream=stream)

@@ -46,3 +46,53 @@ def test_swiglu_gradient_of_long_rows_in_place(I, dtype):
     room = np.concatenate([16 * U * np.abs(dv * u * O.sigmoid(a)) * (1 + np.abs(a)), 8 * U * np.abs(ref[:, I:])], 1)
     assert (np.abs(dgu[rows].double().cpu().numpy() - ref) - room - v * np.abs(ref) - 2.0 ** -120).max() <= 0
     assert (np.abs(h[rows].double().cpu().numpy() - rh) - 8 * U * np.abs(rh) - v * np.abs(rh) - 2.0 ** -120).max() <= 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_first_training_run_on_another_stream(dtype):
+    """The buffers that a first training run makes come from the current stream's memory, where work that was given
+    before is still to write what has been freed since; its results are those of a layer that has run before."""
+    print("first run elsewhere", dtype, flush=True)
+    T, E, K, H, I = 3000, 5, 2, 264, 520
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def rand(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    x, dout, logits = rand(T, H).to(dtype), rand(T, H).to(dtype), rand(T, E)
+    w_gu, w_d = (rand(E, 2 * I, H) * H ** -0.5).to(dtype), (rand(E, H, I) * I ** -0.5).to(dtype)
+    code = M.MOE_F32 if dtype == F32 else M.MOE_BF16
+
+    def step(layer, outs, stream=None, before=None):
+        for part in range(2):
+            if before:
+                before(part)
+            if part == 0:
+                layer.run(x, logits, w_gu, w_d, outs[0], train=True, stream=stream)
+            else:
+                layer.backward(dout, *outs[1:], stream=stream)
+
+    outs = [[torch.empty_like(t) for t in (x, x, logits, w_gu, w_d)] for _ in range(2)]
+    first = M.ExpertTrainLayer(E, H, I, K, code, T)
+    step(first, outs[0])
+    step(first, outs[0])
+    one, side = M.ExpertTrainLayer(E, H, I, K, code, T), torch.cuda.Stream()
+    a, b = rand(8192, 8192), rand(8192, 8192)
+    product = torch.empty_like(a)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    made = []
+
+    def pending(part):
+        for _ in range(6):
+            torch.mm(a, b, out=product)  # some milliseconds each
+        freed = [torch.empty(T * K, c, dtype=dtype, device="cuda") for c in ((H,) if part == 0 else (H, I, H))]
+        for t in freed:
+            t.fill_(float("nan"))
+        made.append({t.data_ptr() for t in freed})
+
+    step(one, outs[1], stream=side, before=pending)
+    torch.cuda.synchronize()
+    assert one.xs.data_ptr() in made[0] and one._back[0].data_ptr() in made[1]  # or this tests nothing
+    for got, ref in zip(outs[1], outs[0]):
+        assert torch.equal(bits(got), bits(ref))
