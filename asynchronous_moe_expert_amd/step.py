@@ -299,6 +299,7 @@ class ExpertTrainLayer:
         self._adt = torch.float32 if dtype == N.MOE_F32 else torch.bfloat16
         i32 = dict(dtype=torch.int32, device=self._dev)
         self._expert, self.pos, self.row_slot = (torch.empty(n, **i32) for _ in range(3))
+        self._dev = self._expert.device  # with its number: what is made later is made there too
         self._w = torch.empty(n, dtype=torch.float32, device=self._dev)
         self.counts, self.offsets, self.err = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.zeros(1, **i32)
         self.sort_ws = torch.empty(max(N.moe_sort_rows_workspace_size(n), 16), dtype=torch.uint8, device=self._dev)

@@ -89,3 +89,22 @@ def test_a_capture_that_cannot_wait_is_refused(calls, streams, monkeypatch):
     assert not calls
     one.run(*inputs(), train=True)
     one.run(*inputs(), train=True, stream=77)
+
+
+def test_later_buffers_are_made_where_the_layer_is(calls, monkeypatch):
+    """A device without a number is the current one when the layer is built, whatever it is later on."""
+    real, asked = torch.empty, []
+
+    def empty(*size, device=None, **k):
+        asked.append(torch.device(device))
+        return real(*size, device="meta" if torch.device(device).type == "cuda" else device, **k)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "zeros", lambda *size, device=None, **k: empty(*size, device=device, **k))
+    one = M.ExpertTrainLayer(E, H, I, K, M.MOE_F32, T, device="cuda")
+    monkeypatch.undo()
+    made = []
+    monkeypatch.setattr(torch, "empty", lambda *size, device=None, **k: made.append(torch.device(device)) or
+                        real(*size, device="meta", **k))
+    one._rows(H)
+    assert asked and made == [one.y.device]
