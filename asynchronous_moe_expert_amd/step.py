@@ -268,6 +268,35 @@ class ExpertLayer:
         N.moe_merge_rows(self.y[:n], self.pos[:n], self.w, out, self.err, stream=stream)
 
 
+def _rows_check(what: str, t, shape, dtypes, device, reach: int = 0) -> None:
+    """Refuses what the calls of a step would refuse of a tensor of rows ([..][rows][columns]) only after work before them
+    has been enqueued.  reach: also the limits of a product's operand, 16 MiB between rows and so many bytes of them."""
+    def refuse(why):
+        raise N.MoeError(f"ExpertTrainLayer: {what} {why}")
+
+    if t.device != device:
+        refuse(f"on {t.device}, the layer on {device}")
+    if t.dtype not in dtypes:
+        refuse(f"of {t.dtype}")
+    if t.shape != shape:
+        refuse(f"of shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, columns, es = *shape[-2:], t.element_size()
+    pitch = t.stride(-2) if rows > 1 else columns
+    if (columns > 1 and t.stride(-1) != 1) or pitch < columns:
+        refuse(f"of strides {t.stride()}: the elements of a row must be contiguous and rows must not overlap")
+    stride = t.stride(0) if t.dim() == 3 and shape[0] > 1 else (rows - 1) * pitch + columns if rows else 0
+    if t.dim() == 3 and stride < (rows - 1) * pitch + columns:
+        refuse(f"of strides {t.stride()}: its matrices overlap")
+    if t.numel() and (t.data_ptr() % 16 or pitch * es % 16 or (t.dim() == 3 and shape[0] > 1 and stride * es % 16)):
+        refuse("with a row that does not begin at a multiple of 16 bytes")
+    if pitch > 1 << 32 or (reach and (pitch * es > 1 << 24 or rows * pitch * es > reach or stride > reach)):
+        refuse(f"of strides {t.stride()}: rows too far apart")
+
+
+_REACH = 1 << 36  # bytes of a product's rows, or of an expert's matrix
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
 class ExpertTrainLayer:
     """A layer whose experts are all on this rank, with its gradients, over plain row-major weights:
     moe_route, moe_sort_rows, two products per expert with moe_swiglu between them, moe_merge_rows; and
@@ -368,16 +397,22 @@ class ExpertTrainLayer:
     def backward(self, dout, dx, dlogits, dw_gu, dw_d, accumulate: bool = False, stream=None) -> None:
         """The gradients of the last run(train=True) for dout [T][H]: dx [T][H], dlogits [T][E] (of the
         logits' type; the choice itself and a bias have none), dw_gu and dw_d like the weights (f32, or bf16 in a
-        bf16 layer), added to with accumulate.  logits and the weights are read again."""
+        bf16 layer), added to with accumulate.  logits and the weights are read again.  A call that is refused has
+        written nothing, and may be made again."""
         if self._kept is None:
             raise N.MoeError("ExpertTrainLayer: backward() comes after run(train=True), once")
         T, logits, w_gu, w_d = self._kept
-        n = T * self.K
-        if dout.shape != (T, self.H) or dx.shape != (T, self.H) or dlogits.shape != (T, self.E):
-            raise N.MoeError(f"ExpertTrainLayer: dout {tuple(dout.shape)}, dx {tuple(dx.shape)} and dlogits "
-                             f"{tuple(dlogits.shape)} for {T} tokens")
-        if dw_gu.shape != w_gu.shape or dw_d.shape != w_d.shape:
-            raise N.MoeError(f"ExpertTrainLayer: gradients {tuple(dw_gu.shape)} and {tuple(dw_d.shape)}")
+        n, at = T * self.K, self.y.device
+        kinds = (torch.float32, self._adt)
+        _rows_check("dout", dout, (T, self.H), _FLOATS, at)
+        _rows_check("dx", dx, (T, self.H), _FLOATS, at)
+        _rows_check("dw_gu", dw_gu, w_gu.shape, kinds, at, _REACH)
+        _rows_check("dw_d", dw_d, w_d.shape, kinds, at, _REACH)
+        if dlogits.shape != (T, self.E) or dlogits.dtype != logits.dtype or dlogits.device != at:
+            raise N.MoeError(f"ExpertTrainLayer: dlogits {tuple(dlogits.shape)} of {dlogits.dtype} on {dlogits.device} for "
+                             f"{T} tokens, logits of {logits.dtype} on {at}")
+        if (self.E > 1 and dlogits.stride(1) != 1) or (T > 1 and not self.E <= dlogits.stride(0) <= 1 << 32):
+            raise N.MoeError(f"ExpertTrainLayer: dlogits of strides {dlogits.stride()}")
         if self._back is None:
             self._back = self._made_now(stream, lambda: (self._rows(self.H), self._rows(self.I), self._rows(self.H),
                                                          torch.empty_like(self._w)))

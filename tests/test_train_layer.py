@@ -108,3 +108,57 @@ def test_later_buffers_are_made_where_the_layer_is(calls, monkeypatch):
                         real(*size, device="meta", **k))
     one._rows(H)
     assert asked and made == [one.y.device]
+
+
+def _bad(good, T_rows=True):
+    """Tensors like `good` that a call has to refuse."""
+    rows, columns = good.shape[-2:]
+    lead = good.shape[:-2]
+    new = lambda *s, **k: torch.zeros(*s, dtype=k.get("dtype", good.dtype))  # noqa: E731
+    yield "type", new(*good.shape, dtype=torch.float16)
+    yield "shape", new(*lead, rows, columns + 8)
+    yield "shape", new(*lead, rows + 1, columns)
+    yield "strides", new(*lead, columns, rows).transpose(-1, -2)
+    yield "overlap", new(*lead, 1, columns).expand(good.shape)
+    yield "alignment", new(*lead, rows, columns + 1)[..., :columns]
+    flat = new(good.numel() + 1)
+    yield "alignment", flat[1:].view(good.shape)
+    yield "device", torch.empty(good.shape, dtype=good.dtype, device="meta")
+    if lead:
+        yield "overlap", new(1, rows, columns).expand(good.shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("which", range(5))
+def test_a_refused_backward_makes_no_call_and_may_be_made_again(calls, which, dtype):
+    """The gradients of the weights may be added to: nothing of them may have been before a later call refuses."""
+    one = layer(M.MOE_F32 if dtype == torch.float32 else M.MOE_BF16)
+    one.run(*inputs(dtype), train=True)
+    good = gradients(dtype)
+    for why, t in _bad(good[which]):
+        if which == 2 and why == "alignment":  # logits have none
+            continue
+        del calls[:]
+        with pytest.raises(M.MoeError, match="ExpertTrainLayer"):
+            one.backward(*good[:which], t, *good[which + 1:], accumulate=True)
+        assert not calls, why
+    if which in (3, 4) and dtype == torch.float32:
+        with pytest.raises(M.MoeError, match="ExpertTrainLayer"):
+            one.backward(*good[:which], good[which].bfloat16(), *good[which + 1:])
+    one.backward(*good, accumulate=True)
+    assert calls[-1] == "moe_route_backward"
+
+
+def test_gradients_of_every_kind_that_the_calls_take(calls):
+    """bf16 layers: f32 gradients of weights, f32 dx; halves of larger tensors, padded rows, logits in any pitch."""
+    one = layer(M.MOE_BF16)
+    dout, dx, dlogits, dw_gu, dw_d = gradients(torch.bfloat16)
+    wide = torch.zeros(E, 2 * I, H + 8)[..., :H]
+    both = torch.zeros(E, 2 * H, I)[:, H:]
+    for made in ((dout, dx, dlogits, dw_gu.float(), dw_d), (dout.float(), dx.float(), dlogits, wide, both),
+                 (dout, dx, torch.zeros(T, E + 3)[:, 1:E + 1], wide.bfloat16(), dw_d.float())):
+        one.run(*inputs(torch.bfloat16), train=True)
+        one.backward(*made)
+    none = M.ExpertTrainLayer(E, H, I, K, M.MOE_BF16, 0, device="cpu")
+    none.run(*[t[:0] if t.shape[0] == T else t for t in inputs(torch.bfloat16)], train=True)
+    none.backward(dout[:0], dx[:0], dlogits[:0], dw_gu, dw_d)
