@@ -23,6 +23,8 @@ in order, 101 us overlapped).
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _native as N
@@ -271,6 +273,10 @@ class ExpertLayer:
 def _rows_check(what: str, t, shape, dtypes, device, reach: int = 0) -> None:
     """Refuses what the calls of a step would refuse of a tensor of rows ([..][rows][columns]) only after work before them
     has been enqueued.  reach: also the limits of a product's operand, 16 MiB between rows and so many bytes of them."""
+    if (t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous() and t.data_ptr() % 16 == 0
+            and t.numel() < 1 << 32):
+        return  # as nearly all are; rows of a layer's columns are whole runs of 16 bytes
+
     def refuse(why):
         raise N.MoeError(f"ExpertTrainLayer: {what} {why}")
 
@@ -291,6 +297,15 @@ def _rows_check(what: str, t, shape, dtypes, device, reach: int = 0) -> None:
         refuse("with a row that does not begin at a multiple of 16 bytes")
     if pitch > 1 << 32 or (reach and (pitch * es > 1 << 24 or rows * pitch * es > reach or stride > reach)):
         refuse(f"of strides {t.stride()}: rows too far apart")
+
+
+def _scales_check(what: str, t, shape, device) -> None:
+    """Scales are contiguous: flat, or of `shape` (rows may have more behind them)."""
+    fits = (t.numel() >= math.prod(shape) if t.dim() == 1 else t.dim() == len(shape) and t.shape[1:] == shape[1:]
+            and (t.shape[0] == shape[0] or (len(shape) == 2 and t.shape[0] > shape[0])))
+    if t.device != device or t.dtype != torch.float32 or not t.is_contiguous() or not fits:
+        raise N.MoeError(f"ExpertTrainLayer: {what} {tuple(t.shape)} of {t.dtype} on {t.device}, expected {shape}, "
+                         f"contiguous fp32 on {device}")
 
 
 _REACH = 1 << 36  # bytes of a product's rows, or of an expert's matrix
@@ -361,16 +376,21 @@ class ExpertTrainLayer:
             raise N.MoeError(f"ExpertTrainLayer: x on {x.device}, the layer on {self.y.device}")
         if T > self.T_max:
             raise N.MoeError(f"ExpertTrainLayer: {T} tokens, built for {self.T_max}")
-        if x.shape != (T, self.H) or out.shape != (T, self.H) or logits.shape != (T, self.E):
-            raise N.MoeError(f"ExpertTrainLayer: x {tuple(x.shape)} with logits {tuple(logits.shape)} and out "
-                             f"{tuple(out.shape)}")
-        if w_gu.shape != (self.E, 2 * self.I, self.H) or w_d.shape != (self.E, self.H, self.I):
-            raise N.MoeError(f"ExpertTrainLayer: weights {tuple(w_gu.shape)} and {tuple(w_d.shape)}")
-        for t in (x, w_gu, w_d):
-            if N.dtype_code(t) != self.dtype:
-                raise N.MoeError(f"ExpertTrainLayer: {t.dtype} in a layer of type {self.dtype}")
+        if logits.shape != (T, self.E):
+            raise N.MoeError(f"ExpertTrainLayer: x {tuple(x.shape)} with logits {tuple(logits.shape)}")
+        at = self.y.device
+        kinds = (torch.uint8, torch.float8_e4m3fn) if fp8 else (self._adt,)
+        _rows_check("x", x, (T, self.H), kinds, at, _REACH)
+        _rows_check("w_gu", w_gu, (self.E, 2 * self.I, self.H), kinds, at, _REACH)
+        _rows_check("w_d", w_d, (self.E, self.H, self.I), kinds, at, _REACH)
+        _rows_check("out", out, (T, self.H), _FLOATS, at)
         if fp8 and (train or x_scale is None or s_gu is None or s_d is None):
             raise N.MoeError("ExpertTrainLayer: fp8 takes x_scale, s_gu and s_d, and runs forward only")
+        if fp8:
+            hb, ib, gb = ((c + 127) // 128 for c in (self.H, self.I, 2 * self.I))
+            _scales_check("x_scale", x_scale, (T, hb), at)
+            _scales_check("s_gu", s_gu, (self.E, gb, hb), at)
+            _scales_check("s_d", s_d, (self.E, hb, ib), at)
         self._kept = None
         self.expert, self.w = self._expert[:n].view(T, self.K), self._w[:n].view(T, self.K)
         xs = None

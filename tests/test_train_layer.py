@@ -162,3 +162,46 @@ def test_gradients_of_every_kind_that_the_calls_take(calls):
     none = M.ExpertTrainLayer(E, H, I, K, M.MOE_BF16, 0, device="cpu")
     none.run(*[t[:0] if t.shape[0] == T else t for t in inputs(torch.bfloat16)], train=True)
     none.backward(dout[:0], dx[:0], dlogits[:0], dw_gu, dw_d)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.uint8])
+@pytest.mark.parametrize("which", range(5))
+def test_a_refused_run_makes_no_call(calls, which, dtype):
+    """A run that is refused leaves what the last one keeps for backward()."""
+    fp8 = dtype == torch.uint8
+    one = layer({torch.float32: M.MOE_F32, torch.bfloat16: M.MOE_BF16, torch.uint8: M.MOE_FP8_E4M3}[dtype])
+    good = inputs(dtype)
+    if fp8:
+        good[4] = good[4].bfloat16()
+    scales = dict(x_scale=torch.zeros(T, 1), s_gu=torch.zeros(E, 1, 1), s_d=torch.zeros(E, 1, 1)) if fp8 else {}
+    one.run(*good, train=not fp8, **scales)
+    for why, t in _bad(good[which]):
+        if which == 1 and why not in ("shape", ):  # the rest is moe_route's, the first call
+            continue
+        del calls[:]
+        with pytest.raises(M.MoeError, match="ExpertTrainLayer"):
+            one.run(*good[:which], t, *good[which + 1:], **scales)
+        assert not calls, why
+    if not fp8:
+        one.backward(*gradients(dtype))
+        return
+    for name, t in scales.items():
+        for bad in (t.double(), t[1:], t.expand(*t.shape[:-1], 2), t[None], torch.empty(t.shape, device="meta"),
+                    t.view(-1)[1:], None, torch.zeros(E * 2, *t.shape[1:])[::2]):
+            if name == "x_scale" and bad is not None and bad.dim() == 2 and bad.shape[0] > T:
+                continue
+            del calls[:]
+            with pytest.raises(M.MoeError, match="ExpertTrainLayer"):
+                one.run(*good, **dict(scales, **{name: bad}))
+            assert not calls
+    one.run(*good, **dict(scales, x_scale=torch.zeros(T + 3, 1), s_d=torch.zeros(E)))
+    one.run(good[0].view(torch.float8_e4m3fn), *good[1:], **scales)
+
+
+def test_rows_of_every_layout_that_the_calls_take(calls):
+    one = layer(M.MOE_BF16)
+    x, logits, w_gu, w_d, out = inputs(torch.bfloat16)
+    wide = torch.zeros(T, H + 16, dtype=torch.bfloat16)[:, 8:H + 8]
+    one.run(wide, torch.zeros(T, E + 1)[:, 1:], torch.zeros(E, 2 * I, H + 8, dtype=torch.bfloat16)[..., :H],
+            torch.zeros(E, 2 * H, I, dtype=torch.bfloat16)[:, H:], torch.zeros(T, H + 4)[:, 4:])
+    one.run(torch.zeros(H, 1, dtype=torch.bfloat16).t(), logits[:1], w_gu, w_d, out[:1])  # one row has no pitch
