@@ -18,27 +18,32 @@ static __device__ u32x4 g_zeros;  // what lanes past a contraction's end copy
 // A wave's copy of 64 x 16 (or 64 x 4) bytes to LDS, lane after lane from dst on.  In inline assembly, so that
 // the compiler does not put waits of its own before every LDS read that might meet a copy (it tells the copies of
 // a few instructions apart, and a tile has more); the waits are wait_copies and meet below.  The address is
-// read when the copy is issued, and nothing is returned to a register.
+// read when the copy is issued, and nothing is returned to a register.  m0, which the copies take their place in LDS
+// from, is named as written so that none of them comes between a value that the compiler puts there and its use (it
+// warns that it would not keep one in m0 across the statement, which is as well).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 template <int AT = 0>
 __device__ __forceinline__ void copy16(const char* src, uint32_t dst) {
   asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst), "n"(AT)
-               : "memory", "scc");
+               : "memory", "scc", "m0");
 }
 template <int AT = 0>
 __device__ __forceinline__ void copy16(const char* base, uint32_t off, uint32_t dst) {  // base in scalar registers
   asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst), "n"(AT)
-               : "memory", "scc");
+               : "memory", "scc", "m0");
 }
 __device__ __forceinline__ void copy16_once(const char* base, uint32_t off, uint32_t dst) {  // non-temporal
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(dst)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(const char* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 template <typename F, int... I>
 __device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
   (f(std::integral_constant<int, I>{}), ...);
