@@ -468,7 +468,7 @@ PyObject* expert_matmul(Call& c) {
     if (!x_scale || !w_scale) refuse("x_scale and w_scale: required for fp8");
     const int64_t kb = groups(in.cols, 128), nb = groups(s.cols, 128);
     a.x_scale = (const float*)table("x_scale", x_scale, in.rows, kb, F32);
-    if (w_scale->dim() == 3) mats("w_scale", *w_scale, E, nb, kb, F32);
+    if (w_scale->dim() != 1) mats("w_scale", *w_scale, E, nb, kb, F32);  // or flat
     a.w_scale = (const float*)vec("w_scale", w_scale, E * nb * kb, F32);
   }
   a.out_pitch = mat("out", out, s.rows, s.cols, F32 | BF16);
