@@ -194,7 +194,7 @@ static int run_product(const ProductJob& j, int dtype, hipStream_t stream) {
 
 // a matrix of `rows` rows of `cols` elements, one of several `stride` apart
 static int matrix_status(const void* p, int64_t rows, int64_t cols, int64_t pitch, int64_t stride, int many, int es) {
-  if (pitch < cols || pitch * es > kPitch || rows * pitch * es > kReach) return MOE_EINVAL_SIZE;
+  if (pitch < cols || pitch > kPitch / es || rows * pitch * es > kReach) return MOE_EINVAL_SIZE;
   if (many > 1 && (stride < (rows - 1) * pitch + cols || stride > kReach)) return MOE_EINVAL_SIZE;
   if (!aligned_rows(p, pitch, es, 16) || (many > 1 && (stride * es) % 16)) return MOE_EINVAL_ALIGN;
   return MOE_OK;

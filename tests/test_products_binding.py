@@ -1,4 +1,5 @@
 """The binding's checks of the experts' products' tensors, beyond those of their sizes."""
+import ctypes as C
 import os
 
 import pytest
@@ -31,3 +32,20 @@ def test_weights_scales_of_another_shape():
     for fine in (good, good.view(-1)):
         with pytest.raises(M.MoeError, match="on a GPU"):
             call(fine)
+
+
+def test_pitches_whose_bytes_pass_64_bits():
+    """They are over the limit of 16 MiB like any other that is."""
+    from asynchronous_moe_expert_amd import _native as N
+    from test_products_cpu import F32, MATMUL, MATMUL_B, SIZE
+
+    lib = M.load()
+    for pitch in (1 << 62, 3 << 61, (1 << 63) - 8):
+        for name, struct, good, fields in (
+                ("moe_expert_matmul", N.ExpertMatmulArgs, MATMUL, ("x_pitch", "w_pitch")),
+                ("moe_expert_matmul_backward", N.ExpertMatmulBackwardArgs, MATMUL_B, ("x_pitch", "dout_pitch", "dw_pitch"))):
+            for field in fields:
+                a = dict(good, dtype=F32, **{field: pitch})
+                a.update(dict(out_dtype=F32) if "out_dtype" in a else {})
+                a.update({s: (1 << 36) - 8 for s in ("w_stride", "dw_stride") if s in a})
+                assert getattr(lib, name)(C.byref(struct(**a)), None) == SIZE, (name, field, pitch)
