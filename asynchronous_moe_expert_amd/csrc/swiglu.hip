@@ -7,9 +7,10 @@
 namespace moe {
 
 // s = 1 / (1 + exp(-g)).  exp(-g) = 2^t with t = -g log2(e): t's own rounding error times ln 2 is put back to
-// first order, so that the result stays within 3 x 2^-24 of itself for every g (v_exp_f32 alone is off by
-// |g| 2^-24); past |t| = 127 the exponential is 0 or infinite and the correction, which would be NaN for
-// infinite g, is left out.
+// first order (v_exp_f32 alone is off by |g| 2^-24), so that s is within 5 x 2^-24 of itself as long as it is a normal
+// number, g >= -87.3: 2 x 2^-24 of v_exp_f32, a rounding of each sum, the quotient's (g s measured: within 4.3 x 2^-24).
+// Below, s is off by at most 2^-126: its subnormal values come out as 0.  Past |t| = 127 the exponential is 0 or
+// infinite or about to be, and the correction, which would be NaN for infinite g, is left out.
 __device__ __forceinline__ float sigmoid(float g) {
   const float t = -1.44269504f * g;
   float lo = fmaf(-1.44269504f, g, -t);      // what rounding t lost
