@@ -96,3 +96,44 @@ def test_first_training_run_on_another_stream(dtype):
     assert one.xs.data_ptr() in made[0] and one._back[0].data_ptr() in made[1]  # or this tests nothing
     for got, ref in zip(outs[1], outs[0]):
         assert torch.equal(bits(got), bits(ref))
+
+
+def product8(x, w, odt):
+    """x [n][D] and w [N][D], values that 8-bit codes hold, as one expert's product with scales of one."""
+    (n, D), N = x.shape, w.shape[0]
+    offsets, out = torch.tensor([0, n], dtype=I32, device="cuda"), torch.full((n, N), float("nan"), dtype=odt, device="cuda")
+    M.moe_expert_matmul(x.to(FP8), w[None].to(FP8), offsets, out, x_scale=torch.ones(n, -(-D // 128), device="cuda"),
+                        w_scale=torch.ones(1, -(-N // 128), -(-D // 128), device="cuda"))
+    return out
+
+
+@pytest.mark.parametrize("odt", [F32, BF16])
+@pytest.mark.parametrize("rows", [16, 300])
+def test_8_bit_products_far_below_the_largest(rows, odt):
+    """2^16 - 2^16 + 2^(16 - d) in one block: exact in bf16 outputs while the products lie within 13 bits, wherever
+    they are, and in fp32 ones within 23, that type's own."""
+    print("8-bit products", rows, odt, flush=True)
+    for i, j, k in ((0, 1, 2), (0, 2, 1), (3, 9, 4), (0, 64, 127), (5, 100, 50), (126, 127, 0), (40, 47, 41)):
+        for d in range(0, (13 if odt == BF16 else 23) + 1):
+            x, w = torch.zeros(rows, 128, device="cuda"), torch.zeros(128, 128, device="cuda")
+            small = min(d, 17)  # codes go down to 2^-9
+            x[:, i], x[:, j], x[:, k] = 256.0, -256.0, 2.0 ** (8 - small)
+            w[:, i], w[:, j], w[:, k] = 256.0, 256.0, 2.0 ** (8 - (d - small))
+            assert bool((product8(x, w, odt) == 2.0 ** (16 - d)).all()), (i, j, k, d)
+
+
+@pytest.mark.parametrize("large", [1, 30, 300])
+@pytest.mark.parametrize("rows,D", [(40, 2880), (400, 1040)])
+def test_8_bit_products_with_a_large_column(rows, D, large):
+    """bf16 outputs: of eight products seven are cut by less than 2^-13 of the largest, so that an element is off by
+    less than 7 2^-13 of the sum of its terms' sizes; the sums in fp32 of at most D of them 2 u (D + 3) of it, the
+    result half a step.  fp32 outputs: the last two."""
+    print("large column", rows, D, large, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(rows + large)
+    x, w = torch.randn(rows, D, generator=g, device="cuda") * 100 / large, torch.randn(264, D, generator=g, device="cuda") * 100
+    x[:, ::128] *= large
+    x, w = (t.clamp(-448, 448).to(FP8).double() for t in (x, w))
+    ref, size = x @ w.t(), x.abs() @ w.abs().t()
+    for odt in (BF16, F32):
+        off = (product8(x.float(), w.float(), odt).double() - ref).abs() - HALF[odt] * ref.abs() - 2 * U * (D + 3) * size
+        assert float((off - (7 * 2.0 ** -13 * size if odt == BF16 else 0)).max()) <= 0, odt
