@@ -14,8 +14,9 @@ namespace moe {
 //           once; run_narrow chooses the NW that leaves the fewest CUs idle;
 //   WK = 4: 32 columns, a step is four times as long, each wave takes its quarter and the waves' sums are added at
 //           the end: for calls that would leave most CUs idle.
-// Fragments lie in LDS as the tiles' do (product_tiles.hip).  256 rows of 8 experts, 5760 x 2880: 45 us in bf16 (the
-// weights at 6.0 TB/s), 34 in 8 bits (4.0: rows of 2880 bytes, whose steps are parts of two lines each); 128 experts
+// Fragments lie in LDS as the tiles' do (product_tiles.hip).  256 rows of 8 experts, 5760 x 2880, other weights each
+// time: 45 us in bf16 (the weights at 6.0 TB/s), 34 in 8 bits (4.0: rows of 2880 bytes, whose steps are parts of two
+// lines each), back to back 42 and 25 (some of the weights are still in the last-level cache then); 128 experts
 // of two rows, 2880 x 2880 bf16: 352 (6.0).
 template <int MODE, int DT, int WK, int NW, int S>
 struct Narrow {

@@ -5,9 +5,12 @@
 // Two groups of four waves take half of a tile's rows each and change places: while one multiplies, the other reads
 // its next fragments; group 0 makes all copies, group 1 finds tiles and rows, so that only one waits for memory.
 // 256 x 256 is the most that two stages in LDS and the accumulators in registers allow; smaller tiles read more from
-// L2 for each product.  Reached, 32 experts of 512 rows, 4096 x 4096: forward 484 to 488 us (1.13 PFLOP/s), rows' gradient 488,
-// 8 bits 350 (1.57); 8192 rows of one expert, 4096 x 8192: 390 (1.41, what a library product reaches) and 8 bits 262
-// (2.1).  With few rows an expert the weights' bytes bound it, with uneven ones the last tiles.
+// L2 for each product.  Reached, 32 experts of 512 rows, 4096 x 4096: forward 473 to 493 us (1.14 PFLOP/s), rows' gradient 484
+// to 500, 8 bits 321 to 370 by the codes' values (1.6); 8192 rows of one expert, 4096 x 8192: 390 to 399 (1.4, what a
+// library product reaches) and 8 bits 258 to 262 (2.1).  Counted there: the matrix cores are busy for 56% of the cycles
+// (8 bits 38%, the weights' gradient 32%), the waves wait for 37% of theirs (19%, 42%), LDS reads take 21% (17%, 12%)
+// with no conflicts, 68% (77%, 61%) of what is asked of L2 is there.  In 8 bits the compiler spills 11 vector registers,
+// with fp32 outputs 72.  With few rows an expert the weights' bytes bound it, with uneven ones the last tiles.
 #include <type_traits>
 
 #include "product_copy.hpp"
@@ -462,7 +465,10 @@ __device__ __forceinline__ Place tile(const ProductJob& j, const Place& at, W& w
 
   // ---- outputs, in whole lines of 128 bytes (but for forward fp32 ones and sums added to bf16).  A large fp32
   // gradient goes through the caches without staying: it would push out the rows that the next tiles read.  32 experts
-  // of 512 rows, 4096 x 4096: 806 us through the caches, 673 so (bf16: 691 either way).
+  // of 512 rows, 4096 x 4096, us through the caches / so: calls back to back 820 / 697, with x and dout from HBM (1 GiB
+  // written in between) 847 / 877 (bf16: 705 / 702, 699 / 702).  In a layer's step the rows have just been written: its
+  // whole backward pass, 8192 tokens, 32 experts, K 2, 4096 x 2048: 2330 / 2275; 2048 tokens, 8, K 4, 2880 x 2880:
+  // 1041 / 1012.
   const int64_t out0 = MODE == kWeightsGrad ? at.e * j.out_stride : 0;
   const bool odd = l16 & 1;
 #pragma unroll

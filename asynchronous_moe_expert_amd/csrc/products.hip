@@ -13,7 +13,9 @@ namespace moe {
 // long as both operands agree.  S = 128 where that makes two tiles for every CU, 64 otherwise.  Forward, us as 64 / 128:
 // 8 experts of 64 rows, 1024 x 1024: 33 / 84; 16 of 256: 88 / 89; 32 of 512: 332 / 314 (109 TFLOP/s); 1 of 4096 rows,
 // 4096 x 4096: 1226 / 1119 (123 of the 154 TFLOP/s that a library product reaches).  The matrix unit bounds the large
-// ones, the latency of one tile's k steps the small ones.
+// ones, the latency of one tile's k steps the small ones.  An element is one running sum over D: off by 5.7e-7 of the
+// outputs' norm at D = 1024 and 1.1e-6 at 4096, as a library product's is with many rows; with few (40), where that one
+// splits D, it has half.
 constexpr int kSK = 32, kSLd = 36;
 
 template <int MODE, int S>
@@ -182,7 +184,9 @@ static int run_f32(const ProductJob& j, int cus, hipStream_t stream) {
 
 // Up to 64 rows of an expert on average a product is a pass over its weights.  32 experts, 4096 x 4096 bf16, us as
 // tiles / narrow, forward: 4 rows each 187 / 159, 32 187 / 164, 64 193 / 177, 96 211 / 246, 128 216 / 259.  The rows'
-// gradient: 186 / 188, 188 / 194, 190 / 203, 198 / 261, 207 / 277; it goes by the same rule.
+// gradient: 185 / 188, 187 / 195, 190 / 204, 198 / 261, 207 / 277; but where the tiles leave CUs idle the narrow ones
+// win: 8 experts, 5760 x 2880, 4 rows each 69 / 44, 32 69 / 44, 64 73 / 58; one of 4096 x 4096, 49 / 31, 50 / 32, 50 / 41.
+// It goes by the same rule: a third saved there for at most 7% lost.
 template <int MODE>
 static int run_product(const ProductJob& j, int dtype, hipStream_t stream) {
   const int cus = compute_units();
@@ -255,7 +259,7 @@ extern "C" int moe_expert_matmul_backward(const moe_expert_matmul_backward_args*
   j.x = a->x; j.x_rows = a->n; j.x_pitch = a->x_pitch; j.dout = a->dout; j.dout_pitch = a->dout_pitch;
   j.out = a->dw; j.out_pitch = a->dw_pitch; j.out_stride = a->E_loc > 1 ? a->dw_stride : 0;
   j.out_f32 = a->dw_dtype == MOE_F32; j.accumulate = a->accumulate;
-  // fp32 ones of 96 MiB and more, which no cache would keep (product_tiles.hip)
+  // fp32 ones of 96 MiB and more, which no cache would keep (both sides' times are in product_tiles.hip)
   j.through = j.out_f32 && (int64_t)a->E_loc * a->N * a->D * 4 >= (96ll << 20);
   return run_product<kWeightsGrad>(j, a->dtype, stream);
 }
