@@ -73,6 +73,7 @@ class ExpertStep:
         fp8 weights come as uint8 codes with fp32 row scales."""
         self.w_gu = torch.empty(self.E_loc * 2 * self.I * self.H, dtype=wg.dtype, device=wg.device)
         self.w_d = torch.empty(self.E_loc * self.H * self.I, dtype=wg.dtype, device=wg.device)
+        N.after_current(stream, wg.get_device())  # whose memory they come from
         N.moe_pack_ffn_weights(wg, wu, wd, self.w_gu, self.w_d, self.w_dtype, stream=stream)
         N.keep_for(stream, wg.get_device(), (wg, wu, wd, self.w_gu, self.w_d))
         self.s_gate, self.s_up, self.s_down = s_gate, s_up, s_down

@@ -205,3 +205,14 @@ def test_rows_of_every_layout_that_the_calls_take(calls):
     one.run(wide, torch.zeros(T, E + 1)[:, 1:], torch.zeros(E, 2 * I, H + 8, dtype=torch.bfloat16)[..., :H],
             torch.zeros(E, 2 * H, I, dtype=torch.bfloat16)[:, H:], torch.zeros(T, H + 4)[:, 4:])
     one.run(torch.zeros(H, 1, dtype=torch.bfloat16).t(), logits[:1], w_gu, w_d, out[:1])  # one row has no pitch
+
+
+def test_packed_weights_are_not_written_before_the_current_stream_is_done_with_their_memory(calls, streams, monkeypatch):
+    monkeypatch.setattr(N, "moe_pack_ffn_weights", lambda *a, **k: calls.append("pack"))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    one = M.ExpertLayer(E, H, I, K, M.MOE_F32, M.MOE_F32, T, device="cpu")
+    w = torch.zeros(E, I, H), torch.zeros(E, I, H), torch.zeros(E, H, I)
+    one.load_weights(*w, stream=streams[1])
+    assert calls == ["77 waits for 5", "pack"]
+    one.load_weights(*w)
+    assert calls == ["77 waits for 5", "pack", "pack"]
