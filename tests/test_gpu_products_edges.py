@@ -137,3 +137,34 @@ def test_8_bit_products_with_a_large_column(rows, D, large):
     for odt in (BF16, F32):
         off = (product8(x.float(), w.float(), odt).double() - ref).abs() - HALF[odt] * ref.abs() - 2 * U * (D + 3) * size
         assert float((off - (7 * 2.0 ** -13 * size if odt == BF16 else 0)).max()) <= 0, odt
+
+
+@pytest.mark.parametrize("rows", [30, 200])
+def test_rows_gradient_through_weights_quantised_the_other_way(rows):
+    """moe_quantize_weights(transposed) gives the weights of the 8-bit product in the other direction.  Against fp64 of
+    the values that the codes stand for: a sum of N terms is off by 2 u (N + 3) of the sum of their sizes; and those
+    values against the weights: a code is off by half a step, 2^-4 of its value or 2^-10 of its scale."""
+    print("transposed codes", rows, flush=True)
+    E, N, D = 3, 272, 200
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    w = (torch.randn(E, N, D, generator=g, device="cuda") * 0.05).to(BF16)
+    codes, scale = torch.empty(E, D, N, dtype=FP8, device="cuda"), torch.empty(E, 2, 3, device="cuda")
+    M.moe_quantize_weights(w, codes, scale, transposed=True)
+    sizes = [rows, 0, rows // 3]
+    n = sum(sizes)
+    d8 = (torch.randn(n, N, generator=g, device="cuda") * 60).clamp(-448, 448).to(FP8)
+    ds = torch.rand(n, 3, generator=g, device="cuda") + 0.5
+    offsets = torch.tensor([0, *np.cumsum(sizes)], dtype=I32, device="cuda")
+    dx = torch.empty(n, D, device="cuda")
+    M.moe_expert_matmul(d8, codes, offsets, dx, x_scale=ds, w_scale=scale)
+    each = scale.double().repeat_interleave(128, 1)[:, :D].repeat_interleave(128, 2)[:, :, :N]
+    wv = codes.double() * each
+    w0 = w.double().transpose(1, 2)
+    assert float(((wv - w0).abs() - torch.maximum(2.0 ** -4 * w0.abs(), 2.0 ** -10 * each) * (1 + 16 * U)).max()) <= 0
+    dv = d8.double() * ds.double().repeat_interleave(128, 1)[:, :N]
+    at = 0
+    for e, s in enumerate(sizes):
+        r = dv[at:at + s]
+        off = (dx[at:at + s].double() - r @ wv[e].t()).abs() - (2 * U * (N + 3) * (r.abs() @ wv[e].abs().t()) + U * (r @ wv[e].t()).abs())
+        assert off.numel() == 0 or float(off.max()) <= 0, e
+        at += s
