@@ -216,3 +216,16 @@ def test_packed_weights_are_not_written_before_the_current_stream_is_done_with_t
     assert calls == ["77 waits for 5", "pack"]
     one.load_weights(*w)
     assert calls == ["77 waits for 5", "pack", "pack"]
+
+
+def test_rows_far_apart(calls):
+    """A product takes rows at most 16 MiB apart; a training run multiplies a copy of x and takes any."""
+    one = layer()
+    x, logits, w_gu, w_d, out = inputs()
+    far = torch.empty(2 * (1 << 22) + 64).as_strided((2, H), ((1 << 22) + 8, 1))
+    one.run(far, logits[:2], w_gu, w_d, out[:2], train=True)
+    one.backward(out[:2], far, logits[:2], w_gu, w_d)
+    del calls[:]
+    with pytest.raises(M.MoeError, match="too far apart"):
+        one.run(far, logits[:2], w_gu, w_d, out[:2])
+    assert not calls
